@@ -368,6 +368,200 @@ int sv_accept_rejection_noalloc(const float *logits, int64_t V, const float *q, 
                                 void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Key-value cache.                                                    */
+/* ------------------------------------------------------------------ */
+/* The attention history that a pass's q, k and v projections read and
+ * extend: a pool of pages on the device, one page table row per sequence,
+ * and the operators on them.  Nothing is decided on the host: lengths, page
+ * tables, free pages and accepted counts stay on the device, so a whole
+ * cycle (reserve, projections, append, attention, acceptance, commit) runs
+ * without a host round trip and can be captured in a graph.
+ *
+ * Positions.  A sequence holds len committed positions in slots 0..len-1
+ * (slot s lies in page table[seq][s / page]).  The M new rows of a round
+ * (the current token and the drafts) go to slots len..len+M-1; they become
+ * part of the sequence when sv_kv_commit keeps them.  Row m of a round sees
+ * the committed slots and, of the new rows, those whose bit is set in its
+ * tree mask (bit t = row t; without masks the rows 0..m).  Its position is
+ * len plus the number of rows before it that it sees, so a row of a draft
+ * tree has the position it will hold if its path is kept.
+ *
+ * Layout of the pool: [layers][n_pages] pages; a page is [heads][page / 32]
+ * blocks, each 32 slots of one head: keys [dim/8][32][8], then values
+ * [4][dim][8] (eight slots innermost), so the operand of every matrix
+ * instruction of the attention is one contiguous piece of a block.  An
+ * SV_KV_I8 block holds int8 codes and then the rows' fp32 scales, 32 of the
+ * keys and 32 of the values: value = code * scale.
+ *
+ * Calls on one cache must be ordered (one stream, or events between
+ * streams), except that attention and read calls of the same state may
+ * overlap each other.  A problem that only the device can see sets bits of
+ * ctl[1] (sv_kv_status), and the call leaves alone what it names. */
+#define SV_KV_F16 1   /* fp16, round to nearest even */
+#define SV_KV_BF16 30 /* bf16, round to nearest even */
+#define SV_KV_I8 24   /* int8 codes, one fp32 scale per slot and head: d = amax / 127, codes
+                         as sv_quantize_act_q8 rounds them; a row whose d is below 2^-126
+                         is stored as zeros, one that holds an infinity or NaN as d = NaN */
+
+#define SV_KV_MAX_SEQS 4096
+
+typedef struct {
+    int32_t type;     /* SV_KV_* */
+    int32_t layers;
+    int32_t heads;    /* key / value heads */
+    int32_t dim;      /* head dimension: a multiple of 32, at most 256 */
+    int32_t page;     /* slots per page: 32, 64, 128 or 256 */
+    int32_t n_pages;
+    int32_t seqs;     /* rows of the page table, at most SV_KV_MAX_SEQS */
+    int32_t width;    /* page table entries per sequence; seqs * width < 2^31 */
+    void *data;       /* sv_kv_data_bytes bytes, 256-byte aligned */
+    int32_t *table;   /* [seqs][width] page ids, -1 = none; the valid entries of a row come first */
+    int32_t *len;     /* [seqs] committed positions */
+    int32_t *refs;    /* [n_pages] sequences holding the page */
+    int32_t *free_ids; /* [n_pages] free pages, taken from the end */
+    int32_t *ctl;     /* [4]: number of free pages, status bits, result of the last fork or
+                         compaction (pairs granted / pages moved), 0 */
+} sv_kv;
+
+/* Status bits in ctl[1]; they stay set until sv_kv_status clears them. */
+#define SV_KV_NO_PAGES 1   /* reserve / fork: too few free pages; the call did nothing */
+#define SV_KV_TOO_LONG 2   /* reserve: more slots than a table row holds; the call did nothing */
+#define SV_KV_BAD_FORK 4   /* fork: a pair that is not allowed; the call did nothing */
+#define SV_KV_NO_SLOT 8    /* append: a row's slot has no page; the row was dropped */
+#define SV_KV_BAD_COMMIT 16 /* commit: a count or path out of range; that sequence was left as it was */
+#define SV_KV_OVER_MAX 32  /* attention: a sequence longer than max_len; its rows are NaN */
+
+/* The sequences and new rows of a call.  An index outside [0, seqs) has no
+ * rows.  Where a call writes, a sequence named twice counts once (its first
+ * place in the list). */
+typedef struct {
+    int32_t B;             /* sequences of this call, 1..4096 */
+    int32_t M;             /* rows per sequence in the row-major buffers */
+    const int32_t *seq;    /* [B] table rows, or NULL: 0..B-1 */
+    const int32_t *n_new;  /* [B] rows in use (clamped to 0..M), or NULL: M.  Buffers of rows
+                              past it are neither read nor written */
+    const uint32_t *tree;  /* [B][M] masks (M <= 32), or NULL: row m sees rows 0..m */
+} sv_kv_batch;
+
+/* Rotary position embedding, applied in fp32 (each product and each sum
+ * rounded): (x0, x1) -> (x0 c - x1 s, x1 c + x0 s) with (c, s) =
+ * table[position][pair]. */
+#define SV_ROPE_NONE 0
+#define SV_ROPE_PAIRS 1  /* pair i = elements 2i, 2i + 1 */
+#define SV_ROPE_HALVES 2 /* pair i = elements i, i + rot / 2 */
+typedef struct {
+    int32_t mode;       /* SV_ROPE_* */
+    int32_t rot;        /* elements rotated, the first of a head: even, at most dim */
+    int32_t n_pos;      /* rows of table, at least width * page */
+    const float *table; /* [n_pos][rot / 2][2] cos, sin; 8-byte aligned */
+} sv_kv_rope;
+
+/* Bytes of one page / of the pool, or 0 for an unsupported cache. */
+size_t sv_kv_page_bytes(int32_t type, int32_t heads, int32_t dim, int32_t page);
+size_t sv_kv_data_bytes(const sv_kv *kv);
+
+/* Empties the cache: every page free (page 0 is taken first), no entry in
+ * any table row, lengths and status 0.  The pool is not touched. */
+int sv_kv_init(const sv_kv *kv, void *stream);
+
+/* Gives each sequence of the batch the pages of slots len..len+n-1 that its
+ * table row lacks (n = n_new, or M), in the order of the batch.  Either
+ * every sequence gets its pages or none does (SV_KV_NO_PAGES,
+ * SV_KV_TOO_LONG).  tree is not read. */
+int sv_kv_reserve(const sv_kv *kv, const sv_kv_batch *batch, void *stream);
+
+/* Writes the new rows of one layer: k (rotated for its row's position when
+ * rope is given) and v, fp32 [B][M][heads][dim] as sv_verify_matvec writes
+ * them, rounded to the cache's type.  M may be as long as a prompt; then
+ * tree must be NULL. */
+int sv_kv_append(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const float *k, const float *v,
+                 const sv_kv_rope *rope, void *stream);
+
+/* Reads M slots of one layer of each sequence as fp32 [B][M][heads][dim]
+ * (k_out, v_out; either may be NULL), from slot start[b] on (NULL: from len
+ * on, the new rows).  Slots without a page, and those before 0, read as 0. */
+int sv_kv_read(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const int32_t *start, float *k_out,
+               float *v_out, void *stream);
+
+/* Ends a round: sequence b keeps accepted[b * stride] + 1 of its rows
+ * (accepted is out[0] of sv_accept_greedy / sv_accept_rejection, so stride
+ * is the length of one such output, or 1).  path [B][M], or NULL: the rows
+ * kept, strictly ascending (a root-to-leaf path of the tree; row path[i]
+ * moves to slot len + i in every layer); NULL keeps rows 0, 1, ...  len
+ * grows by the number kept, and the pages past it are freed.  A sequence
+ * whose accepted is negative (a round that failed) keeps its len and gives
+ * its spare pages back; one whose count exceeds its rows, or whose path is
+ * not as above, is left as it was (SV_KV_BAD_COMMIT). tree is not read. */
+int sv_kv_commit(const sv_kv *kv, const sv_kv_batch *batch, const int32_t *accepted, int32_t stride,
+                 const int32_t *path, void *stream);
+
+/* Sequence dst[i] becomes a copy of sequence src[i], for n pairs: it shares
+ * the pages that src has filled and gets a copy of the part-filled one
+ * (every layer), so neither sees what the other appends.  dst must be
+ * empty (never used, or released), the dst distinct and none of them a src:
+ * otherwise, or if pages are short, the call does nothing and says so
+ * (SV_KV_BAD_FORK, SV_KV_NO_PAGES).  Rows of src that are not committed are
+ * not part of the copy. */
+int sv_kv_fork(const sv_kv *kv, const int32_t *src, const int32_t *dst, int32_t n, void *stream);
+
+/* Drops sequences: their pages lose a holder each, a page without holders
+ * becomes free, and len is 0.  Indices out of range are passed over. */
+int sv_kv_release(const sv_kv *kv, const int32_t *ids, int32_t n, void *stream);
+
+/* Moves the held pages with the highest ids to the free ones with the
+ * lowest (every layer) until all free pages lie above all held ones, and
+ * rewrites the table: afterwards the pool's upper part, from page n_pages -
+ * ctl[0] on, can be cut off or handed on. */
+size_t sv_kv_compact_workspace_bytes(const sv_kv *kv);
+int sv_kv_compact(const sv_kv *kv, void *workspace, size_t ws_bytes, void *stream);
+
+/* Host: the status bits set since the previous call (or since sv_kv_init);
+ * synchronises the device, then clears them. */
+int sv_kv_status(const sv_kv *kv, uint32_t *status);
+
+/* Attention of the new rows over the cache, after sv_kv_append has written
+ * them:  out[b][m][hq] = sum_j p_j v_j / sum_j p_j over the slots j that row
+ * m sees, p_j = exp(scale * q . k_j - max), with key / value head hq /
+ * (q_heads / heads); 0 if it sees none.  With window > 0 a row sees a slot
+ * only if its position lies less than `window` before the row's own, or is
+ * one of the first `sinks` positions.  Only visible slots count: what
+ * others hold, infinities and NaN too, changes nothing; a visible row that
+ * holds one makes the outputs that depend on it NaN or infinite.
+ *
+ * fp32 accuracy: q and the weights p enter the matrix instructions as two
+ * (fp16) or three (bf16) parts each, so their products are exact to about
+ * 2^-22, and all sums and softmax statistics are fp32.
+ *
+ * The length is cut into chunks (`chunk` slots; 0 = a rule of B, heads,
+ * max_len, window and sinks), each an independent softmax, joined in chunk
+ * order.  A row's result depends on its own q, position and visible slots
+ * and on the chunk length only: not on M, on the other rows and sequences,
+ * or on where pages lie, so a row of a round equals that row run alone bit
+ * for bit when both calls have the same chunk length. */
+typedef struct {
+    int32_t q_heads;        /* a multiple of heads, at most 64 times */
+    float scale;            /* > 0, usually 1 / sqrt(dim) */
+    int32_t window;         /* 0 = none */
+    int32_t sinks;          /* >= 0; only with a window */
+    int32_t max_len;        /* no sequence's len + new rows exceeds it (0: width * page); it sizes
+                               the launch and the workspace */
+    int32_t chunk;          /* 0, or a multiple of 128 */
+    const sv_kv_rope *rope; /* rotates q for its row's position, or NULL */
+} sv_kv_attn;
+
+/* 1 <= M <= SV_MAX_M.  q [B][M][q_heads][dim] fp32, 16-byte aligned.
+ * out [B][M][q_heads * dim] fp32 (16-byte aligned) or NULL.  ep, or NULL:
+ * mode SV_EP_QUANT, the next projection's input, bit for bit what
+ * sv_quantize_act_q8 makes of out: gamma [q_heads * dim] or NULL, and q, d,
+ * s16, sumsq of B * M rows.  At least one of out and ep.
+ * workspace: sv_kv_attention_workspace_bytes bytes, 256-byte aligned, not
+ * shared by calls that run concurrently; needs no initialisation.  May be
+ * NULL when the size is 0. */
+size_t sv_kv_attention_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn);
+int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const sv_kv_attn *attn, const float *q,
+                    float *out, const sv_epilogue *ep, void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Measurement aid (not a step of the pass).                           */
 /* ------------------------------------------------------------------ */
 /* Reads `bytes` (a multiple of 16) at src once with 16-byte streaming loads

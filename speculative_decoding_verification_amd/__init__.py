@@ -19,6 +19,9 @@ LIB_PATH = os.path.join(HERE, "libspecverify.so")
 SV_OK, SV_ERR_ARG, SV_ERR_SHAPE, SV_ERR_ALIGN, SV_ERR_QTYPE, SV_ERR_WORKSPACE, SV_ERR_HIP = 0, -1, -2, -3, -4, -5, -6
 SV_Q8_0, SV_Q4_K, SV_Q6_K = 8, 12, 14
 SV_EP_NONE, SV_EP_QUANT, SV_EP_PAIR = 0, 1, 2
+SV_KV_F16, SV_KV_BF16, SV_KV_I8 = 1, 30, 24
+SV_ROPE_NONE, SV_ROPE_PAIRS, SV_ROPE_HALVES = 0, 1, 2
+SV_KV_NO_PAGES, SV_KV_TOO_LONG, SV_KV_BAD_FORK, SV_KV_NO_SLOT, SV_KV_BAD_COMMIT, SV_KV_OVER_MAX = 1, 2, 4, 8, 16, 32
 MAX_M = 16
 
 EXPORTS = [
@@ -27,7 +30,10 @@ EXPORTS = [
     "sv_head_logits", "sv_argmax_index", "sv_pass_workspace_bytes", "sv_pass_schedule", "sv_pass_create",
     "sv_pass_run", "sv_pass_status", "sv_pass_trace", "sv_pass_destroy", "sv_accept_greedy",
     "sv_accept_workspace_bytes", "sv_accept_rejection", "sv_accept_noalloc_max_bytes",
-    "sv_accept_rejection_noalloc", "sv_read_bandwidth",
+    "sv_accept_rejection_noalloc", "sv_read_bandwidth", "sv_kv_page_bytes", "sv_kv_data_bytes", "sv_kv_init",
+    "sv_kv_reserve", "sv_kv_append", "sv_kv_read", "sv_kv_commit", "sv_kv_fork", "sv_kv_release",
+    "sv_kv_compact_workspace_bytes", "sv_kv_compact", "sv_kv_status", "sv_kv_attention_workspace_bytes",
+    "sv_kv_attention",
 ]
 
 
@@ -58,6 +64,27 @@ class Phase(ctypes.Structure):
     _fields_ = [("W", ctypes.POINTER(Weight)), ("n_w", ctypes.c_int32), ("A", Act),
                 ("y", ctypes.c_void_p * 3), ("ep", Epilogue), ("row_ids", ctypes.c_void_p),
                 ("n_rows", ctypes.c_int64), ("argmax", ctypes.c_void_p)]
+
+
+class Kv(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("type", "layers", "heads", "dim", "page", "n_pages", "seqs", "width")]
+                + [(n, ctypes.c_void_p) for n in ("data", "table", "len", "refs", "free_ids", "ctl")])
+
+
+class KvBatch(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("M", ctypes.c_int32), ("seq", ctypes.c_void_p), ("n_new", ctypes.c_void_p),
+                ("tree", ctypes.c_void_p)]
+
+
+class KvRope(ctypes.Structure):
+    _fields_ = [("mode", ctypes.c_int32), ("rot", ctypes.c_int32), ("n_pos", ctypes.c_int32),
+                ("table", ctypes.c_void_p)]
+
+
+class KvAttn(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("scale", ctypes.c_float), ("window", ctypes.c_int32),
+                ("sinks", ctypes.c_int32), ("max_len", ctypes.c_int32), ("chunk", ctypes.c_int32),
+                ("rope", ctypes.c_void_p)]
 
 
 _lib = None
@@ -109,6 +136,19 @@ def lib():
         L.sv_accept_noalloc_max_bytes.argtypes = []
         L.sv_accept_rejection_noalloc.argtypes = [P, i64, P, P, i32, P, ctypes.c_float, P, P]
         L.sv_read_bandwidth.argtypes = [P, ctypes.c_size_t, P, i32, P]
+        kv, bt, sz = ctypes.POINTER(Kv), ctypes.POINTER(KvBatch), ctypes.c_size_t
+        for f, res, args in (("sv_kv_page_bytes", sz, [i32, i32, i32, i32]), ("sv_kv_data_bytes", sz, [kv]),
+                             ("sv_kv_init", i32, [kv, P]), ("sv_kv_reserve", i32, [kv, bt, P]),
+                             ("sv_kv_append", i32, [kv, i32, bt, P, P, ctypes.POINTER(KvRope), P]),
+                             ("sv_kv_read", i32, [kv, i32, bt, P, P, P, P]),
+                             ("sv_kv_commit", i32, [kv, bt, P, i32, P, P]),
+                             ("sv_kv_fork", i32, [kv, P, P, i32, P]), ("sv_kv_release", i32, [kv, P, i32, P]),
+                             ("sv_kv_compact_workspace_bytes", sz, [kv]), ("sv_kv_compact", i32, [kv, P, sz, P]),
+                             ("sv_kv_status", i32, [kv, ctypes.POINTER(ctypes.c_uint32)]),
+                             ("sv_kv_attention_workspace_bytes", sz, [kv, bt, ctypes.POINTER(KvAttn)]),
+                             ("sv_kv_attention", i32, [kv, i32, bt, ctypes.POINTER(KvAttn), P, P,
+                                                       ctypes.POINTER(Epilogue), P, sz, P])):
+            getattr(L, f).restype, getattr(L, f).argtypes = res, args
         for f in ("sv_repack_weights", "sv_unpack_weights", "sv_quantize_act_q8", "sv_verify_matvec",
                   "sv_head_logits", "sv_accept_greedy", "sv_accept_rejection", "sv_accept_rejection_noalloc",
                   "sv_pass_create",
@@ -351,3 +391,6 @@ def read_bandwidth(src, sink, stream=None):
     sv_read_bandwidth); one workgroup per element of `sink` (uint32/int32)."""
     _check(lib().sv_read_bandwidth(_ptr(src), src.numel() * src.element_size(), _ptr(sink), sink.numel(),
                                    _stream(stream)))
+
+
+from .kv import KvCache, Rope, kv_page_bytes, rope_table  # noqa: E402,F401

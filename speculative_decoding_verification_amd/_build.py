@@ -3,8 +3,9 @@
 Every HIP source is compiled for gfx950 only, with fp contraction off (the
 fused multiply-adds the kernels want are written out explicitly) and packed
 fp32 instructions disabled.  matvec_inst.hip holds the projection and pass
-kernels for one number of positions and is compiled once per M (1..16), so
-the variants build in parallel.  Objects go to _build/; the shared library
+kernels for one number of positions and is compiled once per M (1..16), and
+kv_attn_inst.hip the cache attention of one cache type (three times), so the
+variants build in parallel.  Objects go to _build/; the shared library
 lands next to this file.
 """
 
@@ -33,13 +34,16 @@ FLAGS = [
 
 
 INST = os.path.join(CSRC, "matvec_inst.hip")
+KV_INST = os.path.join(CSRC, "kv_attn_inst.hip")
 MAX_M = 16
+KV_TYPES = (1, 30, 24)
 
 
 def sources():
     """(source, object name, extra defines) of every compile job."""
     jobs = [(s, os.path.basename(s) + ".o", []) for s in sorted(glob.glob(os.path.join(CSRC, "*.hip")))
-            if s != INST]
+            if s not in (INST, KV_INST)]
+    jobs = [(KV_INST, f"kv_attn_inst_t{t}.o", [f"-DSV_INST_KV={t}"]) for t in KV_TYPES] + jobs
     # The kernel keeps a ring of weight records in named registers filled by
     # one load path for every format.  LLVM's sinking of common instructions
     # out of the per-format address branches would merge stores to different

@@ -1,0 +1,187 @@
+// kv_attn.hip - host side of the cache's attention, and the join of the
+// chunks' partial softmaxes.
+#include "kv_attn.h"
+
+namespace sv {
+
+// The join of a row's chunks c: with M = max m_c,
+//   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c,
+// one workgroup a row; its threads split the head dimension and the chunks
+// (chunk number modulo the parts, each part in chunk order, then the parts in
+// order), so the sums do not depend on how many chunks a launch provides for.
+constexpr int kJoin = 256;
+__global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
+    __shared__ float s_v[kJoin], s_l[kJoin / 32], s_top[kJoin / 64];
+    const int r = blockIdx.x, head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
+    if (sid < 0 || sid >= a.kv.seqs) return;
+    const Span sp = span_of(a, b, sid);
+    if (r >= sp.n * a.group) return;
+    const int D = a.kv.dim, parts = kJoin / D;
+    const int n = min(a.chunks, sp.first + max(sp.end - sp.jump, 0));  // chunks in use
+    const int64_t base = (static_cast<int64_t>(b) * a.kv.heads + head) * a.chunks * a.rows + r;
+    float top = -INFINITY;
+    for (int c = tid; c < n; c += kJoin) top = fmaxf(top, gld(a.part_m + base + static_cast<int64_t>(c) * a.rows));
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
+    if ((tid & 63) == 0) s_top[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
+    const int part = tid / D, d = tid % D;
+    float v = 0.0f, l = 0.0f;
+    if (part < parts && top != -INFINITY) {
+        for (int c = 0; c < n; c++) {
+            if (chunk_of(sp, c) % parts != part) continue;
+            const int64_t at = base + static_cast<int64_t>(c) * a.rows;
+            const float w = __builtin_amdgcn_exp2f(gld(a.part_m + at) - top);
+            v += w * gld(a.part_o + at * D + d);
+            l += w * gld(a.part_l + at);
+        }
+    }
+    if (part < parts) {
+        s_v[part * D + d] = v;
+        if (d == 0) s_l[part] = l;
+    }
+    __syncthreads();
+    if (tid < D) {
+        float sum = s_l[0];
+        v = s_v[tid];
+        for (int i = 1; i < parts; i++) {
+            v += s_v[i * D + tid];
+            sum += s_l[i];
+        }
+        const bool over = a.max_len && sp.len + sp.n > a.max_len;
+        if (over && tid == 0) kv_flag(a.kv, SV_KV_OVER_MAX);
+        s_v[tid] = over ? NAN : v * (sum != 0.0f ? 1.0f / sum : 0.0f);
+    }
+    __syncthreads();
+    finish_rows(a, s_v, D, 1, [&](int) -> int64_t {
+        return (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + head * a.group + r % a.group;
+    });
+}
+
+// Slots of a chunk: enough chunks to give every compute unit several
+// workgroups at the longest length of the call, but no shorter than a block
+// for each wave, and no longer than makes the parts a small share of what is
+// read.
+static int chunk_rule(int64_t B, int64_t heads, int64_t span) {
+    int64_t c = (span * B * heads / 768 + 127) / 128 * 128;
+    if (c < 128) c = 128;
+    if (c > 4096) c = 4096;
+    return static_cast<int>(c);
+}
+
+struct Plan {
+    int64_t bound, units;
+    int rt;
+    size_t o_m, o_l, bytes;
+};
+
+static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, AttnArgs *a, Plan *p) {
+    SV_REQUIRE(at, SV_ERR_ARG, "kv_attention: NULL arguments");
+    SV_REQUIRE(at->q_heads >= 1 && at->q_heads % d.heads == 0 && at->q_heads / d.heads <= 64, SV_ERR_SHAPE,
+               "kv_attention: q_heads must be a multiple of heads, at most 64 times");
+    SV_REQUIRE(at->scale > 0.0f && at->scale <= 3.0e38f, SV_ERR_ARG, "kv_attention: scale must be positive and finite");
+    SV_REQUIRE(at->window >= 0 && at->sinks >= 0, SV_ERR_ARG, "kv_attention: window and sinks must not be negative");
+    SV_REQUIRE(at->window > 0 || at->sinks == 0, SV_ERR_ARG, "kv_attention: sinks need a window");
+    SV_REQUIRE(at->max_len >= 0, SV_ERR_ARG, "kv_attention: max_len must not be negative");
+    SV_REQUIRE(at->chunk >= 0 && at->chunk % 128 == 0 && at->chunk <= (1 << 24), SV_ERR_ARG,
+               "kv_attention: chunk must be a multiple of 128, at most 2^24");
+    const int rc = kv_check_rope(d, at->rope, "kv_attention");
+    if (rc) return rc;
+    const int64_t cap = static_cast<int64_t>(d.width) * d.page;
+    p->bound = at->max_len && at->max_len < cap ? at->max_len : cap;
+    const int64_t seen = static_cast<int64_t>(at->window) + at->sinks + SV_MAX_M;
+    const int64_t span = at->window && seen < p->bound ? seen : p->bound;
+    a->kv = d;
+    a->bt = *bt;
+    a->rope = at->rope ? *at->rope : sv_kv_rope{};
+    a->q_heads = at->q_heads;
+    a->group = at->q_heads / d.heads;
+    a->rows = bt->M * a->group;
+    a->window = at->window;
+    a->sinks = at->sinks;
+    a->max_len = at->max_len;
+    a->chunk = at->chunk ? at->chunk : chunk_rule(bt->B, d.heads, span);
+    int64_t chunks = (p->bound + a->chunk - 1) / a->chunk;
+    if (at->window) {
+        const int64_t most = (at->sinks + static_cast<int64_t>(a->chunk) - 1) / a->chunk +
+                             (static_cast<int64_t>(at->window) + SV_MAX_M + a->chunk - 1) / a->chunk + 1;
+        if (most < chunks) chunks = most;
+    }
+    a->chunks = static_cast<int32_t>(chunks);
+    a->scale = at->scale * 1.44269504088896340736f;
+    p->rt = attn_tiles_per_wave(d.dim, a->rows);
+    a->tiles = (a->rows + 16 * p->rt - 1) / (16 * p->rt);
+    p->units = (static_cast<int64_t>(bt->B) * d.heads * chunks + 7) / 8 * 8;
+    SV_REQUIRE(p->units * a->tiles < (1ll << 24), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
+    p->bytes = p->o_m = p->o_l = 0;
+    if (chunks > 1) {
+        const size_t parts = static_cast<size_t>(bt->B) * d.heads * chunks * a->rows;
+        p->o_m = (parts * d.dim * 4 + 255) / 256 * 256;
+        p->o_l = p->o_m + (parts * 4 + 255) / 256 * 256;
+        p->bytes = p->o_l + (parts * 4 + 255) / 256 * 256;
+    }
+    return SV_OK;
+}
+
+}  // namespace sv
+
+using namespace sv;
+
+extern "C" size_t sv_kv_attention_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn) {
+    KvDev d;
+    AttnArgs a{};
+    Plan p;
+    if (kv_check(kv, "kv_attention", &d) || kv_check_batch(d, batch, "kv_attention", SV_MAX_M) ||
+        plan_of(d, batch, attn, &a, &p))
+        return 0;
+    return p.bytes;
+}
+
+extern "C" int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const sv_kv_attn *attn,
+                               const float *q, float *out, const sv_epilogue *ep, void *workspace, size_t ws_bytes,
+                               void *stream) {
+    KvDev d;
+    AttnArgs a{};
+    Plan p;
+    int rc = kv_check(kv, "kv_attention", &d);
+    if (!rc) rc = kv_check_batch(d, batch, "kv_attention", SV_MAX_M);
+    if (!rc) rc = plan_of(d, batch, attn, &a, &p);
+    if (rc) return rc;
+    SV_REQUIRE(layer >= 0 && layer < d.layers, SV_ERR_ARG, "kv_attention: layer out of range");
+    const bool quant = ep && ep->mode != SV_EP_NONE;
+    SV_REQUIRE(q && (out || quant), SV_ERR_ARG, "kv_attention: NULL buffer");
+    SV_REQUIRE(aligned(q, 16) && (!out || aligned(out, 16)), SV_ERR_ALIGN,
+               "kv_attention: q and out must be 16-byte aligned");
+    if (quant) {
+        SV_REQUIRE(ep->mode == SV_EP_QUANT && ep->src == 0, SV_ERR_ARG,
+                   "kv_attention: the epilogue's mode must be SV_EP_QUANT and its src 0");
+        SV_REQUIRE(ep->q && ep->d && ep->s16 && ep->sumsq, SV_ERR_ARG, "kv_attention: NULL epilogue buffer");
+        SV_REQUIRE((!ep->gamma || aligned(ep->gamma, 4)) && aligned(ep->d, 4) && aligned(ep->s16, 4) &&
+                       aligned(ep->sumsq, 4),
+                   SV_ERR_ALIGN, "kv_attention: fp32/int32 buffers must be 4-byte aligned");
+        a.ep = *ep;
+    }
+    SV_REQUIRE(p.bytes == 0 || (workspace && ws_bytes >= p.bytes), SV_ERR_WORKSPACE,
+               "kv_attention: workspace needs " + std::to_string(p.bytes) + " bytes");
+    SV_REQUIRE(p.bytes == 0 || aligned(workspace, 256), SV_ERR_ALIGN,
+               "kv_attention: the workspace must be 256-byte aligned");
+    a.q = q;
+    a.out = out;
+    a.layer = layer;
+    if (p.bytes) {
+        uint8_t *ws = static_cast<uint8_t *>(workspace);
+        a.part_o = reinterpret_cast<float *>(ws);
+        a.part_m = reinterpret_cast<float *>(ws + p.o_m);
+        a.part_l = reinterpret_cast<float *>(ws + p.o_l);
+    }
+    hipStream_t st = as_stream(stream);
+    const dim3 grid(static_cast<unsigned>(p.units * a.tiles));
+    rc = d.type == SV_KV_F16    ? attn_launch_f16(a, p.rt, grid, st)
+         : d.type == SV_KV_BF16 ? attn_launch_bf16(a, p.rt, grid, st)
+                                : attn_launch_i8(a, p.rt, grid, st);
+    if (rc || a.chunks == 1) return rc;
+    hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(kJoin), 0, st, a);
+    return hip_check(hipGetLastError(), "kv_attention join launch");
+}
