@@ -626,14 +626,15 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_
             if (s >= lo && s < hi) {
                 for (int c = tid & 7; c < D; c += 8) {
                     const float y = fabsf(rows[s * ld + c]);
-                    fine = fine && y <= 3.4028234664e38f;
+                    fine &= y <= 3.4028234664e38f;
                     a = fmaxf(a, y);
                 }
             }
 #pragma unroll
             for (int o = 4; o >= 1; o >>= 1) {
                 a = fmaxf(a, __shfl_xor(a, o, 8));
-                fine = fine && __shfl_xor(static_cast<int>(fine), o, 8);
+                const int other = __shfl_xor(static_cast<int>(fine), o, 8);  // by every lane, whatever its own answer
+                fine &= other != 0;
             }
             if ((tid & 7) == 0 && s >= lo && s < hi) {
                 const float d = a / 127.0f;

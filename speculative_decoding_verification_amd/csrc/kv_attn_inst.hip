@@ -71,6 +71,20 @@ __device__ __forceinline__ void split8(const float (&x)[8], V8 (&part)[N]) {
         }
 }
 
+// w y as the products of w's parts make it, for a y that is not finite.
+template <int N, typename V8>
+__device__ __forceinline__ float times_parts(float w, float y) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; n++) {
+        V8 h;
+        h[0] = static_cast<decltype(h[0] + h[0])>(w);
+        w -= static_cast<float>(h[0]);
+        sum += static_cast<float>(h[0]) * y;
+    }
+    return sum;
+}
+
 // Raw piece of a block as one lane loads it.
 template <int ESZ>
 struct Raw {
@@ -292,6 +306,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
         uint32_t any_sees = 0xFFu, all_see = 0xFFu;
         if (edge) any_sees = 0u;
         float p[RT][8];
+        uint32_t seen[RT];  // slots of the lane group that the lane's row sees
 #pragma unroll
         for (int t = 0; t < RT; t++) {
             f4 acc[2];
@@ -308,6 +323,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
                 p[t][e] = acc[e >> 2][e & 3] * rs[t];
                 if constexpr (TYPE == SV_KV_I8) p[t][e] *= ks[e];
             }
+            seen[t] = 0xFFu;
             if (edge) {
                 const bool live = row0 + 16 * t + col < rows;
 #pragma unroll
@@ -320,7 +336,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
                         const int64_t kpos = nth < 0 ? slot : sp.len + row_depth(a, b, nth);
                         sees = pos[t] - kpos < a.window || kpos < a.sinks;
                     }
-                    if (!sees) p[t][e] = -INFINITY;
+                    if (!sees) {
+                        p[t][e] = -INFINITY;
+                        seen[t] &= ~(1u << e);
+                    }
                     const uint32_t by = static_cast<uint32_t>(__ballot(live && sees) >> (16 * g)) & 0xFFFFu;
                     const uint32_t of = static_cast<uint32_t>(__ballot(live) >> (16 * g)) & 0xFFFFu;
                     if (by) any_sees |= 1u << e;
@@ -399,7 +418,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
             if (odd) {
                 for (int gg = 0; gg < 4; gg++) {
 #pragma unroll
-                    for (int t = 0; t < RT; t++)
+                    for (int t = 0; t < RT; t++) {
+                        const uint32_t sees = __shfl(seen[t], 16 * gg + col, 64);
 #pragma unroll
                         for (int e = 0; e < 8; e++) {
                             const float w = __shfl(p[t][e], 16 * gg + col, 64);
@@ -409,10 +429,12 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
 #pragma unroll
                                 for (int k = 0; k < 4; k++) {
                                     const uint32_t h = gld(reinterpret_cast<const uint16_t *>(v) + (16 * i + k) * 8);
-                                    if (odd_pair<TYPE>(h) && w != 0.0f)
-                                        o[t][i][k] += w * (TYPE == SV_KV_F16 ? half_bits_to_float(h) : __uint_as_float(h << 16));
+                                    if (!odd_pair<TYPE>(h) || !(sees >> e & 1u)) continue;
+                                    const float y = TYPE == SV_KV_F16 ? half_bits_to_float(h) : __uint_as_float(h << 16);
+                                    o[t][i][k] += times_parts<Kd::kp, typename Kd::VVec>(w, y);
                                 }
                         }
+                    }
                 }
             }
         }

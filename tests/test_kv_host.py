@@ -1,0 +1,207 @@
+"""Host-side tests of the key-value cache's C ABI (no GPU needed): sizes, and
+the refusal of invalid arguments before any launch."""
+
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import kv_model as km
+import speculative_decoding_verification_amd as sv
+
+pytestmark = pytest.mark.skipif(not os.path.exists(sv.LIB_PATH), reason="libspecverify.so not built")
+
+FAKE = 1 << 20  # never dereferenced: validation fails first
+F = ctypes.c_void_p(FAKE)
+
+
+def cache(**kw):
+    d = dict(type=sv.SV_KV_F16, layers=2, heads=8, dim=128, page=64, n_pages=100, seqs=4, width=16, data=FAKE,
+             table=FAKE, len=FAKE, refs=FAKE, free_ids=FAKE, ctl=FAKE)
+    d.update(kw)
+    return sv.Kv(*[d[n] for n, _ in sv.Kv._fields_])
+
+
+def batch(B=2, M=5, seq=FAKE, n_new=None, tree=None):
+    return sv.KvBatch(B, M, seq, n_new, tree)
+
+
+def refused(rc, code):
+    assert rc == code, (rc, sv.lib().sv_last_error())
+    assert sv.lib().sv_last_error()
+
+
+@pytest.mark.parametrize("kind,heads,dim,page,want", [
+    (1, 8, 128, 64, 8 * 2 * 32 * 128 * 4), (30, 1, 32, 32, 32 * 32 * 4), (24, 3, 96, 256, 3 * 8 * (64 * 96 + 256)),
+    (2, 8, 128, 64, 0), (1, 8, 120, 64, 0), (1, 8, 288, 64, 0), (1, 8, 0, 64, 0), (1, 0, 128, 64, 0),
+    (1, 8, 128, 48, 0), (1, 8, 128, 512, 0)])
+def test_sizes(kind, heads, dim, page, want):
+    assert sv.kv_page_bytes(kind, heads, dim, page) == want
+    kv = cache(type=kind, heads=heads, dim=dim, page=page)
+    assert sv.lib().sv_kv_data_bytes(ctypes.byref(kv)) == 200 * want
+    assert sv.lib().sv_kv_compact_workspace_bytes(ctypes.byref(kv)) == 1200
+
+
+BAD_CACHES = [
+    (dict(type=8), sv.SV_ERR_QTYPE), (dict(dim=100), sv.SV_ERR_SHAPE), (dict(dim=288), sv.SV_ERR_SHAPE),
+    (dict(page=16), sv.SV_ERR_SHAPE), (dict(heads=0), sv.SV_ERR_SHAPE), (dict(layers=0), sv.SV_ERR_SHAPE),
+    (dict(layers=4096, heads=4096), sv.SV_ERR_SHAPE), (dict(n_pages=0), sv.SV_ERR_SHAPE),
+    (dict(n_pages=(1 << 24) + 1), sv.SV_ERR_SHAPE), (dict(seqs=0), sv.SV_ERR_SHAPE), (dict(seqs=4097), sv.SV_ERR_SHAPE),
+    (dict(width=0), sv.SV_ERR_SHAPE), (dict(seqs=4096, width=1 << 20), sv.SV_ERR_SHAPE),
+    (dict(width=1 << 25), sv.SV_ERR_SHAPE), (dict(data=None), sv.SV_ERR_ARG), (dict(table=None), sv.SV_ERR_ARG),
+    (dict(ctl=None), sv.SV_ERR_ARG), (dict(data=FAKE + 128), sv.SV_ERR_ALIGN), (dict(len=FAKE + 2), sv.SV_ERR_ALIGN)]
+
+
+@pytest.mark.parametrize("change,code", BAD_CACHES)
+def test_every_call_checks_the_cache(change, code):
+    L, kv, b = sv.lib(), cache(**change), batch()
+    a = sv.KvAttn(40, 0.1, 0, 0, 0, 0, None)
+    r = ctypes.byref
+    refused(L.sv_kv_init(r(kv), None), code)
+    refused(L.sv_kv_reserve(r(kv), r(b), None), code)
+    refused(L.sv_kv_append(r(kv), 0, r(b), F, F, None, None), code)
+    refused(L.sv_kv_read(r(kv), 0, r(b), None, F, F, None), code)
+    refused(L.sv_kv_commit(r(kv), r(b), F, 1, None, None), code)
+    refused(L.sv_kv_fork(r(kv), F, F, 1, None), code)
+    refused(L.sv_kv_release(r(kv), F, 1, None), code)
+    refused(L.sv_kv_compact(r(kv), F, 1 << 30, None), code)
+    refused(L.sv_kv_attention(r(kv), 0, r(b), r(a), F, F, None, F, 1 << 40, None), code)
+    assert L.sv_kv_attention_workspace_bytes(r(kv), r(b), r(a)) == 0
+    refused(L.sv_kv_status(r(kv), r(ctypes.c_uint32())), code)
+    refused(L.sv_kv_init(None, None), sv.SV_ERR_ARG)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(B=0), sv.SV_ERR_ARG), (dict(B=4097), sv.SV_ERR_ARG), (dict(B=5, seq=None), sv.SV_ERR_ARG),
+    (dict(M=0), sv.SV_ERR_ARG), (dict(M=(1 << 24) + 1), sv.SV_ERR_ARG), (dict(seq=FAKE + 1), sv.SV_ERR_ALIGN),
+    (dict(n_new=FAKE + 2), sv.SV_ERR_ALIGN)])
+def test_batches(change, code):
+    L, kv, b, r = sv.lib(), cache(), batch(**change), ctypes.byref
+    a = sv.KvAttn(40, 0.1, 0, 0, 0, 0, None)
+    refused(L.sv_kv_reserve(r(kv), r(b), None), code)
+    refused(L.sv_kv_append(r(kv), 0, r(b), F, F, None, None), code)
+    refused(L.sv_kv_read(r(kv), 0, r(b), None, F, F, None), code)
+    refused(L.sv_kv_commit(r(kv), r(b), F, 1, None, None), code)
+    refused(L.sv_kv_attention(r(kv), 0, r(b), r(a), F, F, None, F, 1 << 40, None), code)
+    refused(L.sv_kv_reserve(r(kv), None, None), sv.SV_ERR_ARG)
+
+
+def test_rows_and_paths():
+    L, kv, r = sv.lib(), cache(), ctypes.byref
+    b = batch(M=33, tree=FAKE)
+    refused(L.sv_kv_append(r(kv), 0, r(b), F, F, None, None), sv.SV_ERR_ARG)         # trees: M <= 32
+    b = batch(tree=FAKE + 2)
+    refused(L.sv_kv_append(r(kv), 0, r(b), F, F, None, None), sv.SV_ERR_ALIGN)
+    b = batch()
+    refused(L.sv_kv_append(r(kv), 2, r(b), F, F, None, None), sv.SV_ERR_ARG)         # layer
+    refused(L.sv_kv_append(r(kv), -1, r(b), F, F, None, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_append(r(kv), 0, r(b), None, F, None, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_append(r(kv), 0, r(b), F, ctypes.c_void_p(FAKE + 4), None, None), sv.SV_ERR_ALIGN)
+    big = batch(M=1 << 24)
+    refused(L.sv_kv_append(r(cache(heads=64)), 0, r(big), F, F, None, None), sv.SV_ERR_SHAPE)
+    refused(L.sv_kv_read(r(kv), 0, r(b), None, None, None, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_read(r(kv), 2, r(b), None, F, F, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_read(r(kv), 0, r(b), ctypes.c_void_p(FAKE + 1), F, F, None), sv.SV_ERR_ALIGN)
+    refused(L.sv_kv_commit(r(kv), r(b), None, 1, None, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_commit(r(kv), r(b), F, 0, None, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_commit(r(kv), r(batch(M=33)), F, 1, F, None), sv.SV_ERR_ARG)     # a path: M <= 32
+    refused(L.sv_kv_commit(r(kv), r(b), F, 1, ctypes.c_void_p(FAKE + 2), None), sv.SV_ERR_ALIGN)
+    for n in (0, 4097):
+        refused(L.sv_kv_fork(r(kv), F, F, n, None), sv.SV_ERR_ARG)
+        refused(L.sv_kv_release(r(kv), F, n, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_fork(r(kv), None, F, 1, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_release(r(kv), None, 1, None), sv.SV_ERR_ARG)
+    refused(L.sv_kv_release(r(cache(width=1 << 20)), F, 4096, None), sv.SV_ERR_SHAPE)
+    refused(L.sv_kv_compact(r(kv), F, 1199, None), sv.SV_ERR_WORKSPACE)
+    refused(L.sv_kv_compact(r(kv), None, 1200, None), sv.SV_ERR_WORKSPACE)
+    refused(L.sv_kv_status(r(kv), None), sv.SV_ERR_ARG)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(mode=3), sv.SV_ERR_ARG), (dict(rot=3), sv.SV_ERR_SHAPE), (dict(rot=0), sv.SV_ERR_SHAPE),
+    (dict(rot=130), sv.SV_ERR_SHAPE), (dict(n_pos=1023), sv.SV_ERR_SHAPE), (dict(table=None), sv.SV_ERR_ARG),
+    (dict(table=FAKE + 4), sv.SV_ERR_ALIGN)])
+def test_ropes(change, code):
+    d = dict(mode=2, rot=128, n_pos=1024, table=FAKE)
+    d.update(change)
+    rope = sv.KvRope(d["mode"], d["rot"], d["n_pos"], d["table"])
+    L, kv, b, r = sv.lib(), cache(), batch(), ctypes.byref
+    refused(L.sv_kv_append(r(kv), 0, r(b), F, F, r(rope), None), code)
+    a = sv.KvAttn(40, 0.1, 0, 0, 0, 0, ctypes.addressof(rope))
+    refused(L.sv_kv_attention(r(kv), 0, r(b), r(a), F, F, None, F, 1 << 40, None), code)
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(q_heads=12), sv.SV_ERR_SHAPE), (dict(q_heads=0), sv.SV_ERR_SHAPE), (dict(q_heads=520), sv.SV_ERR_SHAPE),
+    (dict(scale=0.0), sv.SV_ERR_ARG), (dict(scale=-1.0), sv.SV_ERR_ARG), (dict(scale=float("inf")), sv.SV_ERR_ARG),
+    (dict(scale=float("nan")), sv.SV_ERR_ARG), (dict(window=-1), sv.SV_ERR_ARG), (dict(sinks=-1), sv.SV_ERR_ARG),
+    (dict(sinks=4), sv.SV_ERR_ARG), (dict(max_len=-1), sv.SV_ERR_ARG), (dict(chunk=64), sv.SV_ERR_ARG),
+    (dict(chunk=-128), sv.SV_ERR_ARG)])
+def test_attention_arguments(change, code):
+    d = dict(q_heads=40, scale=0.1, window=0, sinks=0, max_len=0, chunk=0)
+    d.update(change)
+    a = sv.KvAttn(*d.values(), None)
+    L, kv, b, r = sv.lib(), cache(), batch(), ctypes.byref
+    refused(L.sv_kv_attention(r(kv), 0, r(b), r(a), F, F, None, F, 1 << 40, None), code)
+    assert L.sv_kv_attention_workspace_bytes(r(kv), r(b), r(a)) == 0
+
+
+def test_attention_buffers():
+    L, kv, b, r = sv.lib(), cache(), batch(), ctypes.byref
+    a = sv.KvAttn(40, 0.1, 0, 0, 0, 128, None)
+    need = L.sv_kv_attention_workspace_bytes(r(kv), r(b), r(a))
+    # 8 chunks of 128 slots: 2 sequences x 8 heads x 8 chunks x 25 rows, dim sums and two numbers each
+    rows = 2 * 8 * 8 * 25
+    assert need >= rows * (128 + 2) * 4 and need < rows * 130 * 4 + 768
+
+    def call(layer=0, batch_=b, q=F, out=F, ep=None, ws=F, n=need):
+        return L.sv_kv_attention(r(kv), layer, r(batch_), r(a), q, out, None if ep is None else r(ep), ws, n, None)
+
+    refused(call(n=need - 1), sv.SV_ERR_WORKSPACE)
+    refused(call(ws=None), sv.SV_ERR_WORKSPACE)
+    refused(call(ws=ctypes.c_void_p(FAKE + 128)), sv.SV_ERR_ALIGN)
+    refused(call(layer=2), sv.SV_ERR_ARG)
+    refused(call(q=None), sv.SV_ERR_ARG)
+    refused(call(out=None), sv.SV_ERR_ARG)
+    refused(call(q=ctypes.c_void_p(FAKE + 4)), sv.SV_ERR_ALIGN)
+    refused(call(out=ctypes.c_void_p(FAKE + 8)), sv.SV_ERR_ALIGN)
+    refused(call(batch_=batch(M=17)), sv.SV_ERR_ARG)
+    ep = sv.Epilogue(sv.SV_EP_PAIR, 0, None, FAKE, FAKE, FAKE, FAKE)
+    refused(call(ep=ep), sv.SV_ERR_ARG)
+    ep = sv.Epilogue(sv.SV_EP_QUANT, 1, None, FAKE, FAKE, FAKE, FAKE)
+    refused(call(ep=ep), sv.SV_ERR_ARG)
+    ep = sv.Epilogue(sv.SV_EP_QUANT, 0, None, FAKE, FAKE, None, FAKE)
+    refused(call(ep=ep), sv.SV_ERR_ARG)
+    ep = sv.Epilogue(sv.SV_EP_QUANT, 0, FAKE + 2, FAKE, FAKE, FAKE, FAKE)
+    refused(call(ep=ep), sv.SV_ERR_ALIGN)
+    # a length that fits one chunk needs no workspace
+    one = sv.KvAttn(40, 0.1, 0, 0, 128, 128, None)
+    assert L.sv_kv_attention_workspace_bytes(r(kv), r(b), r(one)) == 0
+    # a window bounds the chunks whatever the length
+    far = cache(width=1 << 14)
+    win = sv.KvAttn(40, 0.1, 1000, 4, 0, 128, None)
+    assert 0 < L.sv_kv_attention_workspace_bytes(r(far), r(b), r(win)) <= 2 * 8 * 11 * 25 * 130 * 4 + 768
+    # too many chunks for one launch
+    huge = cache(width=1 << 24, seqs=1, n_pages=1 << 24)
+    many = sv.KvAttn(40, 0.1, 0, 0, 0, 128, None)
+    refused(L.sv_kv_attention(r(huge), 0, r(batch(B=1)), r(many), F, F, None, F, 1 << 50, None), sv.SV_ERR_SHAPE)
+
+
+def test_model_rounding():
+    """The model's own roundings, on values worked out by hand."""
+    assert km.bf16(np.float32([1.0, 1 + 2.0 ** -8, 1 + 3 * 2.0 ** -8, -3.0])).tolist() == [1.0, 1.0, 1 + 2.0 ** -6, -3.0]
+    x = np.zeros((1, 32), np.float32)
+    x[0, :4] = 127, 2.5, -2.5, 0.4
+    assert km.stored(x, km.I8)[0, :4].tolist() == [127, 3, -3, 0]
+    x[0, 5] = np.inf
+    assert np.isnan(km.stored(x, km.I8)).all()
+    assert (km.stored(np.full((1, 32), 1e-38, np.float32), km.I8) == 0).all()
+    # one slot: the output is its value; two equal keys: the mean
+    q = np.ones((1, 1, 32), np.float32)
+    k = np.ones((2, 1, 32), np.float32)
+    v = np.stack([np.zeros((1, 32)), np.ones((1, 32))]).astype(np.float32)
+    assert np.allclose(km.attention(q, k, v, 1, 1, 0.5)[0], 0.5)
+    assert np.allclose(km.attention(q, k, v, 1, 1, 0.5, window=1)[0], 1.0)
+    assert np.allclose(km.attention(q, k, v, 1, 1, 0.5, window=1, sinks=1)[0], 0.5)
+    assert np.allclose(km.attention(q, k, v, 1, 1, 0.5, masks=[0])[0], 0.0)
