@@ -20,6 +20,12 @@ history the single-key attention of each position returns its own v, so o
 reads v; q and k are computed and written but have no consumer.  There are
 no residual adds.  The whole pass can be captured once in a HIP graph (the
 calls are stream-ordered and allocate nothing) and replayed per cycle.
+
+With an AttnShape the stack keeps that history: each layer appends its rows'
+k and v to a paged key-value cache and attends over it, and the attention's
+epilogue requantises o's input (b = Q8A32(attention * g2)).  The cycle then
+also reserves the rows' pages and, after acceptance, commits the rows that
+were kept, so consecutive cycles continue one sequence on the device.
 """
 
 from __future__ import annotations
@@ -32,7 +38,24 @@ from concurrent.futures import ThreadPoolExecutor
 import numpy as np
 
 from . import (SV_EP_PAIR, SV_EP_QUANT, SV_Q4_K, SV_Q6_K, SV_Q8_0, Pass, accept_greedy, act, epilogue,
-               gguf_bytes, head_logits, phase, quantize_act_q8, repack_weights, repacked_bytes, verify_matvec, weight)
+               gguf_bytes, head_logits, phase, quantize_act_q8, repack_weights, repacked_bytes, verify_matvec, weight,
+               SV_KV_F16, SV_ROPE_HALVES, SV_ROPE_NONE, KvCache, Rope, rope_table)
+
+
+@dataclass
+class AttnShape:
+    """Attention of a stack: heads of `dim` elements, `kv_heads` of them
+    with keys and values, a cache of `max_len` positions."""
+    heads: int
+    kv_heads: int
+    dim: int
+    max_len: int
+    kv_type: int = SV_KV_F16
+    page: int = 64
+    window: int = 0
+    sinks: int = 0
+    rope_mode: int = SV_ROPE_HALVES
+    rope_base: float = 10000.0
 
 
 @dataclass
@@ -46,11 +69,19 @@ class StackShape:
     gate_up_q: int = SV_Q4_K
     down_q: int = SV_Q6_K
     head_q: int = SV_Q6_K
+    attn: AttnShape | None = None   # None: no attention history
+
+    def attn_rows(self):
+        """Outputs of q, and of k and v."""
+        if self.attn is None:
+            return self.hidden, self.hidden
+        return self.attn.heads * self.attn.dim, self.attn.kv_heads * self.attn.dim
 
     def layer_mats(self):
         H, F = self.hidden, self.ffn
-        return [("q", self.attn_q, H, H), ("k", self.attn_q, H, H), ("v", self.v_q, H, H),
-                ("o", self.attn_q, H, H), ("gate", self.gate_up_q, F, H), ("up", self.gate_up_q, F, H),
+        Q, KV = self.attn_rows()
+        return [("q", self.attn_q, Q, H), ("k", self.attn_q, KV, H), ("v", self.v_q, KV, H),
+                ("o", self.attn_q, H, Q), ("gate", self.gate_up_q, F, H), ("up", self.gate_up_q, F, H),
                 ("down", self.down_q, H, F)]
 
     def layer_bytes(self) -> int:
@@ -137,7 +168,7 @@ class VerifyStack:
                     raw = fut.result()
                     lw.mats[name] = upload_gguf(qt, raw, r, c, staging)
                     del raw
-                for g, n in (("g1", H), ("g2", H), ("g3", H), ("g4", F)):
+                for g, n in (("g1", H), ("g2", shape.attn_rows()[0]), ("g3", H), ("g4", F)):
                     lw.gammas[g] = t.from_numpy(weights_fn(layer, "gamma:" + g, None, n, 0)).cuda()
                 self.layers.append(lw)
                 pending = nxt
@@ -155,7 +186,8 @@ class VerifyStack:
         # reader's cache can hold a stale copy of it.
         self.acts = []
         for _ in range(shape.layers):
-            self.acts.append({"in": _Act(M, H), "v": _Act(M, H), "o": _Act(M, H), "h": _Act(M, F)})
+            self.acts.append({"in": _Act(M, H), "v": _Act(M, shape.attn_rows()[0]), "o": _Act(M, H),
+                              "h": _Act(M, F)})
         self.a_final = _Act(M, H)
         self.a_in = self.acts[0]["in"]
         # Each layer writes its q, k and v outputs to buffers of its own: a
@@ -163,13 +195,45 @@ class VerifyStack:
         # layer's q/k units fill idle workgroups wherever the schedule finds
         # them, so a buffer shared by the layers could end with an earlier
         # layer's rows.  yq, yk and yv are the last layer's.
-        self.ys = [{n: t.empty((M, H), dtype=t.float32, device="cuda") for n in "qkv"}
+        rows = dict(zip("qkv", (shape.attn_rows()[0], shape.attn_rows()[1], shape.attn_rows()[1])))
+        self.ys = [{n: t.empty((M, rows[n]), dtype=t.float32, device="cuda") for n in "qkv"}
                    for _ in range(max(shape.layers, 1))]
         self.yq, self.yk, self.yv = self.ys[-1]["q"], self.ys[-1]["k"], self.ys[-1]["v"]
         self.logits = t.empty((M, shape.vocab or 1), dtype=t.float32, device="cuda")
         self.argmax = t.zeros((M,), dtype=t.int64, device="cuda")
         self.drafts = t.zeros((max(M - 1, 1),), dtype=t.int32, device="cuda")
         self.out = t.zeros((M + 1,), dtype=t.int32, device="cuda")
+        self.kv, self.rope, self._attns = None, None, {}
+        if shape.attn is not None:
+            a = shape.attn
+            width = -(-(a.max_len + M) // a.page)
+            self.kv = KvCache(a.kv_type, shape.layers, a.kv_heads, a.dim, a.page, width, 1, width)
+            if a.rope_mode != SV_ROPE_NONE:
+                self.rope = Rope(a.rope_mode, a.dim, rope_table(width * a.page, a.dim, a.rope_base))
+
+    # -------------------------------------------------------- attention
+    def attention(self, M: int):
+        """The attention plan of rounds of M rows (its workspace serves every
+        layer, one after the other)."""
+        if M not in self._attns:
+            a = self.shape.attn
+            self._attns[M] = self.kv.attention(a.heads, 1, M, window=a.window, sinks=a.sinks)
+        return self._attns[M]
+
+    def _attend(self, li: int, M: int, plan):
+        """Rows li's k and v into the cache, attention over it, o's input."""
+        a, y = self.shape.attn, self.ys[li]
+        act_v = self.acts[li]["v"]
+        self.kv.append(li, y["k"][:M].view(1, M, a.kv_heads, a.dim), y["v"][:M].view(1, M, a.kv_heads, a.dim),
+                       rope=self.rope)
+        plan.run(li, y["q"][:M].view(1, M, a.heads, a.dim), rope=self.rope,
+                 ep=act_v.ep(SV_EP_QUANT, self.layers[li].gammas["g2"]))
+
+    def _commit(self, M: int):
+        """Keeps the rows that acceptance kept (all of them without a head)."""
+        if self.head is None:
+            self.out[:1].fill_(M - 1)
+        self.kv.commit(M, self.out[:M + 1])
 
     # ----------------------------------------------------------- phases
     def _specs(self, M: int):
@@ -185,7 +249,15 @@ class VerifyStack:
             last = li + 1 == len(L)
             nxt = self.gamma_f if last else L[li + 1].gammas["g1"]
             out = self.a_final if last else self.acts[li + 1]["in"]
-            if self.shape.attn_q == self.shape.v_q:
+            if self.shape.attn is not None:
+                # q, k and v have no fused consumer: the attention reads them
+                specs.append(("q", [m["q"][0]], a["in"].desc(M, eps), [y["q"]], None))
+                if self.shape.attn_q == self.shape.v_q:
+                    specs.append(("kv", [m["k"][0], m["v"][0]], a["in"].desc(M, eps), [y["k"], y["v"]], None))
+                else:
+                    specs.append(("k", [m["k"][0]], a["in"].desc(M, eps), [y["k"]], None))
+                    specs.append(("v", [m["v"][0]], a["in"].desc(M, eps), [y["v"]], None))
+            elif self.shape.attn_q == self.shape.v_q:
                 specs.append(("qkv", [m["q"][0], m["k"][0], m["v"][0]], a["in"].desc(M, eps),
                               [y["q"], y["k"], y["v"]], a["v"].ep(SV_EP_QUANT, lw.gammas["g2"], src=2)))
             else:
@@ -212,31 +284,65 @@ class VerifyStack:
         """(label, callable) of every launch of one eager pass at M positions
         (one sv_verify_matvec / sv_head_logits call per phase)."""
         ph = [("quant_in", lambda: self._quant_in(M))]
+        plan = None
+        if self.kv is not None:
+            plan = self.attention(M)
+            ph.insert(0, ("reserve", lambda: self.kv.reserve(M)))
+        li = 0
         for label, ws, a, ys, ep in self._specs(M):
+            if label == "o" and plan is not None:
+                ph.append(("attention", lambda li=li: self._attend(li, M, plan)))
+                li += 1
             ph.append((label, lambda ws=ws, a=a, ys=ys, ep=ep: verify_matvec(ws, a, ys, ep)))
         if self.head is not None:
             ph.append(("head", lambda: head_logits(self.head[0], self.a_final.desc(M, self.eps), self.logits[:M],
                                                    self.argmax[:M])))
             ph.append(("accept", lambda: self._accept(M)))
+        if self.kv is not None:
+            ph.append(("commit", lambda: self._commit(M)))
         return ph
 
     def run(self, M: int):
         for _, f in self.phases(M):
             f()
 
-    def make_pass(self, M: int) -> Pass:
-        """The projection phases and the head as one persistent launch."""
+    def make_pass(self, M: int):
+        """The projection phases and the head as one persistent launch; with
+        attention a list of them, cut before each layer's o (whose input the
+        attention writes)."""
+        if self.kv is not None:
+            cuts, phs = [], []
+            for label, ws, a, ys, ep in self._specs(M):
+                if label == "o":
+                    cuts.append(Pass(phs))
+                    phs = []
+                phs.append(phase(ws, a, ys, ep))
+            if self.head is not None:
+                phs.append(phase([self.head[0]], self.a_final.desc(M, self.eps), [self.logits[:M]],
+                                 argmax=self.argmax[:M]))
+            return cuts + [Pass(phs)]
         phs = [phase(ws, a, ys, ep) for _, ws, a, ys, ep in self._specs(M)]
         if self.head is not None:
             phs.append(phase([self.head[0]], self.a_final.desc(M, self.eps), [self.logits[:M]],
                              argmax=self.argmax[:M]))
         return Pass(phs)
 
-    def run_pass(self, M: int, p: Pass):
+    def run_pass(self, M: int, p):
+        if self.kv is not None:
+            self.kv.reserve(M)
         self._quant_in(M)
-        p.run()
+        if self.kv is not None:
+            plan = self.attention(M)
+            for li, part in enumerate(p):
+                if li:
+                    self._attend(li - 1, M, plan)
+                part.run()
+        else:
+            p.run()
         if self.head is not None:
             self._accept(M)
+        if self.kv is not None:
+            self._commit(M)
 
     def capture(self, M: int, persistent: bool = True):
         """Capture one pass at M positions in a HIP graph (torch.cuda.CUDAGraph)."""
@@ -244,10 +350,16 @@ class VerifyStack:
         p = self.make_pass(M) if persistent else None
         fn = (lambda: self.run_pass(M, p)) if persistent else (lambda: self.run(M))
         s = t.cuda.Stream()
+        if self.kv is not None:
+            self.attention(M)          # its workspace is allocated outside the graph
+            kept = [x.clone() for x in self.kv.bookkeeping()]
         s.wait_stream(t.cuda.current_stream())
         with t.cuda.stream(s):
             fn()          # warm-up on the side stream (sizes the shared workspace)
         t.cuda.current_stream().wait_stream(s)
+        if self.kv is not None:        # the warm-up's rows are not part of the sequence
+            for x, y in zip(self.kv.bookkeeping(), kept):
+                x.copy_(y)
         t.cuda.synchronize()
         g = t.cuda.CUDAGraph()
         with t.cuda.graph(g):
@@ -259,6 +371,11 @@ class VerifyStack:
     def phase_bytes(self, label: str) -> int:
         sh = self.shape
         H, F = sh.hidden, sh.ffn
+        Q, KV = sh.attn_rows()
+        if sh.attn is not None and label in ("q", "k", "kv", "v", "o"):
+            rows = {"q": [(sh.attn_q, Q, H)], "k": [(sh.attn_q, KV, H)], "v": [(sh.v_q, KV, H)],
+                    "kv": [(sh.attn_q, KV, H), (sh.v_q, KV, H)], "o": [(sh.attn_q, H, Q)]}
+            return sum(gguf_bytes(*x) for x in rows[label])
         if label == "qkv":
             return 2 * gguf_bytes(sh.attn_q, H, H) + gguf_bytes(sh.v_q, H, H)
         if label == "v":

@@ -211,6 +211,12 @@ class KvCache:
             self._compact_ws = self._torch.empty(need // 4, dtype=self._torch.int32, device=self.device)
         self._call(self._lib.sv_kv_compact, self._compact_ws.data_ptr(), need, stream=stream)
 
+    def bookkeeping(self):
+        """The tensors that say what the cache holds: table, lengths, holders,
+        free pages, counts.  Copying them back undoes calls since, but for
+        rows written to slots that were not committed."""
+        return self.table, self.lens, self.refs, self.free_ids, self.ctl
+
     def status(self) -> int:
         """SV_KV_* bits set on the device since the last call; synchronises."""
         v = ctypes.c_uint32()
