@@ -102,7 +102,7 @@ __device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals
 }
 
 // Row tiles of 16 that one wave holds, by the rows of a head.
-inline int attn_tiles_per_wave(int dim, int rows) { return dim <= 128 && rows > 16 ? 2 : 1; }
+inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 int attn_launch_f16(const AttnArgs &a, int rt, dim3 grid, hipStream_t st);
 int attn_launch_bf16(const AttnArgs &a, int rt, dim3 grid, hipStream_t st);

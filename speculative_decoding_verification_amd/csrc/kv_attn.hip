@@ -6,18 +6,22 @@ namespace sv {
 
 // The join of a row's chunks c: with M = max m_c,
 //   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c,
-// one workgroup a row; its threads split the head dimension and the chunks
-// (chunk number modulo the parts, each part in chunk order, then the parts in
-// order), so the sums do not depend on how many chunks a launch provides for.
-constexpr int kJoin = 256;
+// one workgroup a row; its threads take four elements each of the head
+// dimension and one of `parts` shares of the chunks (chunk number modulo
+// parts, each share in chunk order, then the shares in order), so the sums
+// do not depend on how many chunks a launch provides for.
+constexpr int kJoin = 256, kJoinTile = 1024;
 __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
-    __shared__ float s_v[kJoin], s_l[kJoin / 32], s_top[kJoin / 64];
+    __shared__ float s_w[kJoinTile], s_wl[kJoinTile];
+    __shared__ __align__(16) float s_v[kJoin * 4];
+    __shared__ float s_l[kJoin / 8], s_top[kJoin / 64];
+    typedef float f4 __attribute__((ext_vector_type(4)));
     const int r = blockIdx.x, head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
     const Span sp = span_of(a, b, sid);
     if (r >= sp.n * a.group) return;
-    const int D = a.kv.dim, parts = kJoin / D;
+    const int D = a.kv.dim, quads = D / 4, parts = kJoin / quads;
     const int n = min(a.chunks, sp.first + max(sp.end - sp.jump, 0));  // chunks in use
     const int64_t base = (static_cast<int64_t>(b) * a.kv.heads + head) * a.chunks * a.rows + r;
     float top = -INFINITY;
@@ -27,33 +31,53 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
     if ((tid & 63) == 0) s_top[tid >> 6] = top;
     __syncthreads();
     top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-    const int part = tid / D, d = tid % D;
-    float v = 0.0f, l = 0.0f;
-    if (part < parts && top != -INFINITY) {
-        for (int c = 0; c < n; c++) {
-            if (chunk_of(sp, c) % parts != part) continue;
-            const int64_t at = base + static_cast<int64_t>(c) * a.rows;
-            const float w = __builtin_amdgcn_exp2f(gld(a.part_m + at) - top);
-            v += w * gld(a.part_o + at * D + d);
-            l += w * gld(a.part_l + at);
+    const int part = tid / quads, d = tid % quads * 4;
+    f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+    for (int at = 0; at < n && top != -INFINITY; at += kJoinTile) {
+        const int upto = min(n - at, kJoinTile);
+        for (int i = tid; i < upto; i += kJoin) {
+            const int64_t c = base + static_cast<int64_t>(at + i) * a.rows;
+            const float w = __builtin_amdgcn_exp2f(gld(a.part_m + c) - top);
+            s_w[i] = w;
+            s_wl[i] = w * gld(a.part_l + c);
         }
+        __syncthreads();
+        if (part < parts) {
+            // the chunks of the sinks and those after them: two runs of
+            // consecutive chunk numbers
+            for (int run = 0; run < 2; run++) {
+                const int lo = max(at, run ? sp.first : 0), hi = min(at + upto, run ? n : sp.first);
+                const int shift = run ? sp.jump - sp.first : 0;
+                int c = lo + ((part - (lo + shift)) % parts + parts) % parts;
+#pragma unroll 4
+                for (; c < hi; c += parts) {
+                    v += s_w[c - at] * *(const SV_GLOBAL f4 *)(a.part_o + (base + static_cast<int64_t>(c) * a.rows) * D + d);
+                    l += s_wl[c - at];
+                }
+            }
+        }
+        __syncthreads();
     }
     if (part < parts) {
-        s_v[part * D + d] = v;
+        *reinterpret_cast<f4 *>(s_v + part * D + d) = v;
         if (d == 0) s_l[part] = l;
     }
     __syncthreads();
+    float x = 0.0f;
     if (tid < D) {
         float sum = s_l[0];
-        v = s_v[tid];
+        x = s_v[tid];
         for (int i = 1; i < parts; i++) {
-            v += s_v[i * D + tid];
+            x += s_v[i * D + tid];
             sum += s_l[i];
         }
         const bool over = a.max_len && sp.len + sp.n > a.max_len;
         if (over && tid == 0) kv_flag(a.kv, SV_KV_OVER_MAX);
-        s_v[tid] = over ? NAN : v * (sum != 0.0f ? 1.0f / sum : 0.0f);
+        x = over ? NAN : x * (sum != 0.0f ? 1.0f / sum : 0.0f);
     }
+    __syncthreads();
+    if (tid < D) s_v[tid] = x;
     __syncthreads();
     finish_rows(a, s_v, D, 1, [&](int) -> int64_t {
         return (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + head * a.group + r % a.group;

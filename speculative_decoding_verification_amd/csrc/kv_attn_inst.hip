@@ -149,22 +149,125 @@ __device__ __forceinline__ uint32_t odd_pair(uint32_t w) {
     return ((w & 0x7FFF7FFFu) + (TYPE == SV_KV_F16 ? 0x04000400u : 0x00800080u)) & 0x80008000u;
 }
 
-__device__ __forceinline__ float xor16_max(float v) {
-    v = fmaxf(v, __shfl_xor(v, 16, 64));
-    return fmaxf(v, __shfl_xor(v, 32, 64));
+// Largest value over the four lanes that share a row (16 and 32 lanes apart).
+__device__ __forceinline__ float row_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 constexpr int kWaves = 4;
 
 template <int TYPE, int D, int RT>
-__global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
+struct Lds {
+    // queries as operands, [tile][dim / 32][part][lane][16 bytes]; after the
+    // blocks the waves' sums, two waves at a time
+    static constexpr int q_bytes = RT * (D / 32) * Kind<TYPE>::kq * 1024;
+    static constexpr int ld = D + 4;
+    static constexpr int o_bytes = 2 * 16 * RT * ld * 4;
+    static constexpr int bytes = q_bytes > o_bytes ? q_bytes : o_bytes;
+};
+
+// Prepares the queries of row tile t as the second operand of S^T = K Q^T
+// (one wave): rotated, scaled, and for fp16 multiplied by the power of two
+// that brings the row's largest magnitude into [2^12, 2^13); rs is what the
+// row's scores are multiplied by to undo that.
+template <int TYPE, int D>
+__device__ void put_queries(const AttnArgs &a, const Span &sp, int b, int head, int row0, int rows, uint8_t *to,
+                            float *rs) {
     using Kd = Kind<TYPE>;
+    constexpr int NC = D / 32;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int r = row0 + col;
+    const bool live = r < rows;
+    const int m = live ? r / a.group : 0;
+    const int hq = head * a.group + (live ? r % a.group : 0);
+    const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
+    float xq[NC][8];
+#pragma unroll
+    for (int cc = 0; cc < NC; cc++) {
+        const int d0 = 32 * cc + 8 * g;
+        const uint4 u0 = gld16(qp + d0), u1 = gld16(qp + d0 + 4);
+        const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+        for (int e = 0; e < 8; e++) xq[cc][e] = __uint_as_float(u[e]);
+    }
+    if (a.rope.mode != SV_ROPE_NONE) {
+        const int half = a.rope.rot / 2;
+        const int64_t pos = sp.len + row_depth(a, b, m);
+        const int64_t at = pos < a.rope.n_pos ? pos : a.rope.n_pos - 1;
+        const float *cs = a.rope.table + at * half * 2;
+        const bool pairs = a.rope.mode == SV_ROPE_PAIRS;
+#pragma unroll
+        for (int cc = 0; cc < NC; cc++) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int d = 32 * cc + 8 * g + e;
+                if (d >= a.rope.rot || (pairs && (e & 1))) continue;
+                const bool second = !pairs && d >= half;
+                const int p = pairs ? d >> 1 : (second ? d - half : d);
+                const uint2 w = gld8(cs + 2 * p);
+                const float co = __uint_as_float(w.x), si = __uint_as_float(w.y);
+                if (pairs) {
+                    const float x0 = xq[cc][e], x1 = xq[cc][e | 1];
+                    xq[cc][e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
+                    xq[cc][e | 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
+                } else {
+                    const float own = __fmul_rn(xq[cc][e], co);
+                    const float other = __fmul_rn(gld(qp + (second ? d - half : d + half)), si);
+                    xq[cc][e] = second ? __fadd_rn(own, other) : __fsub_rn(own, other);
+                }
+            }
+        }
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int cc = 0; cc < NC; cc++)
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            xq[cc][e] = live ? xq[cc][e] * a.scale : 0.0f;
+            top = fmaxf(top, fabsf(xq[cc][e]));
+        }
+    float back = 1.0f;
+    if constexpr (__is_same(typename Kd::KVec, h8)) {
+        top = row_max(top);
+        const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased; 255 = not finite
+        const int up = ex == 0 || ex == 255 ? 0 : max(-100, min(100, 12 - (ex - 127)));
+        const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+        back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+        for (int cc = 0; cc < NC; cc++)
+#pragma unroll
+            for (int e = 0; e < 8; e++) xq[cc][e] *= by;
+    }
+    if (g == 0) rs[col] = back;
+#pragma unroll
+    for (int cc = 0; cc < NC; cc++) {
+        typename Kd::KVec part[Kd::kq];
+        split8<Kd::kq>(xq[cc], part);
+#pragma unroll
+        for (int n = 0; n < Kd::kq; n++)
+            *reinterpret_cast<typename Kd::KVec *>(to + ((cc * Kd::kq + n) * 64 + lane) * 16) = part[n];
+    }
+}
+
+// Two waves a SIMD cover each other's waits where the registers allow it.
+template <int TYPE, int D, int RT>
+constexpr int min_waves() {
+    return RT * D <= 256 && (TYPE == SV_KV_I8 || D <= 192) ? 2 : 1;
+}
+
+template <int TYPE, int D, int RT>
+__global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_attn_kernel(AttnArgs a) {
+    using Kd = Kind<TYPE>;
+    using L = Lds<TYPE, D, RT>;
     constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz;
-    constexpr int LD = D + 4;
+    constexpr int LD = L::ld;
     constexpr int ROWS = 16 * RT;
-    // the waves' results: o of two waves at a time, m and l of all
-    __shared__ float s_o[2][ROWS][LD];
-    __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS];
+    __shared__ __align__(16) uint8_t s_mem[L::bytes];
+    __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS], s_rs[ROWS];
+    float *s_o = reinterpret_cast<float *>(s_mem);  // [2][ROWS][LD]
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
@@ -177,7 +280,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
     const int c = unit % a.chunks, bh = unit / a.chunks;
     const int head = bh % heads, b = bh / heads;
     if (b >= a.bt.B) return;
-    const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
+    const int sid = a.bt.seq ? __builtin_amdgcn_readfirstlane(gld(a.bt.seq + b)) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
     const Span sp = span_of(a, b, sid);
     const int ac = chunk_of(sp, c);
@@ -187,154 +290,144 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
     const int rows = sp.n * a.group;  // of this sequence, in use
     if (row0 >= rows) return;
 
-    // ---- the rows' queries, as the second operand of S^T = K Q^T
-    typename Kd::KVec qf[RT][NC][Kd::kq];
-    float rs[RT];           // what the scores are multiplied by (a power of two)
-    uint32_t mask[RT];      // the new rows that the row sees
-    int64_t pos[RT];
-#pragma unroll
-    for (int t = 0; t < RT; t++) {
-        const int r = row0 + 16 * t + col;
-        const bool live = r < rows;
-        const int m = live ? r / a.group : 0;
-        const int hq = head * a.group + (live ? r % a.group : 0);
-        mask[t] = live ? row_mask(a, b, m) : 0u;
-        pos[t] = sp.len + row_depth(a, b, m);
-        const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
-        float xq[NC][8];
-        float top = 0.0f;
-#pragma unroll
-        for (int cc = 0; cc < NC; cc++) {
-            const int d0 = 32 * cc + 8 * g;
-            const uint4 u0 = gld16(qp + d0), u1 = gld16(qp + d0 + 4);
-            const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-            for (int e = 0; e < 8; e++) xq[cc][e] = __uint_as_float(u[e]);
-        }
-        if (a.rope.mode != SV_ROPE_NONE) {
-            const int half = a.rope.rot / 2;
-            const int64_t at = pos[t] < a.rope.n_pos ? pos[t] : a.rope.n_pos - 1;
-            const float *cs = a.rope.table + at * half * 2;
-            const bool pairs = a.rope.mode == SV_ROPE_PAIRS;
-#pragma unroll
-            for (int cc = 0; cc < NC; cc++) {
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const int d = 32 * cc + 8 * g + e;
-                    if (d >= a.rope.rot) continue;
-                    const bool second = pairs ? e & 1 : d >= half;
-                    const int p = pairs ? d >> 1 : (second ? d - half : d);
-                    const float own = pairs ? 0.0f : xq[cc][e];
-                    const float other = pairs ? 0.0f : gld(qp + (second ? d - half : d + half));
-                    const float co = gld(cs + 2 * p), si = gld(cs + 2 * p + 1);
-                    if (pairs) {
-                        if (e & 1) continue;
-                        const float x0 = xq[cc][e], x1 = xq[cc][e | 1];
-                        xq[cc][e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
-                        xq[cc][e | 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
-                    } else {
-                        xq[cc][e] = second ? __fadd_rn(__fmul_rn(own, co), __fmul_rn(other, si))
-                                           : __fsub_rn(__fmul_rn(own, co), __fmul_rn(other, si));
-                    }
-                }
-            }
-        }
+    // ---- the wave's blocks: every fourth one of the chunk, but for those
+    // between the sinks and every row's window
+    const int per = a.chunk / kBlk;
+    const int last = static_cast<int>(min(static_cast<int64_t>(ac + 1) * per, (sp.total + kBlk - 1) / kBlk));
+    const int gap0 = (a.sinks + kBlk - 1) / kBlk, gap1 = static_cast<int>(sp.lo / kBlk);
+    const int begin = ac * per + wave;
+    auto settle = [&](int j) {  // j, or the next of the wave's blocks past the gap
+        return j >= gap0 && j < gap1 ? j + (gap1 - j + kWaves - 1) / kWaves * kWaves : j;
+    };
+    auto page_of = [&](int j) {
+        return j < last ? __builtin_amdgcn_readfirstlane(kv_page_of(a.kv, sid, j >> a.kv.blk_shift)) : -1;
+    };
+    // a block without a page is read from page 0 and masked
+    auto block_at = [&](int j, int page) {
+        return kv_block(a.kv, a.layer, max(page, 0), head, j & ((1 << a.kv.blk_shift) - 1));
+    };
+    Raw<ESZ> kr[NC][2], vr[ND];
+    float ks[8], vs[8];  // int8: the scales of the lane group's eight slots
+    const uint32_t k_at = (g * 32 + 8 * (col >> 2) + (col & 3)) * 8 * ESZ;
+    const uint32_t v_at = (32 * D + (g * D + col) * 8) * ESZ;
+    auto load_k = [&](const uint8_t *blk) {
 #pragma unroll
         for (int cc = 0; cc < NC; cc++)
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                xq[cc][e] = live ? xq[cc][e] * a.scale : 0.0f;
-                top = fmaxf(top, fabsf(xq[cc][e]));
+            for (int u = 0; u < 2; u++) kr[cc][u] = load_raw<ESZ>(blk + k_at + (cc * 128 + 4 * u) * 8 * ESZ);
+        if constexpr (TYPE == SV_KV_I8) {
+            const uint8_t *sc = blk + 64 * D + 32 * g;
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const uint4 w = gld16(sc + 4 * e);
+                ks[e] = __uint_as_float(w.x);
+                ks[e + 1] = __uint_as_float(w.y);
+                ks[e + 2] = __uint_as_float(w.z);
+                ks[e + 3] = __uint_as_float(w.w);
             }
-        rs[t] = 1.0f;
-        if constexpr (__is_same(typename Kd::KVec, h8)) {
-            // the row's largest magnitude into [2^12, 2^13)
-            top = xor16_max(top);
-            const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased; 255 = not finite
-            const int up = ex == 0 || ex == 255 ? 0 : max(-100, min(100, 12 - (ex - 127)));
-            const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-            rs[t] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        }
+    };
+    auto load_v = [&](const uint8_t *blk) {
+        if constexpr (TYPE == SV_KV_I8) {
+            const uint8_t *sc = blk + 64 * D + 128 + 32 * g;
 #pragma unroll
-            for (int cc = 0; cc < NC; cc++)
-#pragma unroll
-                for (int e = 0; e < 8; e++) xq[cc][e] *= by;
+            for (int e = 0; e < 8; e += 4) {
+                const uint4 w = gld16(sc + 4 * e);
+                vs[e] = __uint_as_float(w.x);
+                vs[e + 1] = __uint_as_float(w.y);
+                vs[e + 2] = __uint_as_float(w.z);
+                vs[e + 3] = __uint_as_float(w.w);
+            }
         }
 #pragma unroll
-        for (int cc = 0; cc < NC; cc++) split8<Kd::kq>(xq[cc], qf[t][cc]);
+        for (int i = 0; i < ND; i++) vr[i] = load_raw<ESZ>(blk + v_at + i * 128 * ESZ);
+    };
+
+    int j = settle(begin);
+    int page = page_of(j);
+    const uint8_t *blk = block_at(j, page);
+    int jn = settle(j + kWaves);
+    int page_n = page_of(jn);
+    if (j < last) {
+        load_k(blk);
+        load_v(blk);
     }
+    if (wave < RT)
+        put_queries<TYPE, D>(a, sp, b, head, row0 + 16 * wave, rows, s_mem + wave * (L::q_bytes / RT),
+                             s_rs + 16 * wave);
+    __syncthreads();
 
     f4 o[RT][ND];
-    float mx[RT], l[RT];
+    float mx[RT], l[RT], rs[RT];
 #pragma unroll
     for (int t = 0; t < RT; t++) {
         mx[t] = -INFINITY;
         l[t] = 0.0f;
+        rs[t] = s_rs[16 * t + col];
 #pragma unroll
         for (int i = 0; i < ND; i++) o[t][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-
-    // ---- the wave's blocks
-    const int per = a.chunk / kBlk;
-    int64_t j = static_cast<int64_t>(ac) * per + wave;
-    const int64_t last = min(static_cast<int64_t>(ac + 1) * per, (sp.total + kBlk - 1) / kBlk);
     const int64_t whole = sp.len + sp.n - a.window;  // with a window: from here on every row's window has begun
-    for (; j < last; j += kWaves) {
-        const int64_t s0 = j * kBlk;
-        if (s0 >= a.sinks && s0 + kBlk <= sp.lo) continue;  // between the sinks and every window
-        const int page = kv_page_of(a.kv, sid, j >> a.kv.blk_shift);
-        if (page < 0) continue;
-        const uint8_t *blk = kv_block(a.kv, a.layer, page, head, static_cast<int>(j & ((1 << a.kv.blk_shift) - 1)));
-        Raw<ESZ> kr[NC][2], vr[ND];
-#pragma unroll
-        for (int cc = 0; cc < NC; cc++)
-#pragma unroll
-            for (int u = 0; u < 2; u++)
-                kr[cc][u] = load_raw<ESZ>(blk + (((cc * 4 + g) * 32) + 8 * (col >> 2) + 4 * u + (col & 3)) * 8 * ESZ);
-#pragma unroll
-        for (int i = 0; i < ND; i++) vr[i] = load_raw<ESZ>(blk + (32 * D + (g * D + 16 * i + col) * 8) * ESZ);
-        float ks[8], vs[8];  // int8: the scales of the lane group's eight slots
-        if constexpr (TYPE == SV_KV_I8) {
-            const float *sc = reinterpret_cast<const float *>(blk + 64 * D) + 8 * g;
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                ks[e] = gld(sc + e);
-                vs[e] = gld(sc + 32 + e);
-            }
-        }
-        const bool edge = s0 + kBlk > sp.len || (a.window && s0 < whole && s0 + kBlk > a.sinks);
-        // slots of the lane group that any row of the tile sees, and those that all see
-        uint32_t any_sees = 0xFFu, all_see = 0xFFu;
-        if (edge) any_sees = 0u;
+    while (j < last) {
+        const int64_t s0 = static_cast<int64_t>(j) * kBlk;
+        // ---- scores, and the next block's keys on their way
         float p[RT][8];
+        {
+            f4 acc[RT][2];
+#pragma unroll
+            for (int t = 0; t < RT; t++) acc[t][0] = acc[t][1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int cc = 0; cc < NC; cc++) {
+                const typename Kd::KVec k0 = widen<typename Kd::KVec>(kr[cc][0]);
+                const typename Kd::KVec k1 = widen<typename Kd::KVec>(kr[cc][1]);
+#pragma unroll
+                for (int n = Kd::kq - 1; n >= 0; n--)
+#pragma unroll
+                    for (int t = 0; t < RT; t++) {
+                        const typename Kd::KVec q = *reinterpret_cast<const typename Kd::KVec *>(
+                            s_mem + t * (L::q_bytes / RT) + ((cc * Kd::kq + n) * 64 + lane) * 16);
+                        acc[t][0] = mma(k0, q, acc[t][0]);
+                        acc[t][1] = mma(k1, q, acc[t][1]);
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < RT; t++)
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    p[t][e] = acc[t][e >> 2][e & 3] * rs[t];
+                    if constexpr (TYPE == SV_KV_I8) p[t][e] *= ks[e];
+                }
+        }
+        const uint8_t *blk_n = block_at(jn, page_n);
+        __builtin_amdgcn_sched_barrier(0);
+        if (jn < last) load_k(blk_n);
+        const int jnn = settle(jn + kWaves);
+        const int page_nn = page_of(jnn);
+        __builtin_amdgcn_sched_barrier(0);
+
+        // ---- what is visible, and the running softmax
+        const bool edge = page < 0 || s0 + kBlk > sp.len || (a.window && s0 < whole && s0 + kBlk > a.sinks);
+        // slots of the lane group that any row of the tile sees, and those that all see
+        uint32_t any_sees = edge ? 0u : 0xFFu, all_see = 0xFFu;
         uint32_t seen[RT];  // slots of the lane group that the lane's row sees
 #pragma unroll
-        for (int t = 0; t < RT; t++) {
-            f4 acc[2];
-            acc[0] = acc[1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < RT; t++) seen[t] = 0xFFu;
+        if (edge) {
 #pragma unroll
-            for (int cc = 0; cc < NC; cc++)
-#pragma unroll
-                for (int u = 0; u < 2; u++)
-#pragma unroll
-                    for (int n = Kd::kq - 1; n >= 0; n--)
-                        acc[u] = mma(widen<typename Kd::KVec>(kr[cc][u]), qf[t][cc][n], acc[u]);
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                p[t][e] = acc[e >> 2][e & 3] * rs[t];
-                if constexpr (TYPE == SV_KV_I8) p[t][e] *= ks[e];
-            }
-            seen[t] = 0xFFu;
-            if (edge) {
-                const bool live = row0 + 16 * t + col < rows;
+            for (int t = 0; t < RT; t++) {
+                const int r = row0 + 16 * t + col;
+                const bool live = r < rows;
+                const int m = live ? r / a.group : 0;
+                const uint32_t mask = row_mask(a, b, m);
+                const int64_t pos = sp.len + row_depth(a, b, m);
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
                     const int64_t slot = s0 + 8 * g + e;
                     const int nth = static_cast<int>(slot - sp.len);
-                    bool sees = nth < 0 || (nth < sp.n && (mask[t] >> nth & 1u));
-                    if (slot >= sp.total) sees = false;
+                    bool sees = page >= 0 && slot < sp.total && (nth < 0 || (nth < sp.n && (mask >> nth & 1u)));
                     if (a.window && sees) {
                         const int64_t kpos = nth < 0 ? slot : sp.len + row_depth(a, b, nth);
-                        sees = pos[t] - kpos < a.window || kpos < a.sinks;
+                        sees = pos - kpos < a.window || kpos < a.sinks;
                     }
                     if (!sees) {
                         p[t][e] = -INFINITY;
@@ -346,10 +439,13 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
                     if (by != of) all_see &= ~(1u << e);
                 }
             }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; t++) {
             float top = p[t][0];
 #pragma unroll
             for (int e = 1; e < 8; e++) top = fmaxf(top, p[t][e]);
-            const float now = fmaxf(mx[t], xor16_max(top));
+            const float now = fmaxf(mx[t], row_max(top));
             const float base = now == -INFINITY ? 0.0f : now;
             const float keep = __builtin_amdgcn_exp2f(mx[t] - base);
             mx[t] = now;
@@ -371,6 +467,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
                 for (int e = 0; e < 8; e++) p[t][e] = p[t][e] == 0.0f ? 0.0f : p[t][e] * vs[e];
             }
         }
+
+        // ---- o += V^T P^T
         bool odd = false;
         if constexpr (TYPE != SV_KV_I8) {
             if (edge) {
@@ -378,18 +476,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
                 // hold.  Infinities and NaN in a slot that some rows see and
                 // others do not cannot go through a product with weight 0:
                 // they are taken out and added row by row.
-                uint32_t keep2[4];
+                uint32_t keep2[4], some[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++)
+                for (int e = 0; e < 4; e++) {
                     keep2[e] = (any_sees >> (2 * e) & 1u ? 0x0000FFFFu : 0u) | (any_sees >> (2 * e + 1) & 1u ? 0xFFFF0000u : 0u);
+                    some[e] = (all_see >> (2 * e) & 1u ? 0u : 0x00008000u) | (all_see >> (2 * e + 1) & 1u ? 0u : 0x80000000u);
+                }
                 uint32_t found = 0;
 #pragma unroll
                 for (int i = 0; i < ND; i++)
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         vr[i].w[e] &= keep2[e];
-                        const uint32_t f = odd_pair<TYPE>(vr[i].w[e]);
-                        found |= f & ((all_see >> (2 * e) & 1u ? 0u : 0x00008000u) | (all_see >> (2 * e + 1) & 1u ? 0u : 0x80000000u));
+                        found |= odd_pair<TYPE>(vr[i].w[e]) & some[e];
                     }
                 odd = __any(found != 0);
                 if (odd) {
@@ -404,40 +503,52 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
                 }
             }
         }
+        {
+            typename Kd::VVec pf[RT][Kd::kp];
 #pragma unroll
-        for (int t = 0; t < RT; t++) {
-            typename Kd::VVec pf[Kd::kp];
-            split8<Kd::kp>(p[t], pf);
+            for (int t = 0; t < RT; t++) split8<Kd::kp>(p[t], pf[t]);
 #pragma unroll
-            for (int i = 0; i < ND; i++)
+            for (int i = 0; i < ND; i++) {
+                const typename Kd::VVec v = widen<typename Kd::VVec>(vr[i]);
 #pragma unroll
                 for (int n = Kd::kp - 1; n >= 0; n--)
-                    o[t][i] = mma(widen<typename Kd::VVec>(vr[i]), pf[n], o[t][i]);
+#pragma unroll
+                    for (int t = 0; t < RT; t++) o[t][i] = mma(v, pf[t][n], o[t][i]);
+            }
         }
         if constexpr (TYPE != SV_KV_I8) {
             if (odd) {
-                for (int gg = 0; gg < 4; gg++) {
+#pragma unroll 1
+                for (int s = 0; s < kBlk; s++) {
+                    const uint8_t *v = blk + (32 * D + ((s >> 3) * D + 4 * g) * 8 + (s & 7)) * ESZ;
 #pragma unroll
                     for (int t = 0; t < RT; t++) {
-                        const uint32_t sees = __shfl(seen[t], 16 * gg + col, 64);
+                        float w = p[t][0];
 #pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            const float w = __shfl(p[t][e], 16 * gg + col, 64);
-                            const uint8_t *v = blk + (32 * D + (gg * D + 4 * g) * 8 + e) * ESZ;
+                        for (int e = 1; e < 8; e++) w = (s & 7) == e ? p[t][e] : w;
+                        const int from = 16 * (s >> 3) + col;
+                        w = __shfl(w, from, 64);
+                        const bool sees = __shfl(seen[t], from, 64) >> (s & 7) & 1u;
 #pragma unroll
-                            for (int i = 0; i < ND; i++)
+                        for (int i = 0; i < ND; i++)
 #pragma unroll
-                                for (int k = 0; k < 4; k++) {
-                                    const uint32_t h = gld(reinterpret_cast<const uint16_t *>(v) + (16 * i + k) * 8);
-                                    if (!odd_pair<TYPE>(h) || !(sees >> e & 1u)) continue;
-                                    const float y = TYPE == SV_KV_F16 ? half_bits_to_float(h) : __uint_as_float(h << 16);
-                                    o[t][i][k] += times_parts<Kd::kp, typename Kd::VVec>(w, y);
-                                }
-                        }
+                            for (int k = 0; k < 4; k++) {
+                                const uint32_t h = gld(reinterpret_cast<const uint16_t *>(v) + (16 * i + k) * 8);
+                                if (!odd_pair<TYPE>(h) || !sees) continue;
+                                const float y = TYPE == SV_KV_F16 ? half_bits_to_float(h) : __uint_as_float(h << 16);
+                                o[t][i][k] += times_parts<Kd::kp, typename Kd::VVec>(w, y);
+                            }
                     }
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (jn < last) load_v(blk_n);
+        j = jn;
+        page = page_n;
+        blk = blk_n;
+        jn = jnn;
+        page_n = page_nn;
     }
 
     // ---- the waves' results joined: (0 + 2) + (1 + 3)
@@ -450,19 +561,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
             s_l[wave][16 * t + col] = l[t];
         }
     }
-    __syncthreads();
-    float by[RT];
+    __syncthreads();  // the queries are no longer read
 #pragma unroll
     for (int t = 0; t < RT; t++) {
         float top = s_m[0][16 * t + col];
 #pragma unroll
         for (int w = 1; w < kWaves; w++) top = fmaxf(top, s_m[w][16 * t + col]);
-        by[t] = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[t] - top);
+        const float by = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[t] - top);
 #pragma unroll
-        for (int i = 0; i < ND; i++) o[t][i] *= by[t];
+        for (int i = 0; i < ND; i++) o[t][i] *= by;
         if (wave >= 2)
 #pragma unroll
-            for (int i = 0; i < ND; i++) *reinterpret_cast<f4 *>(&s_o[wave - 2][16 * t + col][16 * i + 4 * g]) = o[t][i];
+            for (int i = 0; i < ND; i++)
+                *reinterpret_cast<f4 *>(s_o + ((wave - 2) * ROWS + 16 * t + col) * LD + 16 * i + 4 * g) = o[t][i];
     }
     __syncthreads();
     if (wave < 2) {
@@ -470,7 +581,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
         for (int t = 0; t < RT; t++)
 #pragma unroll
             for (int i = 0; i < ND; i++) {
-                f4 *at = reinterpret_cast<f4 *>(&s_o[wave][16 * t + col][16 * i + 4 * g]);
+                f4 *at = reinterpret_cast<f4 *>(s_o + (wave * ROWS + 16 * t + col) * LD + 16 * i + 4 * g);
                 *at = o[t][i] + *at;
             }
     }
@@ -480,7 +591,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
     const int64_t part = ((static_cast<int64_t>(b) * heads + head) * a.chunks + c) * a.rows + row0;
     for (int i = threadIdx.x; i < n * (D / 4); i += 64 * kWaves) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        f4 v = *reinterpret_cast<f4 *>(&s_o[0][r][d]) + *reinterpret_cast<f4 *>(&s_o[1][r][d]);
+        f4 v = *reinterpret_cast<f4 *>(s_o + r * LD + d) + *reinterpret_cast<f4 *>(s_o + (ROWS + r) * LD + d);
         float top = s_m[0][r];
         for (int w = 1; w < kWaves; w++) top = fmaxf(top, s_m[w][r]);
         float sum = 0.0f;
@@ -490,7 +601,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
             const bool over = a.max_len && sp.len + sp.n > a.max_len;
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
             v = over ? f4{NAN, NAN, NAN, NAN} : v * inv;
-            *reinterpret_cast<f4 *>(&s_o[0][r][d]) = v;
+            *reinterpret_cast<f4 *>(s_o + r * LD + d) = v;
             if (over && i == 0) kv_flag(a.kv, SV_KV_OVER_MAX);
         } else {
             *(SV_GLOBAL f4 *)(a.part_o + (part + r) * D + d) = v;
@@ -502,7 +613,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
     }
     if (alone) {
         __syncthreads();
-        finish_rows(a, &s_o[0][0][0], LD, n, [&](int i) -> int64_t {
+        finish_rows(a, s_o, LD, n, [&](int i) -> int64_t {
             const int r = row0 + i;
             return (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + head * a.group + r % a.group;
         });
@@ -512,6 +623,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void kv_attn_kernel(AttnArgs a) {
 template <int TYPE, int D>
 static int launch_dim(const AttnArgs &a, int rt, dim3 grid, hipStream_t st) {
     if constexpr (D <= 128) {
+        if (rt == 4) {
+            hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, 4>), grid, dim3(64 * kWaves), 0, st, a);
+            return hip_check(hipGetLastError(), "kv_attention launch");
+        }
         if (rt == 2) {
             hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, 2>), grid, dim3(64 * kWaves), 0, st, a);
             return hip_check(hipGetLastError(), "kv_attention launch");
