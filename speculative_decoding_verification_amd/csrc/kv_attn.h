@@ -59,28 +59,21 @@ __device__ __forceinline__ int chunk_of(const Span &s, int c) { return c < s.fir
 __device__ __forceinline__ uint32_t row_mask(const AttnArgs &a, int b, int m) {
     return a.bt.tree ? gld(a.bt.tree + static_cast<int64_t>(b) * a.bt.M + m) : (2u << m) - 1;
 }
-// Rows before row m that it sees: its place after the committed slots.
-__device__ __forceinline__ int row_depth(const AttnArgs &a, int b, int m) {
-    return a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
-}
-
-// Writes the finished values of `n` heads' rows from LDS: out, and the next
-// projection's input as sv_quantize_act_q8 makes it of out (a half wave per
-// 32 values, the same reductions in the same order).  at(i) gives row i's
-// place in out in units of dim, or -1 to pass over it.
-template <typename At>
-__device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals, int ld, int n, At at) {
+// Writes the finished values of rows row0 .. row0 + n - 1 of a head from LDS:
+// out, and the next projection's input as sv_quantize_act_q8 makes it of out
+// (a half wave per 32 values, the same reductions in the same order).
+__device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals, int ld, int b, int head, int row0,
+                                            int n) {
     const int nb = a.kv.dim / 32, lane = threadIdx.x & 31;
-    const int64_t K = static_cast<int64_t>(a.q_heads) * a.kv.dim;
     for (int it = threadIdx.x >> 5; it < n * nb; it += blockDim.x >> 5) {
-        const int i = it / nb, blk = it % nb;
-        const int64_t row = at(i);
-        if (row < 0) continue;  // a half wave leaves together
+        const int i = it / nb, blk = it % nb, r = row0 + i;
+        const int hq = head * a.group + r % a.group;
+        const int64_t row = (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + hq;
         const float x = vals[i * ld + 32 * blk + lane];
         const int64_t e = row * a.kv.dim + 32 * blk + lane;
         if (a.out) gst(a.out + e, x);
         if (a.ep.mode == SV_EP_NONE) continue;
-        const float y = a.ep.gamma ? x * gld(a.ep.gamma + e % K) : x;
+        const float y = a.ep.gamma ? x * gld(a.ep.gamma + hq * a.kv.dim + 32 * blk + lane) : x;
         float m = fabsf(y);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 32));

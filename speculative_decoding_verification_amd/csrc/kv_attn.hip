@@ -79,9 +79,7 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
     __syncthreads();
     if (tid < D) s_v[tid] = x;
     __syncthreads();
-    finish_rows(a, s_v, D, 1, [&](int) -> int64_t {
-        return (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + head * a.group + r % a.group;
-    });
+    finish_rows(a, s_v, D, b, head, r, 1);
 }
 
 // Slots of a chunk: enough chunks to give every compute unit several

@@ -55,6 +55,8 @@ struct Kind<SV_KV_I8> {
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
+constexpr int kWaves = 4;
+
 // x = sum of N parts of the narrow type, each the rounding of what is left.
 template <int N, typename V8>
 __device__ __forceinline__ void split8(const float (&x)[8], V8 (&part)[N]) {
@@ -157,76 +159,86 @@ __device__ __forceinline__ float row_max(float v) {
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-constexpr int kWaves = 4;
-
 template <int TYPE, int D, int RT>
 struct Lds {
-    // queries as operands, [tile][dim / 32][part][lane][16 bytes]; after the
-    // blocks the waves' sums, two waves at a time
+    // queries as operands, [tile][dim / 32][part][lane][16 bytes], and behind
+    // them the fp32 rows they are made of; after the blocks the waves' sums,
+    // two waves at a time
     static constexpr int q_bytes = RT * (D / 32) * Kind<TYPE>::kq * 1024;
     static constexpr int ld = D + 4;
-    static constexpr int o_bytes = 2 * 16 * RT * ld * 4;
-    static constexpr int bytes = q_bytes > o_bytes ? q_bytes : o_bytes;
+    static constexpr int row_bytes = 16 * RT * ld * 4;
+    static constexpr int bytes = q_bytes > row_bytes ? q_bytes + row_bytes : 2 * row_bytes;
 };
 
-// Prepares the queries of row tile t as the second operand of S^T = K Q^T
-// (one wave): rotated, scaled, and for fp16 multiplied by the power of two
-// that brings the row's largest magnitude into [2^12, 2^13); rs is what the
-// row's scores are multiplied by to undo that.
-template <int TYPE, int D>
-__device__ void put_queries(const AttnArgs &a, const Span &sp, int b, int head, int row0, int rows, uint8_t *to,
-                            float *rs) {
-    using Kd = Kind<TYPE>;
-    constexpr int NC = D / 32;
-    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    const int r = row0 + col;
-    const bool live = r < rows;
-    const int m = live ? r / a.group : 0;
-    const int hq = head * a.group + (live ? r % a.group : 0);
-    const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
-    float xq[NC][8];
+// The rows' queries, rotated and scaled, as fp32 in LDS: the workgroup's
+// threads take four elements each, and every load of an element is issued
+// before any is used.
+template <int D, int ROWS, int MODE>
+__device__ __forceinline__ void stage_rows(const AttnArgs &a, const Span &sp, int b, int head, int row0, int rows,
+                                           const int *depth, float *to) {
+    constexpr int LD = D + 4, QUADS = D / 4;
+#pragma unroll 4
+    for (int it = threadIdx.x; it < ROWS * QUADS; it += 64 * kWaves) {
+        const int i = it / QUADS, d = it % QUADS * 4;
+        const int r = row0 + i;
+        const bool live = r < rows;
+        const int m = live ? r / a.group : 0;
+        const int hq = head * a.group + (live ? r % a.group : 0);
+        const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
+        const uint4 u = gld16(qp + d);
+        float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
+        if constexpr (MODE != SV_ROPE_NONE) {
+            const int half = a.rope.rot / 2;
+            const int64_t pos = min(sp.len + depth[m], static_cast<int64_t>(a.rope.n_pos - 1));
+            const float *cs = a.rope.table + pos * half * 2;
+            if constexpr (MODE == SV_ROPE_PAIRS) {
 #pragma unroll
-    for (int cc = 0; cc < NC; cc++) {
-        const int d0 = 32 * cc + 8 * g;
-        const uint4 u0 = gld16(qp + d0), u1 = gld16(qp + d0 + 4);
-        const uint32_t u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+                for (int e = 0; e < 4; e += 2) {
+                    const bool turn = d + e < a.rope.rot;
+                    const uint2 w = gld8(cs + (turn ? d + e : 0));
+                    const float co = __uint_as_float(w.x), si = __uint_as_float(w.y), x0 = x[e], x1 = x[e + 1];
+                    if (turn) {
+                        x[e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
+                        x[e + 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
+                    }
+                }
+            } else {
 #pragma unroll
-        for (int e = 0; e < 8; e++) xq[cc][e] = __uint_as_float(u[e]);
-    }
-    if (a.rope.mode != SV_ROPE_NONE) {
-        const int half = a.rope.rot / 2;
-        const int64_t pos = sp.len + row_depth(a, b, m);
-        const int64_t at = pos < a.rope.n_pos ? pos : a.rope.n_pos - 1;
-        const float *cs = a.rope.table + at * half * 2;
-        const bool pairs = a.rope.mode == SV_ROPE_PAIRS;
-#pragma unroll
-        for (int cc = 0; cc < NC; cc++) {
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int d = 32 * cc + 8 * g + e;
-                if (d >= a.rope.rot || (pairs && (e & 1))) continue;
-                const bool second = !pairs && d >= half;
-                const int p = pairs ? d >> 1 : (second ? d - half : d);
-                const uint2 w = gld8(cs + 2 * p);
-                const float co = __uint_as_float(w.x), si = __uint_as_float(w.y);
-                if (pairs) {
-                    const float x0 = xq[cc][e], x1 = xq[cc][e | 1];
-                    xq[cc][e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
-                    xq[cc][e | 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
-                } else {
-                    const float own = __fmul_rn(xq[cc][e], co);
-                    const float other = __fmul_rn(gld(qp + (second ? d - half : d + half)), si);
-                    xq[cc][e] = second ? __fadd_rn(own, other) : __fsub_rn(own, other);
+                for (int e = 0; e < 4; e++) {
+                    const bool turn = d + e < a.rope.rot, second = d + e >= half;
+                    const int p = !turn ? 0 : second ? d + e - half : d + e;
+                    const uint2 w = gld8(cs + 2 * p);
+                    const float other = gld(qp + (!turn ? 0 : second ? p : p + half));
+                    const float own = __fmul_rn(x[e], __uint_as_float(w.x));
+                    const float by = __fmul_rn(other, __uint_as_float(w.y));
+                    if (turn) x[e] = second ? __fadd_rn(own, by) : __fsub_rn(own, by);
                 }
             }
         }
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        f4 z;
+#pragma unroll
+        for (int e = 0; e < 4; e++) z[e] = live ? x[e] * a.scale : 0.0f;
+        *reinterpret_cast<f4 *>(to + i * LD + d) = z;
     }
+}
+
+// The queries of a row tile as the second operand of S^T = K Q^T (one wave),
+// for fp16 multiplied by the power of two that brings the row's largest
+// magnitude into [2^12, 2^13); rs is what the row's scores are multiplied by
+// to undo that.
+template <int TYPE, int D>
+__device__ __forceinline__ void put_queries(const float *from, uint8_t *to, float *rs) {
+    using Kd = Kind<TYPE>;
+    constexpr int NC = D / 32, LD = D + 4;
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    float xq[NC][8];
     float top = 0.0f;
 #pragma unroll
     for (int cc = 0; cc < NC; cc++)
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            xq[cc][e] = live ? xq[cc][e] * a.scale : 0.0f;
+            xq[cc][e] = from[col * LD + 32 * cc + 8 * g + e];
             top = fmaxf(top, fabsf(xq[cc][e]));
         }
     float back = 1.0f;
@@ -267,6 +279,8 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
     constexpr int ROWS = 16 * RT;
     __shared__ __align__(16) uint8_t s_mem[L::bytes];
     __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS], s_rs[ROWS];
+    __shared__ uint32_t s_mask[SV_MAX_M];  // the new rows that a row sees, and how many come before it
+    __shared__ int s_depth[SV_MAX_M];
     float *s_o = reinterpret_cast<float *>(s_mem);  // [2][ROWS][LD]
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -352,9 +366,18 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
         load_k(blk);
         load_v(blk);
     }
-    if (wave < RT)
-        put_queries<TYPE, D>(a, sp, b, head, row0 + 16 * wave, rows, s_mem + wave * (L::q_bytes / RT),
-                             s_rs + 16 * wave);
+    if (threadIdx.x < SV_MAX_M) {
+        const uint32_t mask = static_cast<int>(threadIdx.x) < sp.n ? row_mask(a, b, threadIdx.x) : 0u;
+        s_mask[threadIdx.x] = mask;
+        s_depth[threadIdx.x] = __popc(mask & ((1u << threadIdx.x) - 1));
+    }
+    __syncthreads();
+    float *staged = reinterpret_cast<float *>(s_mem + L::q_bytes);
+    if (a.rope.mode == SV_ROPE_NONE) stage_rows<D, ROWS, SV_ROPE_NONE>(a, sp, b, head, row0, rows, s_depth, staged);
+    else if (a.rope.mode == SV_ROPE_PAIRS) stage_rows<D, ROWS, SV_ROPE_PAIRS>(a, sp, b, head, row0, rows, s_depth, staged);
+    else stage_rows<D, ROWS, SV_ROPE_HALVES>(a, sp, b, head, row0, rows, s_depth, staged);
+    __syncthreads();
+    if (wave < RT) put_queries<TYPE, D>(staged + 16 * wave * LD, s_mem + wave * (L::q_bytes / RT), s_rs + 16 * wave);
     __syncthreads();
 
     f4 o[RT][ND];
@@ -418,15 +441,15 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
                 const int r = row0 + 16 * t + col;
                 const bool live = r < rows;
                 const int m = live ? r / a.group : 0;
-                const uint32_t mask = row_mask(a, b, m);
-                const int64_t pos = sp.len + row_depth(a, b, m);
+                const uint32_t mask = s_mask[m];
+                const int64_t pos = sp.len + s_depth[m];
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
                     const int64_t slot = s0 + 8 * g + e;
                     const int nth = static_cast<int>(slot - sp.len);
                     bool sees = page >= 0 && slot < sp.total && (nth < 0 || (nth < sp.n && (mask >> nth & 1u)));
                     if (a.window && sees) {
-                        const int64_t kpos = nth < 0 ? slot : sp.len + row_depth(a, b, nth);
+                        const int64_t kpos = nth < 0 ? slot : sp.len + s_depth[nth];
                         sees = pos - kpos < a.window || kpos < a.sinks;
                     }
                     if (!sees) {
@@ -613,10 +636,7 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
     }
     if (alone) {
         __syncthreads();
-        finish_rows(a, s_o, LD, n, [&](int i) -> int64_t {
-            const int r = row0 + i;
-            return (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + head * a.group + r % a.group;
-        });
+        finish_rows(a, s_o, LD, b, head, row0, n);
     }
 }
 
