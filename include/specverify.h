@@ -453,7 +453,7 @@ typedef struct {
     int32_t mode;       /* SV_ROPE_* */
     int32_t rot;        /* elements rotated, the first of a head: even, at most dim */
     int32_t n_pos;      /* rows of table, at least width * page */
-    const float *table; /* [n_pos][rot / 2][2] cos, sin; 8-byte aligned */
+    const float *table; /* [n_pos][rot / 2][2] cos, sin; 16-byte aligned */
 } sv_kv_rope;
 
 /* Bytes of one page / of the pool, or 0 for an unsupported cache. */

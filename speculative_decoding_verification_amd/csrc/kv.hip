@@ -86,7 +86,7 @@ int kv_check_rope(const KvDev &kv, const sv_kv_rope *r, const char *who_) {
     SV_REQUIRE(static_cast<int64_t>(r->n_pos) >= static_cast<int64_t>(kv.width) * kv.page, SV_ERR_SHAPE,
                who + ": the rope table must cover width * page positions");
     SV_REQUIRE(r->table, SV_ERR_ARG, who + ": NULL rope table");
-    SV_REQUIRE(aligned(r->table, 8), SV_ERR_ALIGN, who + ": the rope table must be 8-byte aligned");
+    SV_REQUIRE(aligned(r->table, 16), SV_ERR_ALIGN, who + ": the rope table must be 16-byte aligned");
     return SV_OK;
 }
 

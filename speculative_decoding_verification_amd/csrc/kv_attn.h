@@ -6,6 +6,19 @@
 
 namespace sv {
 
+// Division of 0 <= x < 2^31 by a number that the host knows.
+struct Div {
+    uint32_t m, sh;
+    __device__ __forceinline__ int operator()(int x) const {
+        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * m >> sh);
+    }
+};
+inline Div div_by(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) l++;
+    return Div{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 struct AttnArgs {
     KvDev kv;
     sv_kv_batch bt;
@@ -23,68 +36,132 @@ struct AttnArgs {
     int32_t chunks;    // of a launch: as many as any sequence can have
     int32_t tiles;     // workgroups that share a (sequence, head, chunk): row groups
     float scale;       // times log2(e)
+    Div by_group, by_chunk, by_tiles, by_heads;
 };
 
-// What a sequence's rows see, in whole chunks.
+// What a sequence's rows see, in whole chunks.  Slots fit 32 bits (width *
+// page is below 2^31 - 65536).
 struct Span {
-    int64_t len;       // committed slots
-    int64_t total;     // slots that can be seen: committed and new, within the table row
-    int64_t lo;        // first slot inside the first row's window
-    int n;             // rows
-    int first;         // chunks [0, first) hold the sinks; the next one of the launch is chunk `jump`
+    int len;      // committed slots
+    int total;    // slots that can be seen: committed and new, within the table row
+    int lo;       // first slot inside the first row's window
+    int n;        // rows
+    int first;    // chunks [0, first) hold the sinks; the next one of the launch is chunk `jump`
     int jump;
-    int end;           // one past the last chunk
+    int end;      // one past the last chunk
 };
 
-__device__ __forceinline__ Span span_of(const AttnArgs &a, int b, int sid) {
+__device__ __forceinline__ Span span_of(const AttnArgs &a, int len, int n) {
     Span s;
-    s.len = kv_len_of(a.kv, sid);
-    s.n = kv_rows_of(a.bt.n_new, b, a.bt.M);
-    const int64_t cap = static_cast<int64_t>(a.kv.width) * a.kv.page;
+    s.len = len;
+    s.n = n;
+    const int cap = a.kv.width * a.kv.page;
     s.total = s.len + s.n < cap ? s.len + s.n : cap;
     s.lo = a.window && s.len >= a.window ? s.len - a.window + 1 : 0;
-    s.end = static_cast<int>((s.total + a.chunk - 1) / a.chunk);
+    s.end = a.by_chunk(s.total + a.chunk - 1);
     s.first = 0;
     s.jump = 0;
     if (s.lo > a.sinks) {
-        s.first = (a.sinks + a.chunk - 1) / a.chunk;
-        s.jump = static_cast<int>(s.lo / a.chunk);
+        s.first = a.by_chunk(a.sinks + a.chunk - 1);
+        s.jump = a.by_chunk(s.lo);
         if (s.jump < s.first) s.jump = s.first;
     }
     return s;
 }
+// Chunks of a sequence in a launch.
+__device__ __forceinline__ int chunks_of(const AttnArgs &a, const Span &s) {
+    return min(a.chunks, s.first + max(s.end - s.jump, 0));
+}
 // Chunk of a launch's index c; at or past s.end: none.
 __device__ __forceinline__ int chunk_of(const Span &s, int c) { return c < s.first ? c : s.jump + (c - s.first); }
+
+// A value that the compiler takes as new, so that what follows from it is
+// formed where it is used and not kept in registers across a loop.
+__device__ __forceinline__ int fresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
 
 __device__ __forceinline__ uint32_t row_mask(const AttnArgs &a, int b, int m) {
     return a.bt.tree ? gld(a.bt.tree + static_cast<int64_t>(b) * a.bt.M + m) : (2u << m) - 1;
 }
+// Sums and maxima over lanes by moves that need no index register (an index
+// would be kept across the kernel's loops).  Over 32 lanes: lanes 16 apart,
+// then rotations within 16 lanes by 8, 4, 2 and 1: with the halves equal,
+// each is the exchange of lanes that far apart.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ int dpp_i32(int v) {
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+constexpr int kRor = 0x120;  // row_ror
+__device__ __forceinline__ void swap16(float v, float *a, float *b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    *a = __uint_as_float(r[0]);
+    *b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap32(float v, float *a, float *b) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    *a = __uint_as_float(r[0]);
+    *b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float max32(float v) {
+    float a, b;
+    swap16(v, &a, &b);
+    v = fmaxf(a, b);
+    v = fmaxf(v, dpp_f32<kRor + 8>(v));
+    v = fmaxf(v, dpp_f32<kRor + 4>(v));
+    v = fmaxf(v, dpp_f32<kRor + 2>(v));
+    return fmaxf(v, dpp_f32<kRor + 1>(v));
+}
+__device__ __forceinline__ float sum32(float v) {
+    float a, b;
+    swap16(v, &a, &b);
+    v = a + b;
+    v += dpp_f32<kRor + 8>(v);
+    v += dpp_f32<kRor + 4>(v);
+    v += dpp_f32<kRor + 2>(v);
+    return v + dpp_f32<kRor + 1>(v);
+}
+__device__ __forceinline__ int sum16(int v) {
+    v += dpp_i32<kRor + 8>(v);
+    v += dpp_i32<kRor + 4>(v);
+    v += dpp_i32<kRor + 2>(v);
+    return v + dpp_i32<kRor + 1>(v);
+}
+// Sum of the lanes up to and with this one.
+__device__ __forceinline__ int scan64(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15, 31
+    return v + __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+}
+
 // Writes the finished values of rows row0 .. row0 + n - 1 of a head from LDS:
 // out, and the next projection's input as sv_quantize_act_q8 makes it of out
 // (a half wave per 32 values, the same reductions in the same order).
 __device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals, int ld, int b, int head, int row0,
                                             int n) {
-    const int nb = a.kv.dim / 32, lane = threadIdx.x & 31;
-    for (int it = threadIdx.x >> 5; it < n * nb; it += blockDim.x >> 5) {
+    const int tid = fresh(threadIdx.x);
+    const int nb = a.kv.dim / 32, lane = tid & 31;
+    for (int it = tid >> 5; it < n * nb; it += blockDim.x >> 5) {
         const int i = it / nb, blk = it % nb, r = row0 + i;
-        const int hq = head * a.group + r % a.group;
-        const int64_t row = (static_cast<int64_t>(b) * a.bt.M + r / a.group) * a.q_heads + hq;
+        const int m = a.by_group(r), hq = head * a.group + r - m * a.group;
+        const int64_t row = (static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq;
         const float x = vals[i * ld + 32 * blk + lane];
         const int64_t e = row * a.kv.dim + 32 * blk + lane;
         if (a.out) gst(a.out + e, x);
         if (a.ep.mode == SV_EP_NONE) continue;
         const float y = a.ep.gamma ? x * gld(a.ep.gamma + hq * a.kv.dim + 32 * blk + lane) : x;
-        float m = fabsf(y);
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, 32));
-        const float d = m / 127.0f, id = d != 0.0f ? 1.0f / d : 0.0f;
+        const float d = max32(fabsf(y)) / 127.0f, id = d != 0.0f ? 1.0f / d : 0.0f;
         const int q = static_cast<int>(fminf(fmaxf(roundf(y * id), -127.0f), 127.0f));
-        int s = q;
-#pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) s += __shfl_xor(s, o, 32);
-        float sq = x * x;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) sq += __shfl_xor(sq, o, 32);
+        const int s = sum16(q);
+        const float sq = sum32(x * x);
         gst(a.ep.q + e, static_cast<int8_t>(q));
         if ((lane & 15) == 0) gst(a.ep.s16 + e / 16, s);
         if (lane == 0) {
@@ -95,10 +172,12 @@ __device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals
 }
 
 // Row tiles of 16 that one wave holds, by the rows of a head.
-inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+constexpr int kMaxLds = 144 * 1024;
 
-int attn_launch_f16(const AttnArgs &a, int rt, dim3 grid, hipStream_t st);
-int attn_launch_bf16(const AttnArgs &a, int rt, dim3 grid, hipStream_t st);
-int attn_launch_i8(const AttnArgs &a, int rt, dim3 grid, hipStream_t st);
+inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 || dim > 64 ? 2 : 4; }
+
+int attn_launch_f16(const AttnArgs &a, int rt, int64_t units, hipStream_t st);
+int attn_launch_bf16(const AttnArgs &a, int rt, int64_t units, hipStream_t st);
+int attn_launch_i8(const AttnArgs &a, int rt, int64_t units, hipStream_t st);
 
 }  // namespace sv

@@ -19,10 +19,10 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
     const int r = blockIdx.x, head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
-    const Span sp = span_of(a, b, sid);
+    const Span sp = span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), kv_rows_of(a.bt.n_new, b, a.bt.M));
     if (r >= sp.n * a.group) return;
     const int D = a.kv.dim, quads = D / 4, parts = kJoin / quads;
-    const int n = min(a.chunks, sp.first + max(sp.end - sp.jump, 0));  // chunks in use
+    const int n = chunks_of(a, sp);
     const int64_t base = (static_cast<int64_t>(b) * a.kv.heads + head) * a.chunks * a.rows + r;
     float top = -INFINITY;
     for (int c = tid; c < n; c += kJoin) top = fmaxf(top, gld(a.part_m + base + static_cast<int64_t>(c) * a.rows));
@@ -82,12 +82,11 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
     finish_rows(a, s_v, D, b, head, r, 1);
 }
 
-// Slots of a chunk: enough chunks to give every compute unit several
-// workgroups at the longest length of the call, but no shorter than a block
-// for each wave, and no longer than makes the parts a small share of what is
-// read.
+// Slots of a chunk: at the longest length of the call a workgroup for every
+// compute unit, but no shorter than a block for each wave, and no longer than
+// makes the parts a small share of what is read.
 static int chunk_rule(int64_t B, int64_t heads, int64_t span) {
-    int64_t c = (span * B * heads / 768 + 127) / 128 * 128;
+    int64_t c = (span * B * heads / 256 + 127) / 128 * 128;
     if (c < 128) c = 128;
     if (c > 4096) c = 4096;
     return static_cast<int>(c);
@@ -104,7 +103,8 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     SV_REQUIRE(at->q_heads >= 1 && at->q_heads % d.heads == 0 && at->q_heads / d.heads <= 64, SV_ERR_SHAPE,
                "kv_attention: q_heads must be a multiple of heads, at most 64 times");
     SV_REQUIRE(at->scale > 0.0f && at->scale <= 3.0e38f, SV_ERR_ARG, "kv_attention: scale must be positive and finite");
-    SV_REQUIRE(at->window >= 0 && at->sinks >= 0, SV_ERR_ARG, "kv_attention: window and sinks must not be negative");
+    SV_REQUIRE(at->window >= 0 && at->sinks >= 0 && at->sinks < (1 << 30), SV_ERR_ARG,
+               "kv_attention: window and sinks must not be negative, sinks below 2^30");
     SV_REQUIRE(at->window > 0 || at->sinks == 0, SV_ERR_ARG, "kv_attention: sinks need a window");
     SV_REQUIRE(at->max_len >= 0, SV_ERR_ARG, "kv_attention: max_len must not be negative");
     SV_REQUIRE(at->chunk >= 0 && at->chunk % 128 == 0 && at->chunk <= (1 << 24), SV_ERR_ARG,
@@ -135,7 +135,11 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     a->scale = at->scale * 1.44269504088896340736f;
     p->rt = attn_tiles_per_wave(d.dim, a->rows);
     a->tiles = (a->rows + 16 * p->rt - 1) / (16 * p->rt);
-    p->units = (static_cast<int64_t>(bt->B) * d.heads * chunks + 7) / 8 * 8;
+    a->by_group = div_by(a->group);
+    a->by_chunk = div_by(a->chunk);
+    a->by_tiles = div_by(a->tiles);
+    a->by_heads = div_by(d.heads);
+    p->units = static_cast<int64_t>(bt->B) * d.heads * chunks;
     SV_REQUIRE(p->units * a->tiles < (1ll << 24), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
     p->bytes = p->o_m = p->o_l = 0;
     if (chunks > 1) {
@@ -199,10 +203,9 @@ extern "C" int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch
         a.part_l = reinterpret_cast<float *>(ws + p.o_l);
     }
     hipStream_t st = as_stream(stream);
-    const dim3 grid(static_cast<unsigned>(p.units * a.tiles));
-    rc = d.type == SV_KV_F16    ? attn_launch_f16(a, p.rt, grid, st)
-         : d.type == SV_KV_BF16 ? attn_launch_bf16(a, p.rt, grid, st)
-                                : attn_launch_i8(a, p.rt, grid, st);
+    rc = d.type == SV_KV_F16    ? attn_launch_f16(a, p.rt, p.units, st)
+         : d.type == SV_KV_BF16 ? attn_launch_bf16(a, p.rt, p.units, st)
+                                : attn_launch_i8(a, p.rt, p.units, st);
     if (rc || a.chunks == 1) return rc;
     hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(kJoin), 0, st, a);
     return hip_check(hipGetLastError(), "kv_attention join launch");

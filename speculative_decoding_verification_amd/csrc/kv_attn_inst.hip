@@ -5,14 +5,14 @@
 //   s_j = q . k_j,  m = max s_j,  l = sum 2^(s_j - m),  o = sum 2^(s_j - m) v_j
 // in one pass over the chunk with a running m, l and o (q is scaled by
 // scale * log2(e) first).  The rows of one key head, M * group of them, are
-// the 16 columns of a tile; a wave takes every fourth block of 32 slots:
+// the 16 columns of a tile; a wave takes every W-th block of 32 slots:
 //   S^T [32 slots x 16 rows] = K Q^T    two 16x16x32 products per 32 of dim
 //   O^T [dim x 16 rows] += V^T P^T      one 16x16x32 product per 16 of dim
 // Row r of the first product's tile t is slot 8 (r / 4) + 4 t + r % 4, so
 // lane group g (lanes 16 g ..) holds the scores of slots 8 g .. 8 g + 7, and
 // these are the eight it supplies to the second product: the weights stay
-// where they are, and keys and values go from the block straight to
-// registers, 16 (int8: 8) contiguous bytes a lane.
+// where they are, and a block's keys and values are the products' operands
+// as they lie, 16 (int8: 8) contiguous bytes a lane.
 //
 // Precision: the fp32 q and weights enter as sums of parts, two for fp16 (q
 // scaled by a power of two per row, the weights by 2^15, so that the second
@@ -21,7 +21,12 @@
 // scale and so have no bounded range, with bf16.
 //
 // Bound by memory: a block of 32 slots is 128 dim bytes (64 dim for int8)
-// and is read once; at 16 rows the products take a tenth of that time.
+// and is read once.  Each wave keeps the next blocks on their way in a ring
+// of its own in LDS, filled by loads that go there directly, so that what is
+// in flight costs no registers; the ring's halves (a block's keys, its
+// values) are refilled as soon as they are in registers.
+#include <atomic>
+
 #include "kv_attn.h"
 
 namespace sv {
@@ -30,6 +35,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef float f4 __attribute__((ext_vector_type(4)));
+#define SV_LDS __attribute__((address_space(3)))
 
 template <int TYPE>
 struct Kind;
@@ -54,8 +60,6 @@ struct Kind<SV_KV_I8> {
 
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-
-constexpr int kWaves = 4;
 
 // x = sum of N parts of the narrow type, each the rounding of what is left.
 template <int N, typename V8>
@@ -87,27 +91,11 @@ __device__ __forceinline__ float times_parts(float w, float y) {
     return sum;
 }
 
-// Raw piece of a block as one lane loads it.
+// Raw piece of a block as one lane holds it.
 template <int ESZ>
 struct Raw {
     uint32_t w[2 * ESZ];
 };
-template <int ESZ>
-__device__ __forceinline__ Raw<ESZ> load_raw(const uint8_t *p) {
-    Raw<ESZ> r;
-    if constexpr (ESZ == 2) {
-        const u32x4 v = *(const SV_GLOBAL u32x4 *)p;
-        r.w[0] = v.x;
-        r.w[1] = v.y;
-        r.w[2] = v.z;
-        r.w[3] = v.w;
-    } else {
-        const u32x2 v = *(const SV_GLOBAL u32x2 *)p;
-        r.w[0] = v.x;
-        r.w[1] = v.y;
-    }
-    return r;
-}
 
 template <typename V8>
 __device__ __forceinline__ V8 widen(const Raw<2> &r) {
@@ -151,95 +139,240 @@ __device__ __forceinline__ uint32_t odd_pair(uint32_t w) {
     return ((w & 0x7FFF7FFFu) + (TYPE == SV_KV_F16 ? 0x04000400u : 0x00800080u)) & 0x80008000u;
 }
 
-// Largest value over the four lanes that share a row (16 and 32 lanes apart).
+// Largest value and sum over the four lanes that share a row (16 and 32 lanes
+// apart).
 __device__ __forceinline__ float row_max(float v) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+    float a, b;
+    swap16(v, &a, &b);
+    swap32(fmaxf(a, b), &a, &b);
+    return fmaxf(a, b);
+}
+__device__ __forceinline__ float row_sum(float v) {
+    float a, b;
+    swap16(v, &a, &b);
+    swap32(a + b, &a, &b);
+    return a + b;
+}
+
+// ------------------------------------------------------------- the ring
+// Pieces of a ring half into registers, behind a wait that leaves the last
+// LEAVE transfers of the wave on their way: the waits are in the same asm
+// block as the reads, so nothing is taken for loaded before it is.
+template <int LEAVE, int STRIDE, int N, int FROM = 0>
+__device__ __forceinline__ void ring_read(uint32_t at, Raw<2> *r) {
+    u32x4 v[8];
+    if constexpr (N >= 8) {
+        asm volatile(
+            "s_waitcnt vmcnt(%17)\n"
+            "ds_read_b128 %0, %8 offset:%9\n ds_read_b128 %1, %8 offset:%10\n"
+            "ds_read_b128 %2, %8 offset:%11\n ds_read_b128 %3, %8 offset:%12\n"
+            "ds_read_b128 %4, %8 offset:%13\n ds_read_b128 %5, %8 offset:%14\n"
+            "ds_read_b128 %6, %8 offset:%15\n ds_read_b128 %7, %8 offset:%16\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+            : "v"(at), "n"(FROM), "n"(FROM + STRIDE), "n"(FROM + 2 * STRIDE), "n"(FROM + 3 * STRIDE),
+              "n"(FROM + 4 * STRIDE), "n"(FROM + 5 * STRIDE), "n"(FROM + 6 * STRIDE), "n"(FROM + 7 * STRIDE), "n"(LEAVE)
+            : "memory");
+    } else if constexpr (N >= 4) {
+        asm volatile(
+            "s_waitcnt vmcnt(%9)\n"
+            "ds_read_b128 %0, %4 offset:%5\n ds_read_b128 %1, %4 offset:%6\n"
+            "ds_read_b128 %2, %4 offset:%7\n ds_read_b128 %3, %4 offset:%8\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+            : "v"(at), "n"(FROM), "n"(FROM + STRIDE), "n"(FROM + 2 * STRIDE), "n"(FROM + 3 * STRIDE), "n"(LEAVE)
+            : "memory");
+    } else {
+        asm volatile(
+            "s_waitcnt vmcnt(%5)\n"
+            "ds_read_b128 %0, %2 offset:%3\n ds_read_b128 %1, %2 offset:%4\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1])
+            : "v"(at), "n"(FROM), "n"(FROM + STRIDE), "n"(LEAVE)
+            : "memory");
+    }
+    constexpr int T = N >= 8 ? 8 : N >= 4 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < T; i++) {
+        r[i].w[0] = v[i].x;
+        r[i].w[1] = v[i].y;
+        r[i].w[2] = v[i].z;
+        r[i].w[3] = v[i].w;
+    }
+    if constexpr (N > T) ring_read<LEAVE, STRIDE, N - T, FROM + T * STRIDE>(at, r + T);
+}
+// int8: pieces of 8 bytes; pairs of them STRIDE apart, the second EVERY past
+// the first (keys: the two slots of a piece's tiles), or EVERY = 0.
+template <int LEAVE, int STRIDE, int EVERY, int N, int FROM = 0>
+__device__ __forceinline__ void ring_read(uint32_t at, Raw<1> *r) {
+    u32x2 v[4];
+    constexpr int O1 = EVERY ? FROM + EVERY : FROM + STRIDE, O2 = EVERY ? FROM + STRIDE : FROM + 2 * STRIDE;
+    constexpr int O3 = EVERY ? O2 + EVERY : FROM + 3 * STRIDE;
+    if constexpr (N >= 4) {
+        asm volatile(
+            "s_waitcnt vmcnt(%9)\n"
+            "ds_read_b64 %0, %4 offset:%5\n ds_read_b64 %1, %4 offset:%6\n"
+            "ds_read_b64 %2, %4 offset:%7\n ds_read_b64 %3, %4 offset:%8\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+            : "v"(at), "n"(FROM), "n"(O1), "n"(O2), "n"(O3), "n"(LEAVE)
+            : "memory");
+    } else {
+        asm volatile(
+            "s_waitcnt vmcnt(%5)\n"
+            "ds_read_b64 %0, %2 offset:%3\n ds_read_b64 %1, %2 offset:%4\n"
+            "s_waitcnt lgkmcnt(0)"
+            : "=&v"(v[0]), "=&v"(v[1])
+            : "v"(at), "n"(FROM), "n"(O1), "n"(LEAVE)
+            : "memory");
+    }
+    constexpr int T = N >= 4 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < T; i++) {
+        r[i].w[0] = v[i].x;
+        r[i].w[1] = v[i].y;
+    }
+    constexpr int NEXT = EVERY ? FROM + T / 2 * STRIDE : FROM + T * STRIDE;
+    if constexpr (N > T) ring_read<LEAVE, STRIDE, EVERY, N - T, NEXT>(at, r + T);
+}
+__device__ __forceinline__ void ring_read_scales(uint32_t at, float (&s)[8]) {
+    u32x4 a, b;
+    asm volatile("ds_read_b128 %0, %2\n ds_read_b128 %1, %2 offset:16\n s_waitcnt lgkmcnt(0)"
+                 : "=&v"(a), "=&v"(b)
+                 : "v"(at)
+                 : "memory");
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        s[e] = __uint_as_float(a[e]);
+        s[4 + e] = __uint_as_float(b[e]);
+    }
+}
+// Transfers global memory to LDS, 16 bytes a lane (lane i to `to` + 16 i).
+// ONCE: no other workgroup of the launch reads it, so it need not stay in
+// the caches (non-temporal).
+template <bool ONCE>
+__device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to) {
+    __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, 0, ONCE ? 2 : 0);
 }
 
 template <int TYPE, int D, int RT>
-struct Lds {
-    // queries as operands, [tile][dim / 32][part][lane][16 bytes], and behind
-    // them the fp32 rows they are made of; after the blocks the waves' sums,
-    // two waves at a time
-    static constexpr int q_bytes = RT * (D / 32) * Kind<TYPE>::kq * 1024;
-    static constexpr int ld = D + 4;
-    static constexpr int row_bytes = 16 * RT * ld * 4;
-    static constexpr int bytes = q_bytes > row_bytes ? q_bytes + row_bytes : 2 * row_bytes;
+struct Shape {
+    using Kd = Kind<TYPE>;
+    static constexpr int W = TYPE == SV_KV_I8 ? 8 : 4;          // waves
+    static constexpr int HALF = 32 * D * Kd::esz;               // bytes of a block's keys, or values
+    static constexpr int LOADS = HALF / 1024;                   // transfers of a half
+    static constexpr int SCALES = TYPE == SV_KV_I8 ? 1 : 0;     // and one of both scales with the keys
+    // halves of a wave's ring: 32 KB (int8: 16 KB, the workgroup has twice
+    // the waves), and at least a block
+    static constexpr int RING = TYPE == SV_KV_I8 ? 16384 : 32768;
+    static constexpr int FIT = RING / HALF / 2 * 2;
+    static constexpr int N = FIT < 2 ? 2 : FIT > 8 ? 8 : FIT;
+    static constexpr int RING_BYTES = N * HALF + N / 2 * 256 * SCALES;
+    // transfers that may still be on their way when the oldest half is read:
+    // those of the halves after it
+    static constexpr int LEAVE_K = (N / 2 - 1) * (LOADS + SCALES) + N / 2 * LOADS;
+    static constexpr int LEAVE_V = N / 2 * (LOADS + SCALES) + (N / 2 - 1) * LOADS;
+    static_assert(LEAVE_K < 64 && LEAVE_V < 64, "the wait counter has six bits");
+    static constexpr int ROWS = 16 * RT, LD = D + 4;
+    static constexpr int SUMS = W * ROWS * LD * 4;              // the waves' sums, after the blocks
+    static constexpr int LDS = W * RING_BYTES > SUMS ? W * RING_BYTES : SUMS;
 };
 
-// The rows' queries, rotated and scaled, as fp32 in LDS: the workgroup's
-// threads take four elements each, and every load of an element is issued
-// before any is used.
-template <int D, int ROWS, int MODE>
-__device__ __forceinline__ void stage_rows(const AttnArgs &a, const Span &sp, int b, int head, int row0, int rows,
-                                           const int *depth, float *to) {
-    constexpr int LD = D + 4, QUADS = D / 4;
-#pragma unroll 4
-    for (int it = threadIdx.x; it < ROWS * QUADS; it += 64 * kWaves) {
-        const int i = it / QUADS, d = it % QUADS * 4;
-        const int r = row0 + i;
-        const bool live = r < rows;
-        const int m = live ? r / a.group : 0;
-        const int hq = head * a.group + (live ? r % a.group : 0);
-        const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
-        const uint4 u = gld16(qp + d);
-        float x[4] = {__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w)};
-        if constexpr (MODE != SV_ROPE_NONE) {
-            const int half = a.rope.rot / 2;
-            const int64_t pos = min(sp.len + depth[m], static_cast<int64_t>(a.rope.n_pos - 1));
-            const float *cs = a.rope.table + pos * half * 2;
-            if constexpr (MODE == SV_ROPE_PAIRS) {
+// The queries of a row tile as the second operand of S^T = K Q^T: rotated,
+// scaled, and for fp16 multiplied by the power of two that brings the row's
+// largest magnitude into [2^12, 2^13); the row's scores are multiplied by
+// the returned power of two to undo that.  Every wave makes its own.
+template <int TYPE, int D>
+__device__ __forceinline__ float make_queries(const AttnArgs &a, int len, int b, int head, int row0, int rows,
+                                              typename Kind<TYPE>::KVec (&qf)[D / 32][Kind<TYPE>::kq]) {
+    using Kd = Kind<TYPE>;
+    constexpr int NC = D / 32;
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    const int r = row0 + (lane & 15);
+    const bool live = r < rows;
+    const int m = live ? a.by_group(r) : 0, hq = head * a.group + (live ? r - m * a.group : 0);
+    const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
+    const int rot = a.rope.mode == SV_ROPE_NONE ? 0 : a.rope.rot, half = rot / 2;
+    const bool pairs = a.rope.mode == SV_ROPE_PAIRS;
+    const float *cs = a.rope.table;
+    if (rot) {
+        const int depth = a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
+        cs += static_cast<int64_t>(min(len + depth, a.rope.n_pos - 1)) * rot;
+    }
+    float x[NC][8];
+    if (rot % 16 == 0) {
+        // whole pieces of eight are rotated alike: all loads first
+        f4 own[NC][2], other[NC][2], w[NC][4];
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const bool turn = d + e < a.rope.rot;
-                    const uint2 w = gld8(cs + (turn ? d + e : 0));
-                    const float co = __uint_as_float(w.x), si = __uint_as_float(w.y), x0 = x[e], x1 = x[e + 1];
-                    if (turn) {
-                        x[e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
-                        x[e + 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
-                    }
+        for (int c = 0; c < NC; c++) {
+            const int d = 32 * c + 8 * g;
+            const bool turn = d < rot, second = d >= half;
+            own[c][0] = gld(reinterpret_cast<const f4 *>(qp + d));
+            own[c][1] = gld(reinterpret_cast<const f4 *>(qp + d + 4));
+            if (!rot) continue;
+            if (pairs) {
+                const float *p = cs + (turn ? d : 0);
+                w[c][0] = gld(reinterpret_cast<const f4 *>(p));
+                w[c][1] = gld(reinterpret_cast<const f4 *>(p + 4));
+            } else {
+                const int i = !turn ? 0 : second ? d - half : d;
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[c][e] = gld(reinterpret_cast<const f4 *>(cs + 2 * i + 4 * e));
+                const float *p = qp + (second ? i : i + half);
+                other[c][0] = gld(reinterpret_cast<const f4 *>(p));
+                other[c][1] = gld(reinterpret_cast<const f4 *>(p + 4));
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NC; c++) {
+            const int d = 32 * c + 8 * g;
+            const bool turn = d < rot, second = d >= half;
+#pragma unroll
+            for (int e = 0; e < 8; e++) x[c][e] = own[c][e >> 2][e & 3];
+            if (!rot) continue;
+            if (pairs) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    const float co = w[c][e >> 2][e & 3], si = w[c][e >> 2][(e & 3) + 1], x0 = x[c][e], x1 = x[c][e + 1];
+                    const float y0 = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
+                    const float y1 = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
+                    x[c][e] = turn ? y0 : x0;
+                    x[c][e + 1] = turn ? y1 : x1;
                 }
             } else {
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const bool turn = d + e < a.rope.rot, second = d + e >= half;
-                    const int p = !turn ? 0 : second ? d + e - half : d + e;
-                    const uint2 w = gld8(cs + 2 * p);
-                    const float other = gld(qp + (!turn ? 0 : second ? p : p + half));
-                    const float own = __fmul_rn(x[e], __uint_as_float(w.x));
-                    const float by = __fmul_rn(other, __uint_as_float(w.y));
-                    if (turn) x[e] = second ? __fadd_rn(own, by) : __fsub_rn(own, by);
+                for (int e = 0; e < 8; e++) {
+                    const float u = __fmul_rn(x[c][e], w[c][e >> 1][2 * (e & 1)]);
+                    const float v = __fmul_rn(other[c][e >> 2][e & 3], w[c][e >> 1][2 * (e & 1) + 1]);
+                    const float y = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
+                    x[c][e] = turn ? y : x[c][e];
                 }
             }
         }
-        typedef float f4 __attribute__((ext_vector_type(4)));
-        f4 z;
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; e++) z[e] = live ? x[e] * a.scale : 0.0f;
-        *reinterpret_cast<f4 *>(to + i * LD + d) = z;
+        for (int c = 0; c < NC; c++)
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int d = 32 * c + 8 * g + e;
+                float y = gld(qp + d);
+                if (d < rot) {
+                    const bool second = pairs ? d & 1 : d >= half;
+                    const int i = pairs ? d >> 1 : second ? d - half : d;
+                    const int mate = pairs ? d ^ 1 : second ? i : i + half;
+                    const float u = __fmul_rn(y, gld(cs + 2 * i)), v = __fmul_rn(gld(qp + mate), gld(cs + 2 * i + 1));
+                    y = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
+                }
+                x[c][e] = y;
+            }
     }
-}
-
-// The queries of a row tile as the second operand of S^T = K Q^T (one wave),
-// for fp16 multiplied by the power of two that brings the row's largest
-// magnitude into [2^12, 2^13); rs is what the row's scores are multiplied by
-// to undo that.
-template <int TYPE, int D>
-__device__ __forceinline__ void put_queries(const float *from, uint8_t *to, float *rs) {
-    using Kd = Kind<TYPE>;
-    constexpr int NC = D / 32, LD = D + 4;
-    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    float xq[NC][8];
     float top = 0.0f;
 #pragma unroll
-    for (int cc = 0; cc < NC; cc++)
+    for (int c = 0; c < NC; c++)
 #pragma unroll
         for (int e = 0; e < 8; e++) {
-            xq[cc][e] = from[col * LD + 32 * cc + 8 * g + e];
-            top = fmaxf(top, fabsf(xq[cc][e]));
+            x[c][e] = live ? x[c][e] * a.scale : 0.0f;
+            top = fmaxf(top, fabsf(x[c][e]));
         }
     float back = 1.0f;
     if constexpr (__is_same(typename Kd::KVec, h8)) {
@@ -249,151 +382,188 @@ __device__ __forceinline__ void put_queries(const float *from, uint8_t *to, floa
         const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll
-        for (int cc = 0; cc < NC; cc++)
+        for (int c = 0; c < NC; c++)
 #pragma unroll
-            for (int e = 0; e < 8; e++) xq[cc][e] *= by;
+            for (int e = 0; e < 8; e++) x[c][e] *= by;
     }
-    if (g == 0) rs[col] = back;
 #pragma unroll
-    for (int cc = 0; cc < NC; cc++) {
-        typename Kd::KVec part[Kd::kq];
-        split8<Kd::kq>(xq[cc], part);
-#pragma unroll
-        for (int n = 0; n < Kd::kq; n++)
-            *reinterpret_cast<typename Kd::KVec *>(to + ((cc * Kd::kq + n) * 64 + lane) * 16) = part[n];
-    }
+    for (int c = 0; c < NC; c++) split8<Kd::kq>(x[c], qf[c]);
+    return back;
 }
 
-// Two waves a SIMD cover each other's waits where the registers allow it.
-template <int TYPE, int D, int RT>
-constexpr int min_waves() {
-    return RT * D <= 256 && (TYPE == SV_KV_I8 || D <= 192) ? 2 : 1;
+// The sequence whose chunk (counted over the sequences, once per head) has
+// number u, and the chunks ahead of it; -1 past the last.  B lengths are
+// read by the lanes, so that no workgroup is spent on a chunk that the
+// longest sequence has and another has not.
+__device__ __forceinline__ int find_chunk(const AttnArgs &a, int u, int *before) {
+    const int lane = threadIdx.x & 63;
+    int passed = 0;
+    for (int b0 = 0; b0 < a.bt.B; b0 += 64) {
+        const int b = b0 + lane;
+        int own = 0;
+        if (b < a.bt.B) {
+            const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
+            if (sid >= 0 && sid < a.kv.seqs) {
+                const int n = kv_rows_of(a.bt.n_new, b, a.bt.M);
+                if (n) own = chunks_of(a, span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), n)) * a.kv.heads;
+            }
+        }
+        const int upto = scan64(own), all = __builtin_amdgcn_readlane(upto, 63);
+        if (passed + all > u) {
+            const int at = __ffsll(__ballot(passed + upto > u)) - 1;
+            *before = passed + __builtin_amdgcn_readlane(upto - own, at);
+            return b0 + at;
+        }
+        passed += all;
+    }
+    return -1;
 }
 
 template <int TYPE, int D, int RT>
-__global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_attn_kernel(AttnArgs a) {
+__global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kernel(AttnArgs a) {
     using Kd = Kind<TYPE>;
-    using L = Lds<TYPE, D, RT>;
-    constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz;
-    constexpr int LD = L::ld;
-    constexpr int ROWS = 16 * RT;
-    __shared__ __align__(16) uint8_t s_mem[L::bytes];
-    __shared__ float s_m[kWaves][ROWS], s_l[kWaves][ROWS], s_rs[ROWS];
-    __shared__ uint32_t s_mask[SV_MAX_M];  // the new rows that a row sees, and how many come before it
-    __shared__ int s_depth[SV_MAX_M];
-    float *s_o = reinterpret_cast<float *>(s_mem);  // [2][ROWS][LD]
-
+    using S = Shape<TYPE, D, RT>;
+    constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz, W = S::W, LD = S::LD, ROWS = S::ROWS;
+    constexpr bool ONCE = D <= 128 && RT < 4;  // one row group
+    extern __shared__ __align__(1024) uint8_t s_mem[];
+    __shared__ float s_m[W][ROWS], s_l[W][ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col = lane & 15, g = lane >> 4;
-    // Row groups of one (sequence, head, chunk) read the same blocks: eight
-    // workgroups apart, so that the same XCD takes them and its L2 serves
-    // the second reading.
-    const int x = blockIdx.x;
-    const int tile = x / 8 % a.tiles, unit = x / 8 / a.tiles * 8 + x % 8;
     const int heads = a.kv.heads;
-    const int c = unit % a.chunks, bh = unit / a.chunks;
-    const int head = bh % heads, b = bh / heads;
+    // Row groups of one chunk read the same blocks: eight workgroups apart,
+    // so that the same XCD takes them and its L2 serves the second reading.
+    const int x = blockIdx.x;
+    const int u8 = a.by_tiles(x / 8), tile = x / 8 - u8 * a.tiles, u = u8 * 8 + x % 8;
+    const bool alone = a.chunks == 1;  // no join: this workgroup finishes the rows
+    int b, head, c;
+    if (alone) {
+        b = a.by_heads(u);
+        head = u - b * heads;
+        c = 0;
+    } else {
+        int before = 0;
+        b = find_chunk(a, u, &before);
+        if (b < 0) return;
+        head = u - before;  // for now: the sequence's chunk, over its heads
+        c = -1;
+    }
     if (b >= a.bt.B) return;
     const int sid = a.bt.seq ? __builtin_amdgcn_readfirstlane(gld(a.bt.seq + b)) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
-    const Span sp = span_of(a, b, sid);
-    const int ac = chunk_of(sp, c);
-    const bool alone = a.chunks == 1;  // no join: this workgroup finishes the rows
-    if (ac >= sp.end && !alone) return;
-    const int row0 = tile * ROWS;
-    const int rows = sp.n * a.group;  // of this sequence, in use
+    const int len = __builtin_amdgcn_readfirstlane(static_cast<int>(kv_len_of(a.kv, sid)));
+    const Span sp = span_of(a, len, __builtin_amdgcn_readfirstlane(kv_rows_of(a.bt.n_new, b, a.bt.M)));
+    if (c < 0) {
+        const int n_chunks = chunks_of(a, sp);
+        const int h = head / n_chunks;
+        c = head - h * n_chunks;
+        head = h;
+    }
+    const int row0 = tile * ROWS, rows = sp.n * a.group;  // of this sequence, in use
     if (row0 >= rows) return;
 
-    // ---- the wave's blocks: every fourth one of the chunk, but for those
+    // ---- the wave's blocks: every W-th one of the chunk, but for those
     // between the sinks and every row's window
-    const int per = a.chunk / kBlk;
-    const int last = static_cast<int>(min(static_cast<int64_t>(ac + 1) * per, (sp.total + kBlk - 1) / kBlk));
-    const int gap0 = (a.sinks + kBlk - 1) / kBlk, gap1 = static_cast<int>(sp.lo / kBlk);
-    const int begin = ac * per + wave;
+    const int per = a.chunk / kBlk, ac = chunk_of(sp, c);
+    const int last = min((ac + 1) * per, (sp.total + kBlk - 1) / kBlk);
+    const int gap0 = (a.sinks + kBlk - 1) / kBlk, gap1 = sp.lo / kBlk;
     auto settle = [&](int j) {  // j, or the next of the wave's blocks past the gap
-        return j >= gap0 && j < gap1 ? j + (gap1 - j + kWaves - 1) / kWaves * kWaves : j;
+        return j >= gap0 && j < gap1 ? j + (gap1 - j + W - 1) / W * W : j;
     };
+    // The page of a block, by a scalar load (a vector load would be counted
+    // behind the ring's transfers, and waiting for it would drain them).
     auto page_of = [&](int j) {
-        return j < last ? __builtin_amdgcn_readfirstlane(kv_page_of(a.kv, sid, j >> a.kv.blk_shift)) : -1;
+        const int e = j >> a.kv.blk_shift;
+        if (j >= last || e >= a.kv.width) return -1;
+        const int p = *(const __attribute__((address_space(4))) int32_t *)(reinterpret_cast<uintptr_t>(
+            a.kv.table + static_cast<int64_t>(sid) * a.kv.width + e));
+        return p >= 0 && p < a.kv.n_pages ? p : -1;
     };
     // a block without a page is read from page 0 and masked
     auto block_at = [&](int j, int page) {
         return kv_block(a.kv, a.layer, max(page, 0), head, j & ((1 << a.kv.blk_shift) - 1));
     };
-    Raw<ESZ> kr[NC][2], vr[ND];
-    float ks[8], vs[8];  // int8: the scales of the lane group's eight slots
-    const uint32_t k_at = (g * 32 + 8 * (col >> 2) + (col & 3)) * 8 * ESZ;
-    const uint32_t v_at = (32 * D + (g * D + col) * 8) * ESZ;
-    auto load_k = [&](const uint8_t *blk) {
-#pragma unroll
-        for (int cc = 0; cc < NC; cc++)
-#pragma unroll
-            for (int u = 0; u < 2; u++) kr[cc][u] = load_raw<ESZ>(blk + k_at + (cc * 128 + 4 * u) * 8 * ESZ);
-        if constexpr (TYPE == SV_KV_I8) {
-            const uint8_t *sc = blk + 64 * D + 32 * g;
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const uint4 w = gld16(sc + 4 * e);
-                ks[e] = __uint_as_float(w.x);
-                ks[e + 1] = __uint_as_float(w.y);
-                ks[e + 2] = __uint_as_float(w.z);
-                ks[e + 3] = __uint_as_float(w.w);
-            }
-        }
-    };
-    auto load_v = [&](const uint8_t *blk) {
-        if constexpr (TYPE == SV_KV_I8) {
-            const uint8_t *sc = blk + 64 * D + 128 + 32 * g;
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const uint4 w = gld16(sc + 4 * e);
-                vs[e] = __uint_as_float(w.x);
-                vs[e + 1] = __uint_as_float(w.y);
-                vs[e + 2] = __uint_as_float(w.z);
-                vs[e + 3] = __uint_as_float(w.w);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < ND; i++) vr[i] = load_raw<ESZ>(blk + v_at + i * 128 * ESZ);
-    };
-
-    int j = settle(begin);
+    int j = settle(ac * per + wave);
+    const bool any = j < last;
     int page = page_of(j);
-    const uint8_t *blk = block_at(j, page);
-    int jn = settle(j + kWaves);
-    int page_n = page_of(jn);
-    if (j < last) {
-        load_k(blk);
-        load_v(blk);
+
+    // ---- queries
+    typename Kd::KVec qf[RT][NC][Kd::kq];
+    float rs[RT];
+#pragma unroll
+    for (int t = 0; t < RT; t++)
+    {
+        rs[t] = make_queries<TYPE, D>(a, len, b, head, row0 + 16 * t, rows, qf[t]);
+        __builtin_amdgcn_sched_barrier(0);  // a tile's loads take many registers: one tile at a time
     }
-    if (threadIdx.x < SV_MAX_M) {
-        const uint32_t mask = static_cast<int>(threadIdx.x) < sp.n ? row_mask(a, b, threadIdx.x) : 0u;
-        s_mask[threadIdx.x] = mask;
-        s_depth[threadIdx.x] = __popc(mask & ((1u << threadIdx.x) - 1));
+
+    // ---- the ring: `slot` is the half read next and, once it is in
+    // registers, the half that is refilled
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS uint8_t *)s_mem)) + wave * S::RING_BYTES;
+    uint32_t slot = 0;  // 0 .. N - 1
+    int ji = j, jin = settle(j + W), pin = page_of(jin);  // block to be requested, the one after it, its page
+    const uint8_t *bi = block_at(ji, page);
+    auto advance = [&]() {
+        if (jin < last) {  // past the end the last block is requested again, so that the counts hold
+            ji = jin;
+            bi = block_at(ji, pin);
+            jin = settle(jin + W);
+            pin = page_of(jin);
+        }
+    };
+    // fp16, bf16: lane by lane what the lane will read; int8: as it lies
+    const uint32_t k_from = ESZ == 2 ? (g * 32 + 8 * (col >> 2) + (col & 3)) * 16 : lane * 16;
+    const uint32_t v_from = ESZ == 2 ? (g * D + col) * 16 : lane * 16;
+    auto request_k = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::LOADS; i++)
+            to_lds<ONCE>(bi + k_from + (ESZ == 2 ? (i >> 1) * 2048 + (i & 1) * 64 : i * 1024), ring + slot * S::HALF + i * 1024);
+        if constexpr (S::SCALES) {
+            if (lane < 16) to_lds<ONCE>(bi + 64 * D + lane * 16, ring + S::N * S::HALF + (slot >> 1) * 256);
+        }
+    };
+    auto request_v = [&]() {
+#pragma unroll
+        for (int i = 0; i < S::LOADS; i++)
+            to_lds<ONCE>(bi + S::HALF + v_from + (ESZ == 2 ? i * 256 : i * 1024), ring + slot * S::HALF + i * 1024);
+        advance();
+    };
+    auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
+    if (any) {
+#pragma unroll 1
+        for (int i = 0; i < S::N / 2; i++) {
+            request_k();
+            turn();
+            request_v();
+            turn();
+        }
     }
-    __syncthreads();
-    float *staged = reinterpret_cast<float *>(s_mem + L::q_bytes);
-    if (a.rope.mode == SV_ROPE_NONE) stage_rows<D, ROWS, SV_ROPE_NONE>(a, sp, b, head, row0, rows, s_depth, staged);
-    else if (a.rope.mode == SV_ROPE_PAIRS) stage_rows<D, ROWS, SV_ROPE_PAIRS>(a, sp, b, head, row0, rows, s_depth, staged);
-    else stage_rows<D, ROWS, SV_ROPE_HALVES>(a, sp, b, head, row0, rows, s_depth, staged);
-    __syncthreads();
-    if (wave < RT) put_queries<TYPE, D>(staged + 16 * wave * LD, s_mem + wave * (L::q_bytes / RT), s_rs + 16 * wave);
-    __syncthreads();
 
     f4 o[RT][ND];
-    float mx[RT], l[RT], rs[RT];
+    float mx[RT], l[RT];
 #pragma unroll
     for (int t = 0; t < RT; t++) {
         mx[t] = -INFINITY;
         l[t] = 0.0f;
-        rs[t] = s_rs[16 * t + col];
 #pragma unroll
         for (int i = 0; i < ND; i++) o[t][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    const int64_t whole = sp.len + sp.n - a.window;  // with a window: from here on every row's window has begun
+    const int whole = sp.len + sp.n - a.window;  // with a window: from here on every row's window has begun
     while (j < last) {
-        const int64_t s0 = static_cast<int64_t>(j) * kBlk;
-        // ---- scores, and the next block's keys on their way
+        const int s0 = j * kBlk;
+        const int jn = settle(j + W), page_n = page_of(jn);
+        // ---- scores
+        Raw<ESZ> kr[2 * NC], vr[ND];
+        float ks[8], vs[8];  // int8: the scales of the lane group's eight slots
+        if constexpr (ESZ == 2) {
+            ring_read<S::LEAVE_K, 1024, 2 * NC>(ring + slot * S::HALF + lane * 16, kr);
+        } else {
+            ring_read<S::LEAVE_K, 1024, 32, 2 * NC>(
+                ring + slot * S::HALF + (g * 32 + 8 * (col >> 2) + (col & 3)) * 8, kr);
+            ring_read_scales(ring + S::N * S::HALF + (slot >> 1) * 256 + 32 * g, ks);
+            ring_read_scales(ring + S::N * S::HALF + (slot >> 1) * 256 + 128 + 32 * g, vs);
+        }
+        request_k();
+        turn();
         float p[RT][8];
         {
             f4 acc[RT][2];
@@ -401,16 +571,14 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
             for (int t = 0; t < RT; t++) acc[t][0] = acc[t][1] = f4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int cc = 0; cc < NC; cc++) {
-                const typename Kd::KVec k0 = widen<typename Kd::KVec>(kr[cc][0]);
-                const typename Kd::KVec k1 = widen<typename Kd::KVec>(kr[cc][1]);
+                const typename Kd::KVec k0 = widen<typename Kd::KVec>(kr[2 * cc]);
+                const typename Kd::KVec k1 = widen<typename Kd::KVec>(kr[2 * cc + 1]);
 #pragma unroll
                 for (int n = Kd::kq - 1; n >= 0; n--)
 #pragma unroll
                     for (int t = 0; t < RT; t++) {
-                        const typename Kd::KVec q = *reinterpret_cast<const typename Kd::KVec *>(
-                            s_mem + t * (L::q_bytes / RT) + ((cc * Kd::kq + n) * 64 + lane) * 16);
-                        acc[t][0] = mma(k0, q, acc[t][0]);
-                        acc[t][1] = mma(k1, q, acc[t][1]);
+                        acc[t][0] = mma(k0, qf[t][cc][n], acc[t][0]);
+                        acc[t][1] = mma(k1, qf[t][cc][n], acc[t][1]);
                     }
             }
 #pragma unroll
@@ -421,12 +589,6 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
                     if constexpr (TYPE == SV_KV_I8) p[t][e] *= ks[e];
                 }
         }
-        const uint8_t *blk_n = block_at(jn, page_n);
-        __builtin_amdgcn_sched_barrier(0);
-        if (jn < last) load_k(blk_n);
-        const int jnn = settle(jn + kWaves);
-        const int page_nn = page_of(jnn);
-        __builtin_amdgcn_sched_barrier(0);
 
         // ---- what is visible, and the running softmax
         const bool edge = page < 0 || s0 + kBlk > sp.len || (a.window && s0 < whole && s0 + kBlk > a.sinks);
@@ -436,28 +598,31 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
 #pragma unroll
         for (int t = 0; t < RT; t++) seen[t] = 0xFFu;
         if (edge) {
+            // the rows' numbers are formed here, not kept in registers while
+            // whole blocks go by
+            const int at_lane = fresh(lane), to_g = at_lane >> 4, from = row0 + (at_lane & 15);
 #pragma unroll
             for (int t = 0; t < RT; t++) {
-                const int r = row0 + 16 * t + col;
+                const int r = from + 16 * t;
                 const bool live = r < rows;
-                const int m = live ? r / a.group : 0;
-                const uint32_t mask = s_mask[m];
-                const int64_t pos = sp.len + s_depth[m];
+                const int m = live ? a.by_group(r) : 0;
+                const uint32_t mask = row_mask(a, b, m);
+                const int pos = sp.len + __popc(mask & ((1u << m) - 1));
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    const int64_t slot = s0 + 8 * g + e;
-                    const int nth = static_cast<int>(slot - sp.len);
-                    bool sees = page >= 0 && slot < sp.total && (nth < 0 || (nth < sp.n && (mask >> nth & 1u)));
+                    const int slot_e = s0 + 8 * to_g + e, nth = slot_e - sp.len;
+                    bool sees = page >= 0 && slot_e < sp.total && (nth < 0 || (nth < sp.n && (mask >> nth & 1u)));
                     if (a.window && sees) {
-                        const int64_t kpos = nth < 0 ? slot : sp.len + s_depth[nth];
+                        int kpos = slot_e;
+                        if (nth > 0 && a.bt.tree) kpos = sp.len + __popc(row_mask(a, b, nth) & ((1u << nth) - 1));
                         sees = pos - kpos < a.window || kpos < a.sinks;
                     }
                     if (!sees) {
                         p[t][e] = -INFINITY;
                         seen[t] &= ~(1u << e);
                     }
-                    const uint32_t by = static_cast<uint32_t>(__ballot(live && sees) >> (16 * g)) & 0xFFFFu;
-                    const uint32_t of = static_cast<uint32_t>(__ballot(live) >> (16 * g)) & 0xFFFFu;
+                    const uint32_t by = static_cast<uint32_t>(__ballot(live && sees) >> (16 * to_g)) & 0xFFFFu;
+                    const uint32_t of = static_cast<uint32_t>(__ballot(live) >> (16 * to_g)) & 0xFFFFu;
                     if (by) any_sees |= 1u << e;
                     if (by != of) all_see &= ~(1u << e);
                 }
@@ -492,6 +657,14 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
         }
 
         // ---- o += V^T P^T
+        const uint8_t *blk = block_at(j, page);
+        if constexpr (ESZ == 2) {
+            ring_read<S::LEAVE_V, 1024, ND>(ring + slot * S::HALF + lane * 16, vr);
+        } else {
+            ring_read<S::LEAVE_V, 128, 0, ND>(ring + slot * S::HALF + (g * D + col) * 8, vr);
+        }
+        request_v();
+        turn();
         bool odd = false;
         if constexpr (TYPE != SV_KV_I8) {
             if (edge) {
@@ -541,17 +714,18 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
         }
         if constexpr (TYPE != SV_KV_I8) {
             if (odd) {
+                const int at_lane = fresh(lane), to_col = at_lane & 15, to_g = at_lane >> 4;
 #pragma unroll 1
                 for (int s = 0; s < kBlk; s++) {
-                    const uint8_t *v = blk + (32 * D + ((s >> 3) * D + 4 * g) * 8 + (s & 7)) * ESZ;
+                    const uint8_t *v = blk + (32 * D + ((s >> 3) * D + 4 * to_g) * 8 + (s & 7)) * ESZ;
 #pragma unroll
                     for (int t = 0; t < RT; t++) {
                         float w = p[t][0];
 #pragma unroll
                         for (int e = 1; e < 8; e++) w = (s & 7) == e ? p[t][e] : w;
-                        const int from = 16 * (s >> 3) + col;
-                        w = __shfl(w, from, 64);
-                        const bool sees = __shfl(seen[t], from, 64) >> (s & 7) & 1u;
+                        const int from = 16 * (s >> 3) + to_col;
+                        w = __uint_as_float(__builtin_amdgcn_ds_bpermute(4 * from, __float_as_uint(w)));
+                        const bool sees = __builtin_amdgcn_ds_bpermute(4 * from, seen[t]) >> (s & 7) & 1;
 #pragma unroll
                         for (int i = 0; i < ND; i++)
 #pragma unroll
@@ -565,66 +739,47 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
                 }
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (jn < last) load_v(blk_n);
         j = jn;
         page = page_n;
-        blk = blk_n;
-        jn = jnn;
-        page_n = page_nn;
     }
+    // the last requests land before the ring's memory is used again
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-    // ---- the waves' results joined: (0 + 2) + (1 + 3)
+    // ---- the waves' results joined, wave by wave
+    float *s_o = reinterpret_cast<float *>(s_mem);  // [W][ROWS][LD]
+    __syncthreads();
 #pragma unroll
     for (int t = 0; t < RT; t++) {
-        l[t] += __shfl_xor(l[t], 16, 64);
-        l[t] += __shfl_xor(l[t], 32, 64);
+        l[t] = row_sum(l[t]);
         if (g == 0) {
             s_m[wave][16 * t + col] = mx[t];
             s_l[wave][16 * t + col] = l[t];
         }
-    }
-    __syncthreads();  // the queries are no longer read
 #pragma unroll
-    for (int t = 0; t < RT; t++) {
-        float top = s_m[0][16 * t + col];
-#pragma unroll
-        for (int w = 1; w < kWaves; w++) top = fmaxf(top, s_m[w][16 * t + col]);
-        const float by = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(mx[t] - top);
-#pragma unroll
-        for (int i = 0; i < ND; i++) o[t][i] *= by;
-        if (wave >= 2)
-#pragma unroll
-            for (int i = 0; i < ND; i++)
-                *reinterpret_cast<f4 *>(s_o + ((wave - 2) * ROWS + 16 * t + col) * LD + 16 * i + 4 * g) = o[t][i];
+        for (int i = 0; i < ND; i++)
+            *reinterpret_cast<f4 *>(s_o + (wave * ROWS + 16 * t + col) * LD + 16 * i + 4 * g) = o[t][i];
     }
     __syncthreads();
-    if (wave < 2) {
-#pragma unroll
-        for (int t = 0; t < RT; t++)
-#pragma unroll
-            for (int i = 0; i < ND; i++) {
-                f4 *at = reinterpret_cast<f4 *>(s_o + (wave * ROWS + 16 * t + col) * LD + 16 * i + 4 * g);
-                *at = o[t][i] + *at;
-            }
-    }
-    __syncthreads();
-    // ---- o = o0 + o1, l, m per row; out, or the chunk's part
     const int n = min(ROWS, rows - row0);
     const int64_t part = ((static_cast<int64_t>(b) * heads + head) * a.chunks + c) * a.rows + row0;
-    for (int i = threadIdx.x; i < n * (D / 4); i += 64 * kWaves) {
+    for (int i = threadIdx.x; i < n * (D / 4); i += 64 * W) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
-        f4 v = *reinterpret_cast<f4 *>(s_o + r * LD + d) + *reinterpret_cast<f4 *>(s_o + (ROWS + r) * LD + d);
         float top = s_m[0][r];
-        for (int w = 1; w < kWaves; w++) top = fmaxf(top, s_m[w][r]);
+#pragma unroll
+        for (int w = 1; w < W; w++) top = fmaxf(top, s_m[w][r]);
         float sum = 0.0f;
-        if (top != -INFINITY)
-            for (int w = 0; w < kWaves; w++) sum += s_l[w][r] * __builtin_amdgcn_exp2f(s_m[w][r] - top);
+        f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int w = 0; w < W; w++) {
+            const float by = top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(s_m[w][r] - top);
+            sum += s_l[w][r] * by;
+            v += by * *reinterpret_cast<const f4 *>(s_o + (w * ROWS + r) * LD + d);
+        }
         if (alone) {
             const bool over = a.max_len && sp.len + sp.n > a.max_len;
             const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
-            v = over ? f4{NAN, NAN, NAN, NAN} : v * inv;
-            *reinterpret_cast<f4 *>(s_o + r * LD + d) = v;
+            // its own place in the first wave's sums, which no other thread reads
+            *reinterpret_cast<f4 *>(s_o + r * LD + d) = over ? f4{NAN, NAN, NAN, NAN} : v * inv;
             if (over && i == 0) kv_flag(a.kv, SV_KV_OVER_MAX);
         } else {
             *(SV_GLOBAL f4 *)(a.part_o + (part + r) * D + d) = v;
@@ -640,43 +795,56 @@ __global__ __launch_bounds__(64 * kWaves, (min_waves<TYPE, D, RT>())) void kv_at
     }
 }
 
-template <int TYPE, int D>
-static int launch_dim(const AttnArgs &a, int rt, dim3 grid, hipStream_t st) {
-    if constexpr (D <= 128) {
-        if (rt == 4) {
-            hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, 4>), grid, dim3(64 * kWaves), 0, st, a);
-            return hip_check(hipGetLastError(), "kv_attention launch");
-        }
-        if (rt == 2) {
-            hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, 2>), grid, dim3(64 * kWaves), 0, st, a);
-            return hip_check(hipGetLastError(), "kv_attention launch");
-        }
+// Launches a variant: a workgroup per chunk that there can be, and row group.
+template <int TYPE, int D, int RT>
+static int launch_one(const AttnArgs &a, int64_t units, hipStream_t st) {
+    using S = Shape<TYPE, D, RT>;
+    static_assert(S::LDS <= kMaxLds, "LDS");
+    static std::atomic<int> allowed{0};
+    if (S::LDS > 65536 && !allowed.load()) {
+        const int rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT>),
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS),
+                                 "kv_attention: LDS size");
+        if (rc) return rc;
+        allowed.store(1);
     }
-    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, 1>), grid, dim3(64 * kWaves), 0, st, a);
+    const unsigned grid = static_cast<unsigned>((units + 7) / 8 * 8 * a.tiles);
+    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
     return hip_check(hipGetLastError(), "kv_attention launch");
 }
 
+template <int TYPE, int D>
+static int launch_dim(const AttnArgs &a, int rt, int64_t units, hipStream_t st) {
+    if constexpr (D <= 64) {
+        if (rt == 4) return launch_one<TYPE, D, 4>(a, units, st);
+    }
+    if constexpr (D <= 128) {
+        if (rt == 2) return launch_one<TYPE, D, 2>(a, units, st);
+    }
+    return launch_one<TYPE, D, 1>(a, units, st);
+}
+
 template <int TYPE>
-static int launch_type(const AttnArgs &a, int rt, dim3 grid, hipStream_t st) {
+static int launch_type(const AttnArgs &a, int rt, int64_t units, hipStream_t st) {
     switch (a.kv.dim) {
-        case 32: return launch_dim<TYPE, 32>(a, rt, grid, st);
-        case 64: return launch_dim<TYPE, 64>(a, rt, grid, st);
-        case 96: return launch_dim<TYPE, 96>(a, rt, grid, st);
-        case 128: return launch_dim<TYPE, 128>(a, rt, grid, st);
-        case 160: return launch_dim<TYPE, 160>(a, rt, grid, st);
-        case 192: return launch_dim<TYPE, 192>(a, rt, grid, st);
-        case 224: return launch_dim<TYPE, 224>(a, rt, grid, st);
-        case 256: return launch_dim<TYPE, 256>(a, rt, grid, st);
+        case 32: return launch_dim<TYPE, 32>(a, rt, units, st);
+        case 64: return launch_dim<TYPE, 64>(a, rt, units, st);
+        case 96: return launch_dim<TYPE, 96>(a, rt, units, st);
+        case 128: return launch_dim<TYPE, 128>(a, rt, units, st);
+        case 160: return launch_dim<TYPE, 160>(a, rt, units, st);
+        case 192: return launch_dim<TYPE, 192>(a, rt, units, st);
+        case 224: return launch_dim<TYPE, 224>(a, rt, units, st);
+        case 256: return launch_dim<TYPE, 256>(a, rt, units, st);
     }
     return fail(SV_ERR_SHAPE, "kv_attention: unsupported head dimension");
 }
 
 #if SV_INST_KV == 1
-int attn_launch_f16(const AttnArgs &a, int rt, dim3 grid, hipStream_t st) { return launch_type<SV_KV_F16>(a, rt, grid, st); }
+int attn_launch_f16(const AttnArgs &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_F16>(a, rt, units, st); }
 #elif SV_INST_KV == 30
-int attn_launch_bf16(const AttnArgs &a, int rt, dim3 grid, hipStream_t st) { return launch_type<SV_KV_BF16>(a, rt, grid, st); }
+int attn_launch_bf16(const AttnArgs &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_BF16>(a, rt, units, st); }
 #else
-int attn_launch_i8(const AttnArgs &a, int rt, dim3 grid, hipStream_t st) { return launch_type<SV_KV_I8>(a, rt, grid, st); }
+int attn_launch_i8(const AttnArgs &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_I8>(a, rt, units, st); }
 #endif
 
 }  // namespace sv

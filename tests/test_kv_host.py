@@ -136,7 +136,7 @@ def test_ropes(change, code):
     (dict(q_heads=12), sv.SV_ERR_SHAPE), (dict(q_heads=0), sv.SV_ERR_SHAPE), (dict(q_heads=520), sv.SV_ERR_SHAPE),
     (dict(scale=0.0), sv.SV_ERR_ARG), (dict(scale=-1.0), sv.SV_ERR_ARG), (dict(scale=float("inf")), sv.SV_ERR_ARG),
     (dict(scale=float("nan")), sv.SV_ERR_ARG), (dict(window=-1), sv.SV_ERR_ARG), (dict(sinks=-1), sv.SV_ERR_ARG),
-    (dict(sinks=4), sv.SV_ERR_ARG), (dict(max_len=-1), sv.SV_ERR_ARG), (dict(chunk=64), sv.SV_ERR_ARG),
+    (dict(sinks=4), sv.SV_ERR_ARG), (dict(max_len=-1), sv.SV_ERR_ARG), (dict(chunk=48), sv.SV_ERR_ARG),
     (dict(chunk=-128), sv.SV_ERR_ARG)])
 def test_attention_arguments(change, code):
     d = dict(q_heads=40, scale=0.1, window=0, sinks=0, max_len=0, chunk=0)
