@@ -172,7 +172,7 @@ __device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals
 }
 
 // Row tiles of 16 that one wave holds, by the rows of a head.
-constexpr int kMaxLds = 144 * 1024;
+constexpr int kMaxLds = 156 * 1024;
 
 inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 || dim > 64 ? 2 : 4; }
 

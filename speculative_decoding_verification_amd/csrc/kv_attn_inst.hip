@@ -235,7 +235,7 @@ __device__ __forceinline__ void ring_read(uint32_t at, Raw<1> *r) {
     constexpr int NEXT = EVERY ? FROM + T / 2 * STRIDE : FROM + T * STRIDE;
     if constexpr (N > T) ring_read<LEAVE, STRIDE, EVERY, N - T, NEXT>(at, r + T);
 }
-__device__ __forceinline__ void ring_read_scales(uint32_t at, float (&s)[8]) {
+__device__ __forceinline__ void lds_read8(uint32_t at, float (&s)[8]) {
     u32x4 a, b;
     asm volatile("ds_read_b128 %0, %2\n ds_read_b128 %1, %2 offset:16\n s_waitcnt lgkmcnt(0)"
                  : "=&v"(a), "=&v"(b)
@@ -274,106 +274,128 @@ struct Shape {
     static constexpr int LEAVE_V = N / 2 * (LOADS + SCALES) + (N / 2 - 1) * LOADS;
     static_assert(LEAVE_K < 64 && LEAVE_V < 64, "the wait counter has six bits");
     static constexpr int ROWS = 16 * RT, LD = D + 4;
+    static constexpr int STAGED = W * RING_BYTES;               // fp32 rows, before the blocks
     static constexpr int SUMS = W * ROWS * LD * 4;              // the waves' sums, after the blocks
-    static constexpr int LDS = W * RING_BYTES > SUMS ? W * RING_BYTES : SUMS;
+    static constexpr int LDS = STAGED + ROWS * LD * 4 > SUMS ? STAGED + ROWS * LD * 4 : SUMS;
 };
 
-// The queries of a row tile as the second operand of S^T = K Q^T: rotated,
-// scaled, and for fp16 multiplied by the power of two that brings the row's
-// largest magnitude into [2^12, 2^13); the row's scores are multiplied by
-// the returned power of two to undo that.  Every wave makes its own.
+// The rows' queries on their way to LDS: each of the workgroup's threads
+// takes N pieces of four elements, and all loads are issued before any is
+// used.  Where a rotation's pairs do not fall into whole pieces (rot not a
+// multiple of 8) it is made element by element when the rows are stored.
+template <int D, int ROWS, int THREADS>
+struct Rows {
+    static constexpr int QUADS = D / 4, N = (ROWS * QUADS + THREADS - 1) / THREADS;
+    u32x4 own[N], other[N];  // other: the other elements of the pairs (halves)
+    u32x2 w[N][4];           // cos, sin
+
+    static __device__ __forceinline__ const float *angles(const AttnArgs &a, int len, int b, int m) {
+        const int depth = a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
+        return a.rope.table + static_cast<int64_t>(min(len + depth, a.rope.n_pos - 1)) * a.rope.rot;
+    }
+    static __device__ __forceinline__ const float *query(const AttnArgs &a, int b, int head, int m, int r) {
+        return a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + head * a.group + (r - m * a.group)) * D;
+    }
+
+    __device__ __forceinline__ void load(const AttnArgs &a, int len, int b, int head, int row0, int rows) {
+        const int tid = threadIdx.x, half = a.rope.rot / 2;
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const int it = tid + k * THREADS, i = it / QUADS, d = it % QUADS * 4;
+            const int r = i < ROWS && row0 + i < rows ? row0 + i : row0;
+            const int m = a.by_group(r);
+            const float *qp = query(a, b, head, m, r);
+            own[k] = gld(reinterpret_cast<const u32x4 *>(qp + d));
+            if (a.rope.mode == SV_ROPE_NONE || a.rope.rot % 8) continue;
+            const bool turn = d < a.rope.rot, second = d >= half;
+            const float *cs = angles(a, len, b, m);
+            if (a.rope.mode == SV_ROPE_PAIRS) {
+                cs += turn ? d : 0;
+                w[k][0] = gld(reinterpret_cast<const u32x2 *>(cs));
+                w[k][1] = gld(reinterpret_cast<const u32x2 *>(cs + 2));
+            } else {
+                const int p = !turn ? 0 : second ? d - half : d;
+                cs += 2 * p;
+#pragma unroll
+                for (int e = 0; e < 4; e++) w[k][e] = gld(reinterpret_cast<const u32x2 *>(cs + 2 * e));
+                other[k] = gld(reinterpret_cast<const u32x4 *>(qp + (second ? p : p + half)));
+            }
+        }
+    }
+
+    __device__ __forceinline__ void store(const AttnArgs &a, int len, int b, int head, int row0, int rows,
+                                          float *to) {
+        typedef float f4 __attribute__((ext_vector_type(4)));
+        const int tid = threadIdx.x, half = a.rope.rot / 2;
+#pragma unroll
+        for (int k = 0; k < N; k++) {
+            const int it = tid + k * THREADS, i = it / QUADS, d = it % QUADS * 4;
+            if (i >= ROWS) continue;
+            const bool live = row0 + i < rows;
+            f4 x = __builtin_bit_cast(f4, own[k]);
+            if (a.rope.mode != SV_ROPE_NONE && d < a.rope.rot) {
+                if (a.rope.rot % 8) {
+                    const int r = live ? row0 + i : row0, m = a.by_group(r);
+                    const float *qp = query(a, b, head, m, r), *cs = angles(a, len, b, m);
+#pragma unroll 1
+                    for (int e = 0; e < 4; e++) {
+                        const int y = d + e;
+                        if (y >= a.rope.rot) break;
+                        const bool pairs = a.rope.mode == SV_ROPE_PAIRS, second = pairs ? y & 1 : y >= half;
+                        const int p = pairs ? y >> 1 : second ? y - half : y;
+                        const int mate = pairs ? y ^ 1 : second ? p : p + half;
+                        const float u = __fmul_rn(gld(qp + y), gld(cs + 2 * p));
+                        const float v = __fmul_rn(gld(qp + mate), gld(cs + 2 * p + 1));
+                        const float z = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
+                        x.x = e == 0 ? z : x.x;
+                        x.y = e == 1 ? z : x.y;
+                        x.z = e == 2 ? z : x.z;
+                        x.w = e == 3 ? z : x.w;
+                    }
+                } else if (a.rope.mode == SV_ROPE_PAIRS) {
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float co = __uint_as_float(w[k][e / 2].x), si = __uint_as_float(w[k][e / 2].y);
+                        const float x0 = x[e], x1 = x[e + 1];
+                        x[e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
+                        x[e + 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
+                    }
+                } else {
+                    const f4 y = __builtin_bit_cast(f4, other[k]);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float u = __fmul_rn(x[e], __uint_as_float(w[k][e].x));
+                        const float v = __fmul_rn(y[e], __uint_as_float(w[k][e].y));
+                        x[e] = d >= half ? __fadd_rn(u, v) : __fsub_rn(u, v);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[e] = live ? x[e] * a.scale : 0.0f;
+            *reinterpret_cast<f4 *>(to + i * (D + 4) + d) = x;
+        }
+    }
+};
+
+// The queries of a row tile as the second operand of S^T = K Q^T, from the
+// staged rows (by reads in asm: the ring's transfers are on their way), for
+// fp16 multiplied by the power of two that brings the row's largest magnitude
+// into [2^12, 2^13); the row's scores are multiplied by the returned power of
+// two to undo that.
 template <int TYPE, int D>
-__device__ __forceinline__ float make_queries(const AttnArgs &a, int len, int b, int head, int row0, int rows,
-                                              typename Kind<TYPE>::KVec (&qf)[D / 32][Kind<TYPE>::kq]) {
+__device__ __forceinline__ float take_queries(uint32_t staged, typename Kind<TYPE>::KVec (&qf)[D / 32][Kind<TYPE>::kq]) {
     using Kd = Kind<TYPE>;
     constexpr int NC = D / 32;
-    const int lane = threadIdx.x & 63, g = lane >> 4;
-    const int r = row0 + (lane & 15);
-    const bool live = r < rows;
-    const int m = live ? a.by_group(r) : 0, hq = head * a.group + (live ? r - m * a.group : 0);
-    const float *qp = a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + hq) * D;
-    const int rot = a.rope.mode == SV_ROPE_NONE ? 0 : a.rope.rot, half = rot / 2;
-    const bool pairs = a.rope.mode == SV_ROPE_PAIRS;
-    const float *cs = a.rope.table;
-    if (rot) {
-        const int depth = a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
-        cs += static_cast<int64_t>(min(len + depth, a.rope.n_pos - 1)) * rot;
-    }
+    const int lane = threadIdx.x & 63;
+    const uint32_t at = staged + ((lane & 15) * (D + 4) + 8 * (lane >> 4)) * 4;
     float x[NC][8];
-    if (rot % 16 == 0) {
-        // whole pieces of eight are rotated alike: all loads first
-        f4 own[NC][2], other[NC][2], w[NC][4];
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-            const int d = 32 * c + 8 * g;
-            const bool turn = d < rot, second = d >= half;
-            own[c][0] = gld(reinterpret_cast<const f4 *>(qp + d));
-            own[c][1] = gld(reinterpret_cast<const f4 *>(qp + d + 4));
-            if (!rot) continue;
-            if (pairs) {
-                const float *p = cs + (turn ? d : 0);
-                w[c][0] = gld(reinterpret_cast<const f4 *>(p));
-                w[c][1] = gld(reinterpret_cast<const f4 *>(p + 4));
-            } else {
-                const int i = !turn ? 0 : second ? d - half : d;
-#pragma unroll
-                for (int e = 0; e < 4; e++) w[c][e] = gld(reinterpret_cast<const f4 *>(cs + 2 * i + 4 * e));
-                const float *p = qp + (second ? i : i + half);
-                other[c][0] = gld(reinterpret_cast<const f4 *>(p));
-                other[c][1] = gld(reinterpret_cast<const f4 *>(p + 4));
-            }
-        }
-#pragma unroll
-        for (int c = 0; c < NC; c++) {
-            const int d = 32 * c + 8 * g;
-            const bool turn = d < rot, second = d >= half;
-#pragma unroll
-            for (int e = 0; e < 8; e++) x[c][e] = own[c][e >> 2][e & 3];
-            if (!rot) continue;
-            if (pairs) {
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float co = w[c][e >> 2][e & 3], si = w[c][e >> 2][(e & 3) + 1], x0 = x[c][e], x1 = x[c][e + 1];
-                    const float y0 = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
-                    const float y1 = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
-                    x[c][e] = turn ? y0 : x0;
-                    x[c][e + 1] = turn ? y1 : x1;
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    const float u = __fmul_rn(x[c][e], w[c][e >> 1][2 * (e & 1)]);
-                    const float v = __fmul_rn(other[c][e >> 2][e & 3], w[c][e >> 1][2 * (e & 1) + 1]);
-                    const float y = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
-                    x[c][e] = turn ? y : x[c][e];
-                }
-            }
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < NC; c++)
-#pragma unroll
-            for (int e = 0; e < 8; e++) {
-                const int d = 32 * c + 8 * g + e;
-                float y = gld(qp + d);
-                if (d < rot) {
-                    const bool second = pairs ? d & 1 : d >= half;
-                    const int i = pairs ? d >> 1 : second ? d - half : d;
-                    const int mate = pairs ? d ^ 1 : second ? i : i + half;
-                    const float u = __fmul_rn(y, gld(cs + 2 * i)), v = __fmul_rn(gld(qp + mate), gld(cs + 2 * i + 1));
-                    y = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
-                }
-                x[c][e] = y;
-            }
-    }
     float top = 0.0f;
 #pragma unroll
-    for (int c = 0; c < NC; c++)
+    for (int c = 0; c < NC; c++) {
+        lds_read8(at + 128 * c, x[c]);
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            x[c][e] = live ? x[c][e] * a.scale : 0.0f;
-            top = fmaxf(top, fabsf(x[c][e]));
-        }
+        for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[c][e]));
+    }
     float back = 1.0f;
     if constexpr (__is_same(typename Kd::KVec, h8)) {
         top = row_max(top);
@@ -486,15 +508,10 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
     const bool any = j < last;
     int page = page_of(j);
 
-    // ---- queries
-    typename Kd::KVec qf[RT][NC][Kd::kq];
-    float rs[RT];
-#pragma unroll
-    for (int t = 0; t < RT; t++)
-    {
-        rs[t] = make_queries<TYPE, D>(a, len, b, head, row0 + 16 * t, rows, qf[t]);
-        __builtin_amdgcn_sched_barrier(0);  // a tile's loads take many registers: one tile at a time
-    }
+    // ---- the rows' queries to LDS, behind the ring
+    Rows<D, ROWS, 64 * W> staged;
+    staged.load(a, len, b, head, row0, rows);
+    staged.store(a, len, b, head, row0, rows, reinterpret_cast<float *>(s_mem + S::STAGED));
 
     // ---- the ring: `slot` is the half read next and, once it is in
     // registers, the half that is refilled
@@ -538,6 +555,15 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
         }
     }
 
+    // ---- queries, once every wave has stored its pieces
+    asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
+    typename Kd::KVec qf[RT][NC][Kd::kq];
+    float rs[RT];
+#pragma unroll
+    for (int t = 0; t < RT; t++)
+        rs[t] = take_queries<TYPE, D>(
+            static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS uint8_t *)s_mem)) + S::STAGED + 16 * t * LD * 4, qf[t]);
+
     f4 o[RT][ND];
     float mx[RT], l[RT];
 #pragma unroll
@@ -559,8 +585,8 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
         } else {
             ring_read<S::LEAVE_K, 1024, 32, 2 * NC>(
                 ring + slot * S::HALF + (g * 32 + 8 * (col >> 2) + (col & 3)) * 8, kr);
-            ring_read_scales(ring + S::N * S::HALF + (slot >> 1) * 256 + 32 * g, ks);
-            ring_read_scales(ring + S::N * S::HALF + (slot >> 1) * 256 + 128 + 32 * g, vs);
+            lds_read8(ring + S::N * S::HALF + (slot >> 1) * 256 + 32 * g, ks);
+            lds_read8(ring + S::N * S::HALF + (slot >> 1) * 256 + 128 + 32 * g, vs);
         }
         request_k();
         turn();
