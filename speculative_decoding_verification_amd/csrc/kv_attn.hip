@@ -1,5 +1,7 @@
 // kv_attn.hip - host side of the cache's attention, and the join of the
 // chunks' partial softmaxes.
+#include <algorithm>
+
 #include "kv_attn.h"
 
 namespace sv {
@@ -82,14 +84,40 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
     finish_rows(a, s_v, D, b, head, r, 1);
 }
 
-// Slots of a chunk: at the longest length of the call a workgroup for every
-// compute unit, but no shorter than a block for each wave, and no longer than
-// makes the parts a small share of what is read.
-static int chunk_rule(int64_t B, int64_t heads, int64_t span) {
-    int64_t c = (span * B * heads / 256 + 127) / 128 * 128;
-    if (c < 128) c = 128;
-    if (c > 4096) c = 4096;
-    return static_cast<int>(c);
+// Chunks that a sequence can have: of its whole length, or of what a window
+// and the sinks can touch.
+static int64_t chunks_within(int64_t bound, int64_t window, int64_t sinks, int64_t chunk) {
+    const int64_t all = (bound + chunk - 1) / chunk;
+    if (!window) return all;
+    const int64_t most = (sinks + chunk - 1) / chunk + (window + SV_MAX_M + chunk - 1) / chunk + 1;
+    return std::min(all, most);
+}
+
+// Slots of a chunk when the caller leaves the choice: the shortest with which
+// the launch is one round of workgroups (256 compute units hold one wide or
+// two narrow workgroups each).  Without a window the sequences of a batch are
+// seldom all as long as the longest: half a round more is allowed for.  Past
+// one round of 2048 the length evens out the last round.  Measured in us, 128
+// heads of 8 and a group of 5:
+//   5 x 4099 slots, 8 heads, fp16          256: 22, 384: 25, 640: 37
+//   8 rows, window 1024, 8 heads of 96     384: 24, 512: 20, 640: 24
+//   4 trees of up to 8191, 8 heads of 64   256: 50, 384: 36, 512: 43
+//   16 sequences up to 16384, int8         1024: 94, 1536: 90, 2048: 98
+//   32 sequences, window 4096, fp16        1024: 152, 1536: 148, 2048: 166
+// A sequence that fits one short chunk needs no join (300 slots: 11 against
+// 14 with chunks of 256).
+static int chunk_rule(int64_t B, int64_t heads, int dim, int64_t bound, int64_t window, int64_t sinks) {
+    if (bound <= 512) return static_cast<int>((bound + 127) / 128 * 128);
+    for (int c = 256; c <= 2048; c += 128) {
+        int64_t room = attn_wide(dim, c) ? 256 : 512;
+        if (B > 1 && !window) room += room / 2;
+        const int64_t pairs = B * heads;
+        // of a window that lies anywhere: window / c + 1 chunks on average
+        const int64_t units = window && window + sinks < bound ? pairs * ((sinks + c - 1) / c + 1) + pairs * window / c
+                                                               : pairs * ((bound + c - 1) / c);
+        if (units <= room) return c;
+    }
+    return 1536;
 }
 
 struct Plan {
@@ -113,8 +141,6 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     if (rc) return rc;
     const int64_t cap = static_cast<int64_t>(d.width) * d.page;
     p->bound = at->max_len && at->max_len < cap ? at->max_len : cap;
-    const int64_t seen = static_cast<int64_t>(at->window) + at->sinks + SV_MAX_M;
-    const int64_t span = at->window && seen < p->bound ? seen : p->bound;
     a->kv = d;
     a->bt = *bt;
     a->rope = at->rope ? *at->rope : sv_kv_rope{};
@@ -124,14 +150,10 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     a->window = at->window;
     a->sinks = at->sinks;
     a->max_len = at->max_len;
-    a->chunk = at->chunk ? at->chunk : chunk_rule(bt->B, d.heads, span);
-    int64_t chunks = (p->bound + a->chunk - 1) / a->chunk;
-    if (at->window) {
-        const int64_t most = (at->sinks + static_cast<int64_t>(a->chunk) - 1) / a->chunk +
-                             (static_cast<int64_t>(at->window) + SV_MAX_M + a->chunk - 1) / a->chunk + 1;
-        if (most < chunks) chunks = most;
-    }
+    a->chunk = at->chunk ? at->chunk : chunk_rule(bt->B, d.heads, d.dim, p->bound, at->window, at->sinks);
+    const int64_t chunks = chunks_within(p->bound, at->window, at->sinks, a->chunk);
     a->chunks = static_cast<int32_t>(chunks);
+    a->wide = attn_wide(d.dim, a->chunk);
     a->scale = at->scale * 1.44269504088896340736f;
     p->rt = attn_tiles_per_wave(d.dim, a->rows);
     a->tiles = (a->rows + 16 * p->rt - 1) / (16 * p->rt);

@@ -255,10 +255,12 @@ __device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to) {
     __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, 0, ONCE ? 2 : 0);
 }
 
-template <int TYPE, int D, int RT>
+// WIDE: twice the waves a workgroup, and one workgroup a compute unit instead
+// of two.
+template <int TYPE, int D, int RT, bool WIDE>
 struct Shape {
     using Kd = Kind<TYPE>;
-    static constexpr int W = TYPE == SV_KV_I8 ? 8 : 4;          // waves
+    static constexpr int W = (TYPE == SV_KV_I8 ? 4 : 2) * (WIDE ? 2 : 1);  // waves
     static constexpr int HALF = 32 * D * Kd::esz;               // bytes of a block's keys, or values
     static constexpr int LOADS = HALF / 1024;                   // transfers of a half
     static constexpr int SCALES = TYPE == SV_KV_I8 ? 1 : 0;     // and one of both scales with the keys
@@ -267,16 +269,21 @@ struct Shape {
     static constexpr int RING = TYPE == SV_KV_I8 ? 16384 : 32768;
     static constexpr int FIT = RING / HALF / 2 * 2;
     static constexpr int N = FIT < 2 ? 2 : FIT > 8 ? 8 : FIT;
-    static constexpr int RING_BYTES = N * HALF + N / 2 * 256 * SCALES;
+    // [half][wave], then the scales [block][wave]
+    static constexpr int SCALES_AT = N * W * HALF, RING_BYTES = SCALES_AT + N / 2 * W * 256 * SCALES;
     // transfers that may still be on their way when the oldest half is read:
     // those of the halves after it
     static constexpr int LEAVE_K = (N / 2 - 1) * (LOADS + SCALES) + N / 2 * LOADS;
     static constexpr int LEAVE_V = N / 2 * (LOADS + SCALES) + (N / 2 - 1) * LOADS;
     static_assert(LEAVE_K < 64 && LEAVE_V < 64, "the wait counter has six bits");
     static constexpr int ROWS = 16 * RT, LD = D + 4;
-    static constexpr int STAGED = W * RING_BYTES;               // fp32 rows, before the blocks
+    // the fp32 rows that the queries are made of: in the halves past the
+    // first block where they fit, else behind the ring
+    static constexpr bool INSIDE = (N - 2) * W * HALF >= ROWS * LD * 4;
+    static constexpr int STAGED = INSIDE ? 2 * W * HALF : RING_BYTES;
+    static constexpr int NEED = INSIDE ? RING_BYTES : RING_BYTES + ROWS * LD * 4;
     static constexpr int SUMS = W * ROWS * LD * 4;              // the waves' sums, after the blocks
-    static constexpr int LDS = STAGED + ROWS * LD * 4 > SUMS ? STAGED + ROWS * LD * 4 : SUMS;
+    static constexpr int LDS = NEED > SUMS ? NEED : SUMS;
 };
 
 // The rows' queries on their way to LDS: each of the workgroup's threads
@@ -441,10 +448,11 @@ __device__ __forceinline__ int find_chunk(const AttnArgs &a, int u, int *before)
     return -1;
 }
 
-template <int TYPE, int D, int RT>
-__global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kernel(AttnArgs a) {
+template <int TYPE, int D, int RT, bool WIDE>
+__global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_I8 ? 2 : 1)) void kv_attn_kernel(
+    AttnArgs a) {
     using Kd = Kind<TYPE>;
-    using S = Shape<TYPE, D, RT>;
+    using S = Shape<TYPE, D, RT, WIDE>;
     constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz, W = S::W, LD = S::LD, ROWS = S::ROWS;
     constexpr bool ONCE = D <= 128 && RT < 4;  // one row group
     extern __shared__ __align__(1024) uint8_t s_mem[];
@@ -508,14 +516,10 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
     const bool any = j < last;
     int page = page_of(j);
 
-    // ---- the rows' queries to LDS, behind the ring
-    Rows<D, ROWS, 64 * W> staged;
-    staged.load(a, len, b, head, row0, rows);
-    staged.store(a, len, b, head, row0, rows, reinterpret_cast<float *>(s_mem + S::STAGED));
-
     // ---- the ring: `slot` is the half read next and, once it is in
     // registers, the half that is refilled
-    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS uint8_t *)s_mem)) + wave * S::RING_BYTES;
+    const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS uint8_t *)s_mem));
+    const uint32_t mine = ring + wave * S::HALF, mine_scales = ring + S::SCALES_AT + wave * 256;
     uint32_t slot = 0;  // 0 .. N - 1
     int ji = j, jin = settle(j + W), pin = page_of(jin);  // block to be requested, the one after it, its page
     const uint8_t *bi = block_at(ji, page);
@@ -533,27 +537,27 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
     auto request_k = [&]() {
 #pragma unroll
         for (int i = 0; i < S::LOADS; i++)
-            to_lds<ONCE>(bi + k_from + (ESZ == 2 ? (i >> 1) * 2048 + (i & 1) * 64 : i * 1024), ring + slot * S::HALF + i * 1024);
+            to_lds<ONCE>(bi + k_from + (ESZ == 2 ? (i >> 1) * 2048 + (i & 1) * 64 : i * 1024), mine + slot * (W * S::HALF) + i * 1024);
         if constexpr (S::SCALES) {
-            if (lane < 16) to_lds<ONCE>(bi + 64 * D + lane * 16, ring + S::N * S::HALF + (slot >> 1) * 256);
+            if (lane < 16) to_lds<ONCE>(bi + 64 * D + lane * 16, mine_scales + (slot >> 1) * (W * 256));
         }
     };
     auto request_v = [&]() {
 #pragma unroll
         for (int i = 0; i < S::LOADS; i++)
-            to_lds<ONCE>(bi + S::HALF + v_from + (ESZ == 2 ? i * 256 : i * 1024), ring + slot * S::HALF + i * 1024);
+            to_lds<ONCE>(bi + S::HALF + v_from + (ESZ == 2 ? i * 256 : i * 1024), mine + slot * (W * S::HALF) + i * 1024);
         advance();
     };
     auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
+    Rows<D, ROWS, 64 * W> staged;
+    staged.load(a, len, b, head, row0, rows);
     if (any) {
-#pragma unroll 1
-        for (int i = 0; i < S::N / 2; i++) {
-            request_k();
-            turn();
-            request_v();
-            turn();
-        }
+        request_k();
+        turn();
+        request_v();
+        turn();
     }
+    staged.store(a, len, b, head, row0, rows, reinterpret_cast<float *>(s_mem + S::STAGED));
 
     // ---- queries, once every wave has stored its pieces
     asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
@@ -561,8 +565,19 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
     float rs[RT];
 #pragma unroll
     for (int t = 0; t < RT; t++)
-        rs[t] = take_queries<TYPE, D>(
-            static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS uint8_t *)s_mem)) + S::STAGED + 16 * t * LD * 4, qf[t]);
+        rs[t] = take_queries<TYPE, D>(ring + S::STAGED + 16 * t * LD * 4, qf[t]);
+    if constexpr (S::N > 2) {
+        if constexpr (S::INSIDE) asm volatile("s_barrier" ::: "memory");  // every wave has its queries
+        if (any) {
+#pragma unroll
+            for (int i = 1; i < S::N / 2; i++) {
+                request_k();
+                turn();
+                request_v();
+                turn();
+            }
+        }
+    }
 
     f4 o[RT][ND];
     float mx[RT], l[RT];
@@ -581,12 +596,12 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
         Raw<ESZ> kr[2 * NC], vr[ND];
         float ks[8], vs[8];  // int8: the scales of the lane group's eight slots
         if constexpr (ESZ == 2) {
-            ring_read<S::LEAVE_K, 1024, 2 * NC>(ring + slot * S::HALF + lane * 16, kr);
+            ring_read<S::LEAVE_K, 1024, 2 * NC>(mine + slot * (W * S::HALF) + lane * 16, kr);
         } else {
             ring_read<S::LEAVE_K, 1024, 32, 2 * NC>(
-                ring + slot * S::HALF + (g * 32 + 8 * (col >> 2) + (col & 3)) * 8, kr);
-            lds_read8(ring + S::N * S::HALF + (slot >> 1) * 256 + 32 * g, ks);
-            lds_read8(ring + S::N * S::HALF + (slot >> 1) * 256 + 128 + 32 * g, vs);
+                mine + slot * (W * S::HALF) + (g * 32 + 8 * (col >> 2) + (col & 3)) * 8, kr);
+            lds_read8(mine_scales + (slot >> 1) * (W * 256) + 32 * g, ks);
+            lds_read8(mine_scales + (slot >> 1) * (W * 256) + 128 + 32 * g, vs);
         }
         request_k();
         turn();
@@ -685,9 +700,9 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
         // ---- o += V^T P^T
         const uint8_t *blk = block_at(j, page);
         if constexpr (ESZ == 2) {
-            ring_read<S::LEAVE_V, 1024, ND>(ring + slot * S::HALF + lane * 16, vr);
+            ring_read<S::LEAVE_V, 1024, ND>(mine + slot * (W * S::HALF) + lane * 16, vr);
         } else {
-            ring_read<S::LEAVE_V, 128, 0, ND>(ring + slot * S::HALF + (g * D + col) * 8, vr);
+            ring_read<S::LEAVE_V, 128, 0, ND>(mine + slot * (W * S::HALF) + (g * D + col) * 8, vr);
         }
         request_v();
         turn();
@@ -822,32 +837,42 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), 1) void kv_attn_kerne
 }
 
 // Launches a variant: a workgroup per chunk that there can be, and row group.
-template <int TYPE, int D, int RT>
+template <int TYPE, int D, int RT, bool WIDE>
 static int launch_one(const AttnArgs &a, int64_t units, hipStream_t st) {
-    using S = Shape<TYPE, D, RT>;
+    using S = Shape<TYPE, D, RT, WIDE>;
     static_assert(S::LDS <= kMaxLds, "LDS");
     static std::atomic<int> allowed{0};
     if (S::LDS > 65536 && !allowed.load()) {
-        const int rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT>),
+        const int rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT, WIDE>),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS),
                                  "kv_attention: LDS size");
         if (rc) return rc;
         allowed.store(1);
     }
     const unsigned grid = static_cast<unsigned>((units + 7) / 8 * 8 * a.tiles);
-    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
+    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT, WIDE>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
     return hip_check(hipGetLastError(), "kv_attention launch");
+}
+
+template <int TYPE, int D, int RT>
+static int launch_rows(const AttnArgs &a, int64_t units, hipStream_t st) {
+    if constexpr (D > 224)
+        return launch_one<TYPE, D, RT, true>(a, units, st);
+    else if constexpr (D <= 64)
+        return launch_one<TYPE, D, RT, false>(a, units, st);
+    else
+        return a.wide ? launch_one<TYPE, D, RT, true>(a, units, st) : launch_one<TYPE, D, RT, false>(a, units, st);
 }
 
 template <int TYPE, int D>
 static int launch_dim(const AttnArgs &a, int rt, int64_t units, hipStream_t st) {
     if constexpr (D <= 64) {
-        if (rt == 4) return launch_one<TYPE, D, 4>(a, units, st);
+        if (rt == 4) return launch_rows<TYPE, D, 4>(a, units, st);
     }
     if constexpr (D <= 128) {
-        if (rt == 2) return launch_one<TYPE, D, 2>(a, units, st);
+        if (rt == 2) return launch_rows<TYPE, D, 2>(a, units, st);
     }
-    return launch_one<TYPE, D, 1>(a, units, st);
+    return launch_rows<TYPE, D, 1>(a, units, st);
 }
 
 template <int TYPE>
