@@ -37,7 +37,7 @@ struct AttnArgs {
     int32_t wide;      // 1: few chunks, so each gets twice the waves
     int32_t tiles;     // workgroups that share a (sequence, head, chunk): row groups
     float scale;       // times log2(e)
-    Div by_group, by_chunk, by_tiles, by_heads;
+    Div by_group, by_chunk, by_tiles, by_heads, by_turns;  // by_turns: by rot / 8
 };
 
 // What a sequence's rows see, in whole chunks.  Slots fit 32 bits (width *

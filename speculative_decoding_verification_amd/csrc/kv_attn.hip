@@ -161,6 +161,7 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     a->by_chunk = div_by(a->chunk);
     a->by_tiles = div_by(a->tiles);
     a->by_heads = div_by(d.heads);
+    a->by_turns = div_by(std::max(1, a->rope.rot / 8));
     p->units = static_cast<int64_t>(bt->B) * d.heads * chunks;
     SV_REQUIRE(p->units * a->tiles < (1ll << 24), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
     p->bytes = p->o_m = p->o_l = 0;

@@ -235,11 +235,11 @@ __device__ __forceinline__ void ring_read(uint32_t at, Raw<1> *r) {
     constexpr int NEXT = EVERY ? FROM + T / 2 * STRIDE : FROM + T * STRIDE;
     if constexpr (N > T) ring_read<LEAVE, STRIDE, EVERY, N - T, NEXT>(at, r + T);
 }
-__device__ __forceinline__ void lds_read8(uint32_t at, float (&s)[8]) {
+__device__ __forceinline__ void lds_read8(uint32_t at, uint32_t at4, float (&s)[8]) {
     u32x4 a, b;
-    asm volatile("ds_read_b128 %0, %2\n ds_read_b128 %1, %2 offset:16\n s_waitcnt lgkmcnt(0)"
+    asm volatile("ds_read_b128 %0, %2\n ds_read_b128 %1, %3\n s_waitcnt lgkmcnt(0)"
                  : "=&v"(a), "=&v"(b)
-                 : "v"(at)
+                 : "v"(at), "v"(at4)
                  : "memory");
 #pragma unroll
     for (int e = 0; e < 4; e++) {
@@ -277,131 +277,122 @@ struct Shape {
     static constexpr int LEAVE_V = N / 2 * (LOADS + SCALES) + (N / 2 - 1) * LOADS;
     static_assert(LEAVE_K < 64 && LEAVE_V < 64, "the wait counter has six bits");
     static constexpr int ROWS = 16 * RT, LD = D + 4;
-    // the fp32 rows that the queries are made of: in the halves past the
-    // first block where they fit, else behind the ring
-    static constexpr bool INSIDE = (N - 2) * W * HALF >= ROWS * LD * 4;
-    static constexpr int STAGED = INSIDE ? 2 * W * HALF : RING_BYTES;
-    static constexpr int NEED = INSIDE ? RING_BYTES : RING_BYTES + ROWS * LD * 4;
+    // the fp32 rows that the queries are made of, and the angles of up to 16
+    // positions: in the halves past the first block where they fit, else in
+    // the ring's beginning, which is then filled after they are used
+    static constexpr int FIRST = (N - 2) * W * HALF >= (ROWS + 16) * D * 4 ? 1 : 0;  // blocks requested before
+    static constexpr int STAGED = FIRST * 2 * W * HALF, ANGLES = STAGED + ROWS * D * 4;
+    static_assert(ANGLES + 16 * D * 4 <= SCALES_AT, "staging");
     static constexpr int SUMS = W * ROWS * LD * 4;              // the waves' sums, after the blocks
-    static constexpr int LDS = NEED > SUMS ? NEED : SUMS;
+    static constexpr int LDS = RING_BYTES > SUMS ? RING_BYTES : SUMS;
 };
 
-// The rows' queries on their way to LDS: each of the workgroup's threads
-// takes N pieces of four elements, and all loads are issued before any is
-// used.  Where a rotation's pairs do not fall into whole pieces (rot not a
-// multiple of 8) it is made element by element when the rows are stored.
-template <int D, int ROWS, int THREADS>
-struct Rows {
-    static constexpr int QUADS = D / 4, N = (ROWS * QUADS + THREADS - 1) / THREADS;
-    u32x4 own[N], other[N];  // other: the other elements of the pairs (halves)
-    u32x2 w[N][4];           // cos, sin
+// Queries are staged as they lie, a row's quads of four elements exchanged by
+// the row's number, so that reads of one quad of 16 rows spread over the
+// banks: quad q of row i is the row's (q ^ i % 8)-th.
+template <int D>
+__device__ __forceinline__ uint32_t quad_at(uint32_t staged, int i, int q) {
+    return staged + (i * (D / 4) + (q ^ (i & 7))) * 16;
+}
+__device__ __forceinline__ const float *query_of(const AttnArgs &a, int b, int head, int r) {
+    const int m = a.by_group(r);
+    return a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + head * a.group + (r - m * a.group)) * a.kv.dim;
+}
 
-    static __device__ __forceinline__ const float *angles(const AttnArgs &a, int len, int b, int m) {
-        const int depth = a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
-        return a.rope.table + static_cast<int64_t>(min(len + depth, a.rope.n_pos - 1)) * a.rope.rot;
-    }
-    static __device__ __forceinline__ const float *query(const AttnArgs &a, int b, int head, int m, int r) {
-        return a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + head * a.group + (r - m * a.group)) * D;
-    }
-
-    __device__ __forceinline__ void load(const AttnArgs &a, int len, int b, int head, int row0, int rows) {
-        const int tid = threadIdx.x, half = a.rope.rot / 2;
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-            const int it = tid + k * THREADS, i = it / QUADS, d = it % QUADS * 4;
-            const int r = i < ROWS && row0 + i < rows ? row0 + i : row0;
-            const int m = a.by_group(r);
-            const float *qp = query(a, b, head, m, r);
-            own[k] = gld(reinterpret_cast<const u32x4 *>(qp + d));
-            if (a.rope.mode == SV_ROPE_NONE || a.rope.rot % 8) continue;
-            const bool turn = d < a.rope.rot, second = d >= half;
-            const float *cs = angles(a, len, b, m);
-            if (a.rope.mode == SV_ROPE_PAIRS) {
-                cs += turn ? d : 0;
-                w[k][0] = gld(reinterpret_cast<const u32x2 *>(cs));
-                w[k][1] = gld(reinterpret_cast<const u32x2 *>(cs + 2));
-            } else {
-                const int p = !turn ? 0 : second ? d - half : d;
-                cs += 2 * p;
-#pragma unroll
-                for (int e = 0; e < 4; e++) w[k][e] = gld(reinterpret_cast<const u32x2 *>(cs + 2 * e));
-                other[k] = gld(reinterpret_cast<const u32x4 *>(qp + (second ? p : p + half)));
-            }
+// Requests n rows' queries and, unless a rotation's quads of pairs are not
+// whole, the angles of their positions [position][rot].
+template <int D, int W>
+__device__ __forceinline__ void stage_rows(const AttnArgs &a, int len, int b, int head, int row0, int n, int wave,
+                                           uint32_t staged, uint32_t angles) {
+    const int lane = threadIdx.x & 63;
+    if (a.rope.mode != SV_ROPE_NONE && a.rope.rot % 8 == 0) {
+        const int m0 = a.by_group(row0), of = a.by_group(row0 + n - 1) - m0 + 1;
+        int depth = m0 + lane;
+        if (a.bt.tree && lane < of) depth = __popc(row_mask(a, b, depth) & ((1u << depth) - 1));
+        for (int i = wave; i < of; i += W) {
+            const int pos = min(len + __builtin_amdgcn_readlane(depth, i), a.rope.n_pos - 1);
+            if (lane < a.rope.rot / 4)
+                to_lds<false>(reinterpret_cast<const uint8_t *>(a.rope.table + static_cast<int64_t>(pos) * a.rope.rot + 4 * lane),
+                              angles + i * a.rope.rot * 4);
         }
     }
-
-    __device__ __forceinline__ void store(const AttnArgs &a, int len, int b, int head, int row0, int rows,
-                                          float *to) {
-        typedef float f4 __attribute__((ext_vector_type(4)));
-        const int tid = threadIdx.x, half = a.rope.rot / 2;
-#pragma unroll
-        for (int k = 0; k < N; k++) {
-            const int it = tid + k * THREADS, i = it / QUADS, d = it % QUADS * 4;
-            if (i >= ROWS) continue;
-            const bool live = row0 + i < rows;
-            f4 x = __builtin_bit_cast(f4, own[k]);
-            if (a.rope.mode != SV_ROPE_NONE && d < a.rope.rot) {
-                if (a.rope.rot % 8) {
-                    const int r = live ? row0 + i : row0, m = a.by_group(r);
-                    const float *qp = query(a, b, head, m, r), *cs = angles(a, len, b, m);
+    constexpr int QUADS = D / 4;
 #pragma unroll 1
-                    for (int e = 0; e < 4; e++) {
-                        const int y = d + e;
-                        if (y >= a.rope.rot) break;
-                        const bool pairs = a.rope.mode == SV_ROPE_PAIRS, second = pairs ? y & 1 : y >= half;
-                        const int p = pairs ? y >> 1 : second ? y - half : y;
-                        const int mate = pairs ? y ^ 1 : second ? p : p + half;
-                        const float u = __fmul_rn(gld(qp + y), gld(cs + 2 * p));
-                        const float v = __fmul_rn(gld(qp + mate), gld(cs + 2 * p + 1));
-                        const float z = second ? __fadd_rn(u, v) : __fsub_rn(u, v);
-                        x.x = e == 0 ? z : x.x;
-                        x.y = e == 1 ? z : x.y;
-                        x.z = e == 2 ? z : x.z;
-                        x.w = e == 3 ? z : x.w;
-                    }
-                } else if (a.rope.mode == SV_ROPE_PAIRS) {
-#pragma unroll
-                    for (int e = 0; e < 4; e += 2) {
-                        const float co = __uint_as_float(w[k][e / 2].x), si = __uint_as_float(w[k][e / 2].y);
-                        const float x0 = x[e], x1 = x[e + 1];
-                        x[e] = __fsub_rn(__fmul_rn(x0, co), __fmul_rn(x1, si));
-                        x[e + 1] = __fadd_rn(__fmul_rn(x1, co), __fmul_rn(x0, si));
-                    }
-                } else {
-                    const f4 y = __builtin_bit_cast(f4, other[k]);
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const float u = __fmul_rn(x[e], __uint_as_float(w[k][e].x));
-                        const float v = __fmul_rn(y[e], __uint_as_float(w[k][e].y));
-                        x[e] = d >= half ? __fadd_rn(u, v) : __fsub_rn(u, v);
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 4; e++) x[e] = live ? x[e] * a.scale : 0.0f;
-            *reinterpret_cast<f4 *>(to + i * (D + 4) + d) = x;
-        }
+    for (int at = wave * 64; at < n * QUADS; at += W * 64) {
+        const int i = (at + lane) / QUADS, q = ((at + lane) % QUADS) ^ (i & 7);
+        to_lds<false>(reinterpret_cast<const uint8_t *>(query_of(a, b, head, row0 + min(i, n - 1)) + 4 * q),
+                      staged + at * 16);
     }
-};
+}
 
-// The queries of a row tile as the second operand of S^T = K Q^T, from the
-// staged rows (by reads in asm: the ring's transfers are on their way), for
-// fp16 multiplied by the power of two that brings the row's largest magnitude
-// into [2^12, 2^13); the row's scores are multiplied by the returned power of
-// two to undo that.
+// Turns the staged rows by their angles, four pairs a thread and step.
+template <int D, int THREADS>
+__device__ __forceinline__ void turn_rows(const AttnArgs &a, int len, int b, int row0, int n, uint32_t staged,
+                                          uint32_t angles) {
+    const int rot = a.rope.rot, m0 = a.by_group(row0);
+    if (rot % 8) {  // pair by pair, with the angles where they are
+        for (int it = threadIdx.x; it < n * (rot / 2); it += THREADS) {
+            const int i = it / (rot / 2), p = it - i * (rot / 2), m = a.by_group(row0 + i);
+            const int depth = a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
+            const float *cs = a.rope.table + static_cast<int64_t>(min(len + depth, a.rope.n_pos - 1)) * rot + 2 * p;
+            const int e0 = a.rope.mode == SV_ROPE_PAIRS ? 2 * p : p, e1 = a.rope.mode == SV_ROPE_PAIRS ? e0 + 1 : p + rot / 2;
+            SV_LDS float *x0 = (SV_LDS float *)static_cast<uintptr_t>(quad_at<D>(staged, i, e0 / 4) + e0 % 4 * 4);
+            SV_LDS float *x1 = (SV_LDS float *)static_cast<uintptr_t>(quad_at<D>(staged, i, e1 / 4) + e1 % 4 * 4);
+            const float co = gld(cs), si = gld(cs + 1), u = *x0, v = *x1;
+            *x0 = __fsub_rn(__fmul_rn(u, co), __fmul_rn(v, si));
+            *x1 = __fadd_rn(__fmul_rn(v, co), __fmul_rn(u, si));
+        }
+        return;
+    }
+    const bool pairs = a.rope.mode == SV_ROPE_PAIRS;
+    const int of = rot / 8;
+#pragma unroll 1
+    for (int it = threadIdx.x; it < n * of; it += THREADS) {
+        const int i = a.by_turns(it), k = it - i * of;
+        const uint32_t at0 = quad_at<D>(staged, i, pairs ? 2 * k : k), at1 = quad_at<D>(staged, i, pairs ? 2 * k + 1 : k + of);
+        const uint32_t cs = angles + ((a.by_group(row0 + i) - m0) * rot + 8 * k) * 4;
+        f4 x, y, c0, c1;
+        asm volatile("ds_read_b128 %0, %4\n ds_read_b128 %1, %5\n ds_read_b128 %2, %6\n ds_read_b128 %3, %6 offset:16\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(x), "=&v"(y), "=&v"(c0), "=&v"(c1)
+                     : "v"(at0), "v"(at1), "v"(cs)
+                     : "memory");
+        const f4 u = pairs ? f4{x.x, x.z, y.x, y.z} : x, v = pairs ? f4{x.y, x.w, y.y, y.w} : y;
+        const f4 co = {c0.x, c0.z, c1.x, c1.z}, si = {c0.y, c0.w, c1.y, c1.w};
+        f4 s, t;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            s[e] = __fsub_rn(__fmul_rn(u[e], co[e]), __fmul_rn(v[e], si[e]));
+            t[e] = __fadd_rn(__fmul_rn(v[e], co[e]), __fmul_rn(u[e], si[e]));
+        }
+        x = pairs ? f4{s.x, t.x, s.y, t.y} : s;
+        y = pairs ? f4{s.z, t.z, s.w, t.w} : t;
+        asm volatile("ds_write_b128 %0, %2\n ds_write_b128 %1, %3" ::"v"(at0), "v"(at1), "v"(x), "v"(y) : "memory");
+    }
+}
+
+// The queries of a row tile as the second operand of S^T = K Q^T, from the n
+// staged rows (by reads in asm: the ring's transfers are on their way; lanes
+// past the last row take that one), for fp16 multiplied by the power of two
+// that brings the row's largest magnitude into [2^12, 2^13); the row's scores
+// are multiplied by the returned power of two to undo that.
 template <int TYPE, int D>
-__device__ __forceinline__ float take_queries(uint32_t staged, typename Kind<TYPE>::KVec (&qf)[D / 32][Kind<TYPE>::kq]) {
+__device__ __forceinline__ float take_queries(uint32_t staged, int from, int n, float scale,
+                                              typename Kind<TYPE>::KVec (&qf)[D / 32][Kind<TYPE>::kq]) {
     using Kd = Kind<TYPE>;
     constexpr int NC = D / 32;
-    const int lane = threadIdx.x & 63;
-    const uint32_t at = staged + ((lane & 15) * (D + 4) + 8 * (lane >> 4)) * 4;
+    const int lane = threadIdx.x & 63, i = min(from + (lane & 15), n - 1), g = lane >> 4;
+    const uint32_t at0 = quad_at<D>(staged, i, 2 * g), at1 = quad_at<D>(staged, i, 2 * g + 1);
     float x[NC][8];
     float top = 0.0f;
 #pragma unroll
     for (int c = 0; c < NC; c++) {
-        lds_read8(at + 128 * c, x[c]);
+        lds_read8(at0 + 128 * c, at1 + 128 * c, x[c]);
 #pragma unroll
-        for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[c][e]));
+        for (int e = 0; e < 8; e++) {
+            x[c][e] *= scale;
+            top = fmaxf(top, fabsf(x[c][e]));
+        }
     }
     float back = 1.0f;
     if constexpr (__is_same(typename Kd::KVec, h8)) {
@@ -549,28 +540,34 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
         advance();
     };
     auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
-    Rows<D, ROWS, 64 * W> staged;
-    staged.load(a, len, b, head, row0, rows);
-    if (any) {
+    const uint32_t staged = ring + S::STAGED, angles = ring + S::ANGLES;
+    const int n_rows = min(ROWS, rows - row0);
+    stage_rows<D, W>(a, len, b, head, row0, n_rows, wave, staged, angles);
+    if (S::FIRST && any) {
         request_k();
         turn();
         request_v();
         turn();
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::LOADS + S::SCALES) : "memory");  // all but the block
+    } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     }
-    staged.store(a, len, b, head, row0, rows, reinterpret_cast<float *>(s_mem + S::STAGED));
 
-    // ---- queries, once every wave has stored its pieces
-    asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
+    // ---- queries, once every wave's pieces are there
+    asm volatile("s_barrier" ::: "memory");
+    if (a.rope.mode != SV_ROPE_NONE) {
+        turn_rows<D, 64 * W>(a, len, b, row0, n_rows, staged, angles);
+        asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
+    }
     typename Kd::KVec qf[RT][NC][Kd::kq];
     float rs[RT];
 #pragma unroll
-    for (int t = 0; t < RT; t++)
-        rs[t] = take_queries<TYPE, D>(ring + S::STAGED + 16 * t * LD * 4, qf[t]);
-    if constexpr (S::N > 2) {
-        if constexpr (S::INSIDE) asm volatile("s_barrier" ::: "memory");  // every wave has its queries
+    for (int t = 0; t < RT; t++) rs[t] = take_queries<TYPE, D>(staged, 16 * t, n_rows, a.scale, qf[t]);
+    if constexpr (S::FIRST < S::N / 2) {
+        asm volatile("s_barrier" ::: "memory");  // every wave has its queries
         if (any) {
 #pragma unroll
-            for (int i = 1; i < S::N / 2; i++) {
+            for (int i = S::FIRST; i < S::N / 2; i++) {
                 request_k();
                 turn();
                 request_v();
@@ -600,8 +597,9 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
         } else {
             ring_read<S::LEAVE_K, 1024, 32, 2 * NC>(
                 mine + slot * (W * S::HALF) + (g * 32 + 8 * (col >> 2) + (col & 3)) * 8, kr);
-            lds_read8(mine_scales + (slot >> 1) * (W * 256) + 32 * g, ks);
-            lds_read8(mine_scales + (slot >> 1) * (W * 256) + 128 + 32 * g, vs);
+            const uint32_t at = mine_scales + (slot >> 1) * (W * 256) + 32 * g;
+            lds_read8(at, at + 16, ks);
+            lds_read8(at + 128, at + 144, vs);
         }
         request_k();
         turn();
