@@ -141,6 +141,7 @@ __device__ __forceinline__ int lane_rank(unsigned long long mask) {
 }
 
 __global__ __launch_bounds__(kBookThreads) void kv_init_kernel(KvDev kv) {
+    fetch_args<sizeof(KvDev)>();
     const int64_t n = static_cast<int64_t>(kv.seqs) * kv.width;
     const int64_t step = static_cast<int64_t>(gridDim.x) * kBookThreads;
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kBookThreads + threadIdx.x;
@@ -184,6 +185,7 @@ __device__ int reserve_row(const KvDev &kv, const sv_kv_batch &bt, int b, bool f
 }
 
 __global__ __launch_bounds__(kBookThreads) void kv_reserve_kernel(KvDev kv, sv_kv_batch bt) {
+    fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch)>();
     __shared__ int cnt[SV_KV_MAX_SEQS];
     __shared__ int over;
     const int tid = threadIdx.x, wave = tid >> 6;
@@ -264,6 +266,7 @@ __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int
 }
 
 __global__ __launch_bounds__(kBookThreads) void kv_release_kernel(KvDev kv, const int32_t *ids, int n) {
+    fetch_args<sizeof(KvDev) + 16>();
     __shared__ int from[SV_KV_MAX_SEQS];
     __shared__ int cnt[SV_KV_MAX_SEQS + 1];
     for (int b = threadIdx.x >> 6; b < n; b += kBookWaves) {
@@ -297,6 +300,7 @@ __device__ int kept_rows(const sv_kv_batch &bt, const int32_t *accepted, int str
 
 __global__ __launch_bounds__(kBookThreads) void kv_commit_kernel(KvDev kv, sv_kv_batch bt, const int32_t *accepted,
                                                                  int stride, const int32_t *path) {
+    fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + 24>();
     __shared__ int from[SV_KV_MAX_SEQS];
     __shared__ int cnt[SV_KV_MAX_SEQS + 1];
     const int64_t cap = static_cast<int64_t>(kv.width) * kv.page;
@@ -327,6 +331,7 @@ __global__ __launch_bounds__(kBookThreads) void kv_commit_kernel(KvDev kv, sv_kv
 // dependent page lookups and copies; the moved rows are a few KB.
 __global__ __launch_bounds__(256) void kv_commit_move_kernel(KvDev kv, sv_kv_batch bt, const int32_t *accepted,
                                                              int stride, const int32_t *path) {
+    fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + 24>();
     __shared__ int s_kept, s_sid;
     const int b = blockIdx.y, head = blockIdx.x % kv.heads, layer = blockIdx.x / kv.heads;
     if (threadIdx.x < 64) {
@@ -383,6 +388,7 @@ __global__ __launch_bounds__(256) void kv_commit_move_kernel(KvDev kv, sv_kv_bat
 
 __global__ __launch_bounds__(kBookThreads) void kv_fork_kernel(KvDev kv, const int32_t *src, const int32_t *dst,
                                                                int n) {
+    fetch_args<sizeof(KvDev) + 24>();
     __shared__ int cnt[SV_KV_MAX_SEQS];
     __shared__ int bad;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -447,6 +453,7 @@ __global__ __launch_bounds__(kBookThreads) void kv_fork_kernel(KvDev kv, const i
 // Copies the used blocks of the part-filled pages, one workgroup per (head
 // and layer, pair): contiguous 16-byte pieces, bound by memory bandwidth.
 __global__ __launch_bounds__(256) void kv_fork_copy_kernel(KvDev kv, const int32_t *src, const int32_t *dst, int n) {
+    fetch_args<sizeof(KvDev) + 24>();
     if (gld(kv.ctl + 2) != n) return;  // the bookkeeping refused the call
     const int i = blockIdx.y, head = blockIdx.x % kv.heads, layer = blockIdx.x / kv.heads;
     const int s = gld(src + i), d = gld(dst + i);
@@ -466,6 +473,7 @@ __global__ __launch_bounds__(256) void kv_fork_copy_kernel(KvDev kv, const int32
 // moves[n_pages] (its old id).
 __global__ __launch_bounds__(kBookThreads) void kv_compact_kernel(KvDev kv, int32_t *map, int32_t *holes,
                                                                   int32_t *moves) {
+    fetch_args<sizeof(KvDev) + 24>();
     __shared__ int cnt[kBookThreads];
     const int tid = threadIdx.x;
     const int fc = min(max(gld(kv.ctl), 0), kv.n_pages), live = kv.n_pages - fc;
@@ -509,6 +517,7 @@ __global__ __launch_bounds__(kBookThreads) void kv_compact_kernel(KvDev kv, int3
 constexpr int kPiece = 16384;
 __global__ __launch_bounds__(256) void kv_compact_move_kernel(KvDev kv, const int32_t *map, const int32_t *holes,
                                                               const int32_t *moves) {
+    fetch_args<sizeof(KvDev) + 24>();
     const int n_moves = gld(kv.ctl + 2);
     const int fc = min(max(gld(kv.ctl), 0), kv.n_pages), live = kv.n_pages - fc;
     const int64_t entries = static_cast<int64_t>(kv.seqs) * kv.width;
@@ -566,6 +575,7 @@ constexpr int kPad = 4;  // floats past a staged row, against bank conflicts
 template <int TYPE>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_kv_batch bt, const float *k,
                                                         const float *v, sv_kv_rope rope) {
+    fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + sizeof(sv_kv_rope) + 24>();
     extern __shared__ float rows[];  // [32][dim + kPad]
     __shared__ float scale[kBlk];
     __shared__ int s_sid;
@@ -725,6 +735,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_
 template <int TYPE>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvDev kv, int layer, sv_kv_batch bt, const int32_t *start,
                                                       float *k_out, float *v_out) {
+    fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + 32>();
     extern __shared__ float rows[];  // [32][dim + kPad]
     const int tid = threadIdx.x, b = blockIdx.y;
     const int head = blockIdx.x % kv.heads, nth = blockIdx.x / kv.heads;

@@ -14,6 +14,7 @@ namespace sv {
 // do not depend on how many chunks a launch provides for.
 constexpr int kJoin = 256, kJoinTile = 1024;
 __global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
+    fetch_args<sizeof(AttnArgs)>();
     __shared__ float s_w[kJoinTile], s_wl[kJoinTile];
     __shared__ __align__(16) float s_v[kJoin * 4];
     __shared__ float s_l[kJoin / 8], s_top[kJoin / 64];

@@ -61,20 +61,33 @@ struct Kind<SV_KV_I8> {
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-// x = sum of N parts of the narrow type, each the rounding of what is left.
+// x = sum of N parts of the narrow type, each the rounding of what is left
+// (for fp16 taken off by a fused multiply-add, which reads the half).
 template <int N, typename V8>
 __device__ __forceinline__ void split8(const float (&x)[8], V8 (&part)[N]) {
-    float left[8];
+    typedef decltype(part[0][0] + part[0][0]) E;
+    typedef E E2 __attribute__((ext_vector_type(2)));
+    typedef float f2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int e = 0; e < 8; e++) left[e] = x[e];
+    for (int e = 0; e < 8; e += 2) {
+        f2 left = {x[e], x[e + 1]};
 #pragma unroll
-    for (int n = 0; n < N; n++)
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const auto h = static_cast<decltype(part[0][0] + part[0][0])>(left[e]);
-            part[n][e] = h;
-            left[e] -= static_cast<float>(h);
+        for (int n = 0; n < N; n++) {
+            const E2 h = __builtin_convertvector(left, E2);
+            part[n][e] = h.x;
+            part[n][e + 1] = h.y;
+            if (n + 1 == N) break;
+            if constexpr (__is_same(E, _Float16)) {
+                left.x = __builtin_fmaf(static_cast<float>(h.x), -1.0f, left.x);
+                left.y = __builtin_fmaf(static_cast<float>(h.y), -1.0f, left.y);
+            } else {
+                uint32_t u;
+                __builtin_memcpy(&u, &h, 4);
+                left.x -= __uint_as_float(u << 16);
+                left.y -= __uint_as_float(u & 0xFFFF0000u);
+            }
         }
+    }
 }
 
 // w y as the products of w's parts make it, for a y that is not finite.
@@ -444,6 +457,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
     AttnArgs a) {
     using Kd = Kind<TYPE>;
     using S = Shape<TYPE, D, RT, WIDE>;
+    fetch_args<sizeof(AttnArgs)>();
     constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz, W = S::W, LD = S::LD, ROWS = S::ROWS;
     constexpr bool ONCE = D <= 128 && RT < 4;  // one row group
     extern __shared__ __align__(1024) uint8_t s_mem[];
@@ -624,7 +638,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
             for (int t = 0; t < RT; t++)
 #pragma unroll
                 for (int e = 0; e < 8; e++) {
-                    p[t][e] = acc[t][e >> 2][e & 3] * rs[t];
+                    p[t][e] = acc[t][e >> 2][e & 3];
                     if constexpr (TYPE == SV_KV_I8) p[t][e] *= ks[e];
                 }
         }
@@ -672,16 +686,18 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
             float top = p[t][0];
 #pragma unroll
             for (int e = 1; e < 8; e++) top = fmaxf(top, p[t][e]);
-            const float now = fmaxf(mx[t], row_max(top));
+            // The running maximum is taken up to a whole number: what it
+            // changes by scales exactly, and seldom changes at all.
+            const float now = fmaxf(mx[t], ceilf(row_max(top) * rs[t]));
             const float base = now == -INFINITY ? 0.0f : now;
             const float keep = __builtin_amdgcn_exp2f(mx[t] - base);
             mx[t] = now;
             // fp16 weights are taken times 2^15 (l too, so it cancels)
-            constexpr float kUp = TYPE == SV_KV_F16 ? 15.0f : 0.0f;
+            const float less = TYPE == SV_KV_F16 ? 15.0f - base : -base;
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
-                p[t][e] = __builtin_amdgcn_exp2f(p[t][e] - base + kUp);
+                p[t][e] = __builtin_amdgcn_exp2f(TYPE == SV_KV_BF16 ? p[t][e] + less : __builtin_fmaf(p[t][e], rs[t], less));
                 sum += p[t][e];
             }
             l[t] = l[t] * keep + sum;
@@ -691,7 +707,11 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
             }
             if constexpr (TYPE == SV_KV_I8) {
 #pragma unroll
-                for (int e = 0; e < 8; e++) p[t][e] = p[t][e] == 0.0f ? 0.0f : p[t][e] * vs[e];
+                for (int e = 0; e < 8; e++) p[t][e] *= vs[e];
+                if (edge) {  // scales of hidden slots may be anything
+#pragma unroll
+                    for (int e = 0; e < 8; e++) p[t][e] = seen[t] >> e & 1u ? p[t][e] : 0.0f;
+                }
             }
         }
 

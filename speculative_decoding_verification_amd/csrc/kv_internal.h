@@ -35,6 +35,19 @@ int kv_check(const sv_kv *kv, const char *who, KvDev *out);
 int kv_check_batch(const KvDev &kv, const sv_kv_batch *b, const char *who, int max_m);
 int kv_check_rope(const KvDev &kv, const sv_kv_rope *r, const char *who);
 
+// Requests all BYTES of a kernel's arguments at its start, line by line but
+// together: a kernel begins with none of them in the scalar cache, and fields
+// first used one after another would each wait for their own line.
+template <int BYTES>
+__device__ __forceinline__ void fetch_args() {
+    typedef const __attribute__((address_space(4))) uint32_t *Args;
+    const Args at = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < BYTES; i += 64) all |= at[i / 4];
+    asm volatile("" ::"s"(all));
+}
+
 // The page of an entry, or -1 where the row has none.
 __device__ __forceinline__ int kv_page_of(const KvDev &kv, int sid, int64_t entry) {
     if (entry < 0 || entry >= kv.width) return -1;
