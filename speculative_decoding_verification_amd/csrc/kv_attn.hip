@@ -7,83 +7,210 @@
 namespace sv {
 
 // The join of a row's chunks c: with M = max m_c,
-//   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c,
-// one workgroup a row; its threads take four elements each of the head
-// dimension and one of `parts` shares of the chunks (chunk number modulo
-// parts, each share in chunk order, then the shares in order), so the sums
-// do not depend on how many chunks a launch provides for.
-constexpr int kJoin = 256, kJoinTile = 1024;
-__global__ __launch_bounds__(kJoin) void kv_attn_join_kernel(AttnArgs a) {
+//   out = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c
+// in kShares shares (chunk number modulo kShares), each in chunk order, then
+// the shares in order: the sums depend neither on how many chunks a launch
+// provides for nor on the kernel that forms them.
+//
+// Both kernels are bound by latency: the sequence, its length, the maxima and
+// the sums are loads that wait for one another, so what is likely to be used
+// is requested before the length is known.
+constexpr int kShares = 8, kJoin = 256;
+typedef float f4 __attribute__((ext_vector_type(4)));
+
+struct Parts {
+    const float *o, *m, *l;  // of the row's first chunk
+    int64_t step;            // rows between chunks
+    int D;
+    __device__ Parts(const AttnArgs &a, int b, int head, int r) {
+        const int64_t base = (static_cast<int64_t>(b) * a.kv.heads + head) * a.chunks * a.rows + r;
+        step = a.rows;
+        D = a.kv.dim;
+        o = a.part_o + base * D;
+        m = a.part_m + base;
+        l = a.part_l + base;
+    }
+    __device__ float m_at(int c) const { return gld(m + c * step); }
+    __device__ float l_at(int c) const { return gld(l + c * step); }
+    __device__ f4 o_at(int c, int d) const { return *(const SV_GLOBAL f4 *)(o + c * step * D + d); }
+};
+// The launch's chunks are two runs of consecutive chunk numbers: [0, first)
+// as they are, the others `jump - first` ahead of their index.
+struct Run {
+    int from, to, shift;
+    __device__ Run(const Span &sp, int n, int nth)
+        : from(nth ? sp.first : 0), to(nth ? n : min(n, sp.first)), shift(nth ? sp.jump - sp.first : 0) {}
+};
+__device__ __forceinline__ void flag_over(const AttnArgs &a, const Span &sp) {
+    if (a.max_len && sp.len + sp.n > a.max_len) kv_flag(a.kv, SV_KV_OVER_MAX);
+}
+__device__ __forceinline__ f4 joined(const AttnArgs &a, const Span &sp, f4 x, float sum) {
+    if (a.max_len && sp.len + sp.n > a.max_len) return f4{NAN, NAN, NAN, NAN};
+    return x * (sum != 0.0f ? 1.0f / sum : 0.0f);
+}
+
+// Few rows: one workgroup each, a share to every dim / 4 threads (64 threads
+// a share at most).
+constexpr int kWeights = 1024, kAhead = 8;
+__global__ __launch_bounds__(512) void kv_attn_join_kernel(AttnArgs a) {
+    __shared__ float s_w[kWeights], s_wl[kWeights];
+    __shared__ __align__(16) float s_v[kShares * kMaxDim];
+    __shared__ float s_l[kShares], s_top[8];
     fetch_args<sizeof(AttnArgs)>();
-    __shared__ float s_w[kJoinTile], s_wl[kJoinTile];
-    __shared__ __align__(16) float s_v[kJoin * 4];
-    __shared__ float s_l[kJoin / 8], s_top[kJoin / 64];
-    typedef float f4 __attribute__((ext_vector_type(4)));
-    const int r = blockIdx.x, head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
+    const int r = blockIdx.x, head = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, threads = blockDim.x;
+    const int D = a.kv.dim, quads = D / 4;
+    const Parts at(a, b, head, r);
+    const int group = tid / quads, d = (tid - group * quads) * 4;
+    const bool own = group < kShares;
+    float m_ahead = 0.0f, l_ahead = 0.0f;
+    f4 ahead[kAhead];
+    if (tid < a.chunks) {
+        m_ahead = at.m_at(tid);
+        l_ahead = at.l_at(tid);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; k++) {
+        const int c = group + k * kShares;
+        ahead[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (own && c < a.chunks) ahead[k] = at.o_at(c, d);
+    }
     const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
     const Span sp = span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), kv_rows_of(a.bt.n_new, b, a.bt.M));
     if (r >= sp.n * a.group) return;
-    const int D = a.kv.dim, quads = D / 4, parts = kJoin / quads;
     const int n = chunks_of(a, sp);
-    const int64_t base = (static_cast<int64_t>(b) * a.kv.heads + head) * a.chunks * a.rows + r;
-    float top = -INFINITY;
-    for (int c = tid; c < n; c += kJoin) top = fmaxf(top, gld(a.part_m + base + static_cast<int64_t>(c) * a.rows));
+    float top = tid < n ? m_ahead : -INFINITY;
+    for (int c = tid + threads; c < n; c += threads) top = fmaxf(top, at.m_at(c));
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o, 64));
     if ((tid & 63) == 0) s_top[tid >> 6] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(s_top[0], s_top[1]), fmaxf(s_top[2], s_top[3]));
-    const int part = tid / quads, d = tid % quads * 4;
+    for (int i = 0; i < threads / 64; i++) top = fmaxf(top, s_top[i]);
     f4 v = {0.0f, 0.0f, 0.0f, 0.0f};
     float l = 0.0f;
-    for (int at = 0; at < n && top != -INFINITY; at += kJoinTile) {
-        const int upto = min(n - at, kJoinTile);
-        for (int i = tid; i < upto; i += kJoin) {
-            const int64_t c = base + static_cast<int64_t>(at + i) * a.rows;
-            const float w = __builtin_amdgcn_exp2f(gld(a.part_m + c) - top);
+    // its share: that of the places loaded ahead, which past the sinks are
+    // `jump - first` ahead of their index
+    const int share = (group + (sp.jump - sp.first)) % kShares;
+    for (int from = 0; from < n && top != -INFINITY; from += kWeights) {
+        const int upto = min(n - from, kWeights);
+        for (int i = tid; i < upto; i += threads) {
+            const bool held = from + i == tid;
+            const float w = __builtin_amdgcn_exp2f((held ? m_ahead : at.m_at(from + i)) - top);
             s_w[i] = w;
-            s_wl[i] = w * gld(a.part_l + c);
+            s_wl[i] = w * (held ? l_ahead : at.l_at(from + i));
         }
         __syncthreads();
-        if (part < parts) {
-            // the chunks of the sinks and those after them: two runs of
-            // consecutive chunk numbers
-            for (int run = 0; run < 2; run++) {
-                const int lo = max(at, run ? sp.first : 0), hi = min(at + upto, run ? n : sp.first);
-                const int shift = run ? sp.jump - sp.first : 0;
-                int c = lo + ((part - (lo + shift)) % parts + parts) % parts;
+        if (own) {
+            for (int nth = 0; nth < 2; nth++) {
+                const Run run(sp, n, nth);
+                const int lo = max(run.from, from), hi = min(run.to, from + upto);
+                int c = lo + ((share - (lo + run.shift)) % kShares + kShares) % kShares;
+#pragma unroll
+                for (int k = 0; k < kAhead; k++)
+                    if (c == group + k * kShares && c < hi) {
+                        v += s_w[c - from] * ahead[k];
+                        l += s_wl[c - from];
+                        c += kShares;
+                    }
 #pragma unroll 4
-                for (; c < hi; c += parts) {
-                    v += s_w[c - at] * *(const SV_GLOBAL f4 *)(a.part_o + (base + static_cast<int64_t>(c) * a.rows) * D + d);
-                    l += s_wl[c - at];
+                for (; c < hi; c += kShares) {
+                    v += s_w[c - from] * at.o_at(c, d);
+                    l += s_wl[c - from];
                 }
             }
         }
         __syncthreads();
     }
-    if (part < parts) {
-        *reinterpret_cast<f4 *>(s_v + part * D + d) = v;
-        if (d == 0) s_l[part] = l;
+    if (own) {
+        *reinterpret_cast<f4 *>(s_v + share * D + d) = v;
+        if (d == 0) s_l[share] = l;
     }
     __syncthreads();
-    float x = 0.0f;
-    if (tid < D) {
-        float sum = s_l[0];
-        x = s_v[tid];
-        for (int i = 1; i < parts; i++) {
-            x += s_v[i * D + tid];
+    f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum = 0.0f;
+    if (tid < quads) {
+        for (int i = 0; i < kShares; i++) {
+            x += *reinterpret_cast<f4 *>(s_v + i * D + 4 * tid);
             sum += s_l[i];
         }
-        const bool over = a.max_len && sp.len + sp.n > a.max_len;
-        if (over && tid == 0) kv_flag(a.kv, SV_KV_OVER_MAX);
-        x = over ? NAN : x * (sum != 0.0f ? 1.0f / sum : 0.0f);
+        if (tid == 0) flag_over(a, sp);
+        // its own place in the first share's sums
+        *reinterpret_cast<f4 *>(s_v + 4 * tid) = joined(a, sp, x, sum);
     }
-    __syncthreads();
-    if (tid < D) s_v[tid] = x;
     __syncthreads();
     finish_rows(a, s_v, D, b, head, r, 1);
 }
+
+// Many rows: dim / 4 threads each, which hold the shares' sums in registers.
+__global__ __launch_bounds__(kJoin) void kv_attn_join_rows_kernel(AttnArgs a) {
+    __shared__ __align__(16) float s_v[kJoin * 4];
+    fetch_args<sizeof(AttnArgs)>();
+    const int D = a.kv.dim, quads = D / 4, of = kJoin / quads;
+    const int head = blockIdx.y, b = blockIdx.z, row0 = blockIdx.x * of, tid = threadIdx.x;
+    const int i = tid / quads, d = (tid - i * quads) * 4, r = row0 + min(i, of - 1);
+    const Parts at(a, b, head, min(r, a.rows - 1));
+    float m[kAhead];
+#pragma unroll
+    for (int c = 0; c < kAhead; c++) m[c] = c < a.chunks ? at.m_at(c) : 0.0f;
+    const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
+    if (sid < 0 || sid >= a.kv.seqs) return;
+    const Span sp = span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), kv_rows_of(a.bt.n_new, b, a.bt.M));
+    const int rows = min(sp.n * a.group - row0, of);
+    if (rows <= 0) return;
+    const int n = chunks_of(a, sp);
+    if (i < rows) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kAhead; c++) top = c < n ? fmaxf(top, m[c]) : top;
+#pragma unroll 8
+        for (int c = kAhead; c < n; c++) top = fmaxf(top, at.m_at(c));
+        f4 v[kShares];
+        float s[kShares];
+#pragma unroll
+        for (int k = 0; k < kShares; k++) {
+            v[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
+            s[k] = 0.0f;
+        }
+        for (int nth = 0; nth < 2 && top != -INFINITY; nth++) {
+            const Run run(sp, n, nth);
+            // rounds of one chunk of each share
+            for (int c0 = run.from - ((run.from + run.shift) & (kShares - 1)); c0 < run.to; c0 += kShares) {
+                f4 o[kShares];
+                float mc[kShares], lc[kShares];
+#pragma unroll
+                for (int k = 0; k < kShares; k++) {
+                    const int c = c0 + k;
+                    const bool in = c >= run.from && c < run.to;
+                    o[k] = in ? at.o_at(c, d) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+                    mc[k] = in ? at.m_at(c) : -INFINITY;
+                    lc[k] = in ? at.l_at(c) : 0.0f;
+                }
+#pragma unroll
+                for (int k = 0; k < kShares; k++) {
+                    const float w = __builtin_amdgcn_exp2f(mc[k] - top);
+                    v[k] += w * o[k];
+                    s[k] += w * lc[k];
+                }
+            }
+        }
+        f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        float sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kShares; k++) {
+            x += v[k];
+            sum += s[k];
+        }
+        if (i == 0 && d == 0) flag_over(a, sp);
+        *reinterpret_cast<f4 *>(s_v + i * D + d) = joined(a, sp, x, sum);
+    }
+    __syncthreads();
+    finish_rows(a, s_v, D, b, head, row0, rows);
+}
+
+// Rows from which the second kernel is taken: with ten workgroups of one row
+// to a compute unit (us: 3200 rows of 128 in 13 chunks 10.5 against 8.0, 2048
+// rows of 64 in 22 chunks 8.4 against 9.0).
+constexpr int64_t kManyRows = 2560;
 
 // Chunks that a sequence can have: of its whole length, or of what a window
 // and the sinks can touch.
@@ -98,15 +225,15 @@ static int64_t chunks_within(int64_t bound, int64_t window, int64_t sinks, int64
 // the launch is one round of workgroups (256 compute units hold one wide or
 // two narrow workgroups each).  Without a window the sequences of a batch are
 // seldom all as long as the longest: half a round more is allowed for.  Past
-// one round of 2048 the length evens out the last round.  Measured in us, 128
-// heads of 8 and a group of 5:
-//   5 x 4099 slots, 8 heads, fp16          256: 22, 384: 25, 640: 37
-//   8 rows, window 1024, 8 heads of 96     384: 24, 512: 20, 640: 24
-//   4 trees of up to 8191, 8 heads of 64   256: 50, 384: 36, 512: 43
-//   16 sequences up to 16384, int8         1024: 94, 1536: 90, 2048: 98
-//   32 sequences, window 4096, fp16        1024: 152, 1536: 148, 2048: 166
-// A sequence that fits one short chunk needs no join (300 slots: 11 against
-// 14 with chunks of 256).
+// one round of 2048, chunks short enough to even out the last round.  Measured
+// in us, heads of 128 and groups of 5 where nothing else is said:
+//   5 x 4099 slots, 8 heads, fp16          256: 20, 384: 22, 640: 23
+//   8 rows, window 1024, 8 heads of 96     384: 22, 512: 17, 640: 22
+//   4 trees of up to 8191, 8 heads of 64   256: 36, 384: 28, 512: 31
+//   16 sequences up to 16384, int8         1024: 93, 1280: 88, 2048: 102
+//   32 sequences, window 4096, fp16        1024: 131, 1280: 129, 2048: 137
+// A sequence that fits one short chunk needs no join (300 slots: 9 us against
+// 12 with chunks of 256).
 static int chunk_rule(int64_t B, int64_t heads, int dim, int64_t bound, int64_t window, int64_t sinks) {
     if (bound <= 512) return static_cast<int>((bound + 127) / 128 * 128);
     for (int c = 256; c <= 2048; c += 128) {
@@ -118,7 +245,7 @@ static int chunk_rule(int64_t B, int64_t heads, int dim, int64_t bound, int64_t 
                                                                : pairs * ((bound + c - 1) / c);
         if (units <= room) return c;
     }
-    return 1536;
+    return 1280;
 }
 
 struct Plan {
@@ -231,6 +358,10 @@ extern "C" int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch
          : d.type == SV_KV_BF16 ? attn_launch_bf16(a, p.rt, p.units, st)
                                 : attn_launch_i8(a, p.rt, p.units, st);
     if (rc || a.chunks == 1) return rc;
-    hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(kJoin), 0, st, a);
+    const int of = kJoin / (d.dim / 4);
+    if (static_cast<int64_t>(a.rows) * d.heads * batch->B >= kManyRows)
+        hipLaunchKernelGGL(kv_attn_join_rows_kernel, dim3((a.rows + of - 1) / of, d.heads, batch->B), dim3(kJoin), 0, st, a);
+    else
+        hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(d.dim <= 128 ? 256 : 512), 0, st, a);
     return hip_check(hipGetLastError(), "kv_attention join launch");
 }

@@ -268,18 +268,20 @@ __device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to) {
     __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, 0, ONCE ? 2 : 0);
 }
 
-// WIDE: twice the waves a workgroup, and one workgroup a compute unit instead
-// of two.
+// Waves and their rings.  Where the registers of two waves fit a SIMD (int8,
+// and fp16 up to 128: bf16's queries take half as much again) a compute unit
+// holds eight with 16 KB of ring each, else four with 32 KB.  WIDE: all of
+// them in one workgroup instead of two.
 template <int TYPE, int D, int RT, bool WIDE>
 struct Shape {
     using Kd = Kind<TYPE>;
-    static constexpr int W = (TYPE == SV_KV_I8 ? 4 : 2) * (WIDE ? 2 : 1);  // waves
+    static constexpr bool TWO = TYPE == SV_KV_I8 || (TYPE == SV_KV_F16 && D <= 128);
+    static constexpr int W = (TWO ? 4 : 2) * (WIDE ? 2 : 1);    // waves
     static constexpr int HALF = 32 * D * Kd::esz;               // bytes of a block's keys, or values
     static constexpr int LOADS = HALF / 1024;                   // transfers of a half
     static constexpr int SCALES = TYPE == SV_KV_I8 ? 1 : 0;     // and one of both scales with the keys
-    // halves of a wave's ring: 32 KB (int8: 16 KB, the workgroup has twice
-    // the waves), and at least a block
-    static constexpr int RING = TYPE == SV_KV_I8 ? 16384 : 32768;
+    // halves of a wave's ring, at least a block
+    static constexpr int RING = TWO ? 16384 : 32768;
     static constexpr int FIT = RING / HALF / 2 * 2;
     static constexpr int N = FIT < 2 ? 2 : FIT > 8 ? 8 : FIT;
     // [half][wave], then the scales [block][wave]
@@ -424,36 +426,46 @@ __device__ __forceinline__ float take_queries(uint32_t staged, int from, int n, 
     return back;
 }
 
-// The sequence whose chunk (counted over the sequences, once per head) has
-// number u, and the chunks ahead of it; -1 past the last.  B lengths are
-// read by the lanes, so that no workgroup is spent on a chunk that the
-// longest sequence has and another has not.
-__device__ __forceinline__ int find_chunk(const AttnArgs &a, int u, int *before) {
+// The sequence, head and chunk of number u.  B lengths are read by the lanes,
+// so that no workgroup is spent on a chunk that the longest sequence has and
+// another has not.  The sinks' chunks, of few slots, come after all others:
+// they fill the last round.
+struct Unit {
+    int b, head, c;  // b = -1 past the last
+};
+__device__ __forceinline__ Unit find_unit(const AttnArgs &a, int u) {
     const int lane = threadIdx.x & 63;
     int passed = 0;
-    for (int b0 = 0; b0 < a.bt.B; b0 += 64) {
-        const int b = b0 + lane;
-        int own = 0;
-        if (b < a.bt.B) {
-            const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
-            if (sid >= 0 && sid < a.kv.seqs) {
-                const int n = kv_rows_of(a.bt.n_new, b, a.bt.M);
-                if (n) own = chunks_of(a, span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), n)) * a.kv.heads;
+    for (int sinks = 0; sinks <= (a.sinks ? 1 : 0); sinks++)
+        for (int b0 = 0; b0 < a.bt.B; b0 += 64) {
+            const int b = b0 + lane;
+            int own = 0, first = 0;
+            if (b < a.bt.B) {
+                const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
+                if (sid >= 0 && sid < a.kv.seqs) {
+                    const int n = kv_rows_of(a.bt.n_new, b, a.bt.M);
+                    if (n) {
+                        const Span sp = span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), n);
+                        const int chunks = chunks_of(a, sp);
+                        first = min(sp.first, chunks);
+                        own = sinks ? first : chunks - first;
+                    }
+                }
             }
+            const int upto = scan64(own * a.kv.heads), all = __builtin_amdgcn_readlane(upto, 63);
+            if (passed + all > u) {
+                const int at = __ffsll(__ballot(passed + upto > u)) - 1;
+                const int n = __builtin_amdgcn_readlane(own, at);
+                const int i = u - passed - __builtin_amdgcn_readlane(upto, at) + n * a.kv.heads, head = i / n;
+                return Unit{b0 + at, head, i - head * n + (sinks ? 0 : __builtin_amdgcn_readlane(first, at))};
+            }
+            passed += all;
         }
-        const int upto = scan64(own), all = __builtin_amdgcn_readlane(upto, 63);
-        if (passed + all > u) {
-            const int at = __ffsll(__ballot(passed + upto > u)) - 1;
-            *before = passed + __builtin_amdgcn_readlane(upto - own, at);
-            return b0 + at;
-        }
-        passed += all;
-    }
-    return -1;
+    return Unit{-1, 0, 0};
 }
 
 template <int TYPE, int D, int RT, bool WIDE>
-__global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_I8 ? 2 : 1)) void kv_attn_kernel(
+__global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (Shape<TYPE, D, RT, WIDE>::TWO ? 2 : 1)) void kv_attn_kernel(
     AttnArgs a) {
     using Kd = Kind<TYPE>;
     using S = Shape<TYPE, D, RT, WIDE>;
@@ -470,29 +482,21 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (TYPE == SV_KV_
     const int x = blockIdx.x;
     const int u8 = a.by_tiles(x / 8), tile = x / 8 - u8 * a.tiles, u = u8 * 8 + x % 8;
     const bool alone = a.chunks == 1;  // no join: this workgroup finishes the rows
-    int b, head, c;
+    Unit unit;
     if (alone) {
-        b = a.by_heads(u);
-        head = u - b * heads;
-        c = 0;
+        unit.b = a.by_heads(u);
+        unit.head = u - unit.b * heads;
+        unit.c = 0;
     } else {
-        int before = 0;
-        b = find_chunk(a, u, &before);
-        if (b < 0) return;
-        head = u - before;  // for now: the sequence's chunk, over its heads
-        c = -1;
+        unit = find_unit(a, u);
+        if (unit.b < 0) return;
     }
+    const int b = unit.b, head = unit.head, c = unit.c;
     if (b >= a.bt.B) return;
     const int sid = a.bt.seq ? __builtin_amdgcn_readfirstlane(gld(a.bt.seq + b)) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
     const int len = __builtin_amdgcn_readfirstlane(static_cast<int>(kv_len_of(a.kv, sid)));
     const Span sp = span_of(a, len, __builtin_amdgcn_readfirstlane(kv_rows_of(a.bt.n_new, b, a.bt.M)));
-    if (c < 0) {
-        const int n_chunks = chunks_of(a, sp);
-        const int h = head / n_chunks;
-        c = head - h * n_chunks;
-        head = h;
-    }
     const int row0 = tile * ROWS, rows = sp.n * a.group;  // of this sequence, in use
     if (row0 >= rows) return;
 

@@ -600,6 +600,44 @@ def test_a_row_does_not_depend_on_the_others(kind, window, sinks, tree, group, d
             assert np.array_equal(host(out)[0, 0], want[b, m]), (m, b)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("heads,group,dim,M,mode,rot", [
+    (1, 3, 32, 16, 2, 24), (2, 4, 64, 16, 1, 64), (1, 5, 96, 5, 2, 20), (2, 5, 128, 5, 2, 128), (1, 2, 160, 9, 1, 160),
+    (1, 3, 192, 4, 2, 96), (1, 1, 224, 16, 1, 6), (1, 16, 256, 1, 2, 256)])
+def test_long_chunks(kind, heads, group, dim, M, mode, rot):
+    """Chunks of more than 512 slots, one and several a sequence."""
+    c = Case(KINDS[kind], heads, group, dim, 32, [1300, 611], M, mode=mode, rot=rot)
+    c.check(c.run(chunk=640), chunk=640)
+    c.check(c.run(chunk=2048), chunk=2048)
+
+
+@pytest.mark.parametrize("kind,window,sinks", [("f16", 0, 0), ("bf16", 700, 40), ("i8", 1100, 700)])
+def test_a_row_of_many_and_long_chunks(kind, window, sinks):
+    """A row's bits with as many rows as fit (which are joined by threads of
+    their own) and alone, in chunks of more than 512 slots."""
+    t = torch()
+    c = Case(KINDS[kind], 4, 8, 128, 32, [2900, 700, 1300, 640, 3, 1281, 2200], 16, window=window, sinks=sinks, mode=2,
+             rot=128)
+    for chunk in (128, 640):
+        want = c.run(chunk=chunk)
+        c.check(want, chunk=chunk)
+        for b in range(7):
+            for m in (0, 9, 15):
+                c.kv.lens.copy_(ints(c.lens))
+                c.kv.lens[b] += m
+                plan = c.kv.attention(32, 1, 1, scale=c.scale, window=window, sinks=sinks, chunk=chunk)
+                out = t.empty((1, 1, 32, 128), device="cuda")
+                plan.run(1, dev(c.q[b:b + 1, m:m + 1].copy()), out, seq=ints([b]), rope=c.rope)
+                assert np.array_equal(host(out)[0, 0], want[b, m]), (chunk, m, b)
+        c.kv.lens.copy_(ints(c.lens))
+
+
+def test_more_chunks_than_a_join_holds():
+    """1094 chunks, whose weights pass the join's table."""
+    c = Case(km.F16, 1, 2, 32, 256, [140000, 139900], 1, seed=5)
+    c.check(c.run(chunk=128), chunk=128)
+
+
 @pytest.mark.parametrize("lens,chunk", [([300, 20], 128), ([60, 20], 0)])
 @pytest.mark.parametrize("gamma", [False, True])
 def test_requantised_output(lens, chunk, gamma):
