@@ -16,9 +16,11 @@
 //
 // Precision: the fp32 q and weights enter as sums of parts, two for fp16 (q
 // scaled by a power of two per row, the weights by 2^15, so that the second
-// part stays a normal number) and three for bf16; int8 codes are exact in
-// either, keys go with fp16 and values, whose weights carry the value's
-// scale and so have no bounded range, with bf16.
+// part stays a normal number) and three for bf16.  int8 codes are exact in
+// fp16 and go with it; there a weight carries its value's scale d_j, and m is
+// the maximum of s_j + log2 d_j, so that the weights end at 1 whatever the
+// scales are (scales below 2^-80 count as that in m: sums of such values
+// alone keep fewer bits).
 //
 // Bound by memory: a block of 32 slots is 128 dim bytes (64 dim for int8)
 // and is read once.  Each wave keeps the next blocks on their way in a ring
@@ -54,15 +56,17 @@ struct Kind<SV_KV_BF16> {
 template <>
 struct Kind<SV_KV_I8> {
     typedef h8 KVec;
-    typedef b8 VVec;
-    static constexpr int kq = 2, kp = 3, esz = 1;
+    typedef h8 VVec;
+    static constexpr int kq = 2, kp = 2, esz = 1;
 };
+
+constexpr float kLeastScale = -80.0f;
 
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
 // x = sum of N parts of the narrow type, each the rounding of what is left
-// (for fp16 taken off by a fused multiply-add, which reads the half).
+// (fp16: taken off by the instruction that reads halves as they are).
 template <int N, typename V8>
 __device__ __forceinline__ void split8(const float (&x)[8], V8 (&part)[N]) {
     typedef decltype(part[0][0] + part[0][0]) E;
@@ -78,8 +82,12 @@ __device__ __forceinline__ void split8(const float (&x)[8], V8 (&part)[N]) {
             part[n][e + 1] = h.y;
             if (n + 1 == N) break;
             if constexpr (__is_same(E, _Float16)) {
-                left.x = __builtin_fmaf(static_cast<float>(h.x), -1.0f, left.x);
-                left.y = __builtin_fmaf(static_cast<float>(h.y), -1.0f, left.y);
+                uint32_t u;
+                __builtin_memcpy(&u, &h, 4);
+                float x0, x1;
+                asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(x0) : "v"(u), "v"(left.x));
+                asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(x1) : "v"(u), "v"(left.y));
+                left = f2{x0, x1};
             } else {
                 uint32_t u;
                 __builtin_memcpy(&u, &h, 4);
@@ -120,28 +128,16 @@ __device__ __forceinline__ V8 widen(const Raw<2> &r) {
 template <typename V8>
 __device__ __forceinline__ V8 widen(const Raw<1> &r) {
     V8 v;
-    if constexpr (__is_same(V8, h8)) {
-        const h2 bias = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
+    const h2 bias = {static_cast<_Float16>(1152.0f), static_cast<_Float16>(1152.0f)};
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t u = r.w[i >> 1] ^ 0x80808080u;
-            const uint32_t w = __builtin_amdgcn_perm(0x64646464u, u, (i & 1) ? 0x04030402u : 0x04010400u);
-            h2 x;
-            __builtin_memcpy(&x, &w, 4);
-            x = x - bias;
-            v[2 * i] = x[0];
-            v[2 * i + 1] = x[1];
-        }
-    } else {
-        uint32_t z[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int32_t u = static_cast<int32_t>(r.w[i >> 1]);
-            const float lo = static_cast<float>(static_cast<int8_t>(u >> ((i & 1) * 16)));
-            const float hi = static_cast<float>(static_cast<int8_t>(u >> ((i & 1) * 16 + 8)));
-            z[i] = __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u);
-        }
-        __builtin_memcpy(&v, z, 16);
+    for (int i = 0; i < 4; i++) {
+        const uint32_t u = r.w[i >> 1] ^ 0x80808080u;
+        const uint32_t w = __builtin_amdgcn_perm(0x64646464u, u, (i & 1) ? 0x04030402u : 0x04010400u);
+        h2 x;
+        __builtin_memcpy(&x, &w, 4);
+        x = x - bias;
+        v[2 * i] = x[0];
+        v[2 * i + 1] = x[1];
     }
     return v;
 }
@@ -685,19 +681,28 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (Shape<TYPE, D,
                 }
             }
         }
+        // int8: the weights carry the values' scales, so the maximum is that
+        // of a weight with its scale
+        float lift[8];
+        if constexpr (TYPE == SV_KV_I8) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) lift[e] = fmaxf(__builtin_amdgcn_logf(vs[e]), kLeastScale);
+        }
 #pragma unroll
         for (int t = 0; t < RT; t++) {
-            float top = p[t][0];
+            auto with_scale = [&](int e) { return TYPE == SV_KV_I8 ? __builtin_fmaf(p[t][e], rs[t], lift[e]) : p[t][e]; };
+            float top = with_scale(0);
 #pragma unroll
-            for (int e = 1; e < 8; e++) top = fmaxf(top, p[t][e]);
+            for (int e = 1; e < 8; e++) top = fmaxf(top, with_scale(e));
+            top = row_max(top);
             // The running maximum is taken up to a whole number: what it
             // changes by scales exactly, and seldom changes at all.
-            const float now = fmaxf(mx[t], ceilf(row_max(top) * rs[t]));
+            const float now = fmaxf(mx[t], ceilf(TYPE == SV_KV_I8 ? top : top * rs[t]));
             const float base = now == -INFINITY ? 0.0f : now;
             const float keep = __builtin_amdgcn_exp2f(mx[t] - base);
             mx[t] = now;
-            // fp16 weights are taken times 2^15 (l too, so it cancels)
-            const float less = TYPE == SV_KV_F16 ? 15.0f - base : -base;
+            // weights for fp16 products are taken times 2^15 (l too, so it cancels)
+            const float less = TYPE == SV_KV_BF16 ? -base : 15.0f - base;
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; e++) {

@@ -244,12 +244,15 @@ def attention_bound(mag, amp, dim, slots, chunk):
     scaled twice more, the exponent is rounded and 2^x is good to 2 u: a
     weight is off by at most (3 dim + 16) u amp + 4 u relative, in the sums
     above and below the line alike.  An output is a sum of at most 96
-    products (three parts, 32 slots) for each block of a wave's quarter of a
-    chunk, then of 4 waves and the chunks; weights are split as q is.
+    products (three parts, 32 slots) for each block of a wave's share of a
+    chunk (half of one at most, in blocks of 32), then of up to 8 waves and
+    the chunks; weights are split as q is, and what is left of one is at most
+    2^-39 of the row's largest weight (int8: with its scale), which is below
+    these sums' roundings unless weights of 2^-15 make up an output.
     """
     u = 2.0 ** -24
     weight = ((3 * dim + 16) * amp[..., None] + 4) * u
-    adds = (96 * -(-chunk // 128) + 4 + -(-slots // chunk) + 16) * u
+    adds = (96 * -(-chunk // 64) + 8 + -(-slots // chunk) + 16) * u
     return (2 * weight + 2 * adds) * mag + 1e-37
 
 

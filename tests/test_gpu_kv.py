@@ -688,6 +688,26 @@ def test_sizes_of_q(kind):
         c.check(c.run())
 
 
+@pytest.mark.parametrize("low,high", [(-6, 6), (-60, -60), (100, 100), (-75, -70), (0, 12)])
+def test_sizes_of_int8_values(low, high):
+    """Value scales of any size, and different ones in the slots of a row."""
+    c = Case(km.I8, 2, 3, 64, 32, [700, 45], 4)
+    rng = np.random.default_rng(8)
+    k, v = rows(rng, 2, 700, 2, 64)
+    v *= (2.0 ** rng.integers(low, high + 1, (2, 700, 2, 1))).astype(np.float32)
+    nk, nv = rows(rng, 2, 4, 2, 64)
+    nv *= np.float32(2.0 ** low)
+    c.kv.lens.zero_()
+    c.kv.append(1, dev(k), dev(v), n_new=ints(c.lens))
+    c.kv.lens.copy_(ints(c.lens))
+    c.kv.append(1, dev(nk), dev(nv))
+    for b, n in enumerate(c.lens):
+        c.k[b, :n], c.v[b, :n] = km.stored(k[b, :n], km.I8), km.stored(v[b, :n], km.I8)
+        c.k[b, n:n + 4], c.v[b, n:n + 4] = km.stored(nk[b], km.I8), km.stored(nv[b], km.I8)
+    for chunk in (0, 128, 640):
+        c.check(c.run(chunk=chunk), chunk=chunk or 4096)
+
+
 # ------------------------------------------------- streams, graphs, wrapper
 def cycle(kv, plan, M, q, k, v, out, acc, tree, rope):
     kv.reserve(M)
