@@ -49,8 +49,7 @@ __device__ __forceinline__ f4 joined(const AttnArgs &a, const Span &sp, f4 x, fl
     return x * (sum != 0.0f ? 1.0f / sum : 0.0f);
 }
 
-// Few rows: one workgroup each, a share to every dim / 4 threads (64 threads
-// a share at most).
+// Few rows: one workgroup each, a share to every dim / 4 threads.
 constexpr int kWeights = 1024, kAhead = 8;
 __global__ __launch_bounds__(512) void kv_attn_join_kernel(AttnArgs a) {
     __shared__ float s_w[kWeights], s_wl[kWeights];
@@ -61,7 +60,6 @@ __global__ __launch_bounds__(512) void kv_attn_join_kernel(AttnArgs a) {
     const int D = a.kv.dim, quads = D / 4;
     const Parts at(a, b, head, r);
     const int group = tid / quads, d = (tid - group * quads) * 4;
-    const bool own = group < kShares;
     float m_ahead = 0.0f, l_ahead = 0.0f;
     f4 ahead[kAhead];
     if (tid < a.chunks) {
@@ -72,7 +70,7 @@ __global__ __launch_bounds__(512) void kv_attn_join_kernel(AttnArgs a) {
     for (int k = 0; k < kAhead; k++) {
         const int c = group + k * kShares;
         ahead[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (own && c < a.chunks) ahead[k] = at.o_at(c, d);
+        if (c < a.chunks) ahead[k] = at.o_at(c, d);
     }
     const int sid = a.bt.seq ? gld(a.bt.seq + b) : b;
     if (sid < 0 || sid >= a.kv.seqs) return;
@@ -100,31 +98,27 @@ __global__ __launch_bounds__(512) void kv_attn_join_kernel(AttnArgs a) {
             s_wl[i] = w * (held ? l_ahead : at.l_at(from + i));
         }
         __syncthreads();
-        if (own) {
-            for (int nth = 0; nth < 2; nth++) {
-                const Run run(sp, n, nth);
-                const int lo = max(run.from, from), hi = min(run.to, from + upto);
-                int c = lo + ((share - (lo + run.shift)) % kShares + kShares) % kShares;
+        for (int nth = 0; nth < 2; nth++) {
+            const Run run(sp, n, nth);
+            const int lo = max(run.from, from), hi = min(run.to, from + upto);
+            int c = lo + ((share - (lo + run.shift)) % kShares + kShares) % kShares;
 #pragma unroll
-                for (int k = 0; k < kAhead; k++)
-                    if (c == group + k * kShares && c < hi) {
-                        v += s_w[c - from] * ahead[k];
-                        l += s_wl[c - from];
-                        c += kShares;
-                    }
-#pragma unroll 4
-                for (; c < hi; c += kShares) {
-                    v += s_w[c - from] * at.o_at(c, d);
+            for (int k = 0; k < kAhead; k++)
+                if (c == group + k * kShares && c < hi) {
+                    v += s_w[c - from] * ahead[k];
                     l += s_wl[c - from];
+                    c += kShares;
                 }
+#pragma unroll 4
+            for (; c < hi; c += kShares) {
+                v += s_w[c - from] * at.o_at(c, d);
+                l += s_wl[c - from];
             }
         }
         __syncthreads();
     }
-    if (own) {
-        *reinterpret_cast<f4 *>(s_v + share * D + d) = v;
-        if (d == 0) s_l[share] = l;
-    }
+    *reinterpret_cast<f4 *>(s_v + share * D + d) = v;
+    if (d == 0) s_l[share] = l;
     __syncthreads();
     f4 x = {0.0f, 0.0f, 0.0f, 0.0f};
     float sum = 0.0f;
@@ -362,6 +356,6 @@ extern "C" int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch
     if (static_cast<int64_t>(a.rows) * d.heads * batch->B >= kManyRows)
         hipLaunchKernelGGL(kv_attn_join_rows_kernel, dim3((a.rows + of - 1) / of, d.heads, batch->B), dim3(kJoin), 0, st, a);
     else
-        hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(d.dim <= 128 ? 256 : 512), 0, st, a);
+        hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(kShares * (d.dim / 4)), 0, st, a);
     return hip_check(hipGetLastError(), "kv_attention join launch");
 }
