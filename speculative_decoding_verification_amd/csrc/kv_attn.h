@@ -34,7 +34,6 @@ struct AttnArgs {
     int32_t max_len;   // 0 = not checked
     int32_t chunk;     // slots
     int32_t chunks;    // of a launch: as many as any sequence can have
-    int32_t wide;      // 1: few chunks, so each gets twice the waves
     int32_t tiles;     // workgroups that share a (sequence, head, chunk): row groups
     float scale;       // times log2(e)
     Div by_group, by_chunk, by_tiles, by_heads, by_turns;  // by_turns: by rot / 8
@@ -173,12 +172,7 @@ __device__ __forceinline__ void finish_rows(const AttnArgs &a, const float *vals
 }
 
 // Row tiles of 16 that one wave holds, by the rows of a head.
-constexpr int kMaxLds = 156 * 1024;
-
-// Few slots of a chunk go to twice the waves, and so to one workgroup a
-// compute unit instead of two.  A function of the type, dim and chunk alone:
-// the waves share a chunk's blocks, so a row's sums depend on it.
-inline bool attn_wide(int dim, int chunk) { return dim > 224 || (dim > 64 && chunk <= 512); }
+constexpr int kMaxLds = 79 * 1024;  // two workgroups a compute unit
 
 inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 || dim > 64 ? 2 : 4; }
 

@@ -216,24 +216,22 @@ static int64_t chunks_within(int64_t bound, int64_t window, int64_t sinks, int64
 }
 
 // Slots of a chunk when the caller leaves the choice: the shortest with which
-// the launch is one round of workgroups (256 compute units hold one wide or
-// two narrow workgroups each).  Without a window the sequences of a batch are
-// seldom all as long as the longest: half a round more is allowed for.  Past
-// one round of 2048, chunks short enough to even out the last round.  Measured
-// in us, heads of 128 and groups of 5 where nothing else is said:
-//   5 x 4099 slots, 8 heads, fp16          256: 20, 384: 22, 640: 23
-//   8 rows, window 1024, 8 heads of 96     384: 22, 512: 17, 640: 22
-//   4 trees of up to 8191, 8 heads of 64   256: 36, 384: 28, 512: 31
-//   16 sequences up to 16384, int8         1024: 93, 1280: 88, 2048: 102
-//   32 sequences, window 4096, fp16        1024: 131, 1280: 129, 2048: 137
-// A sequence that fits one short chunk needs no join (300 slots: 9 us against
-// 12 with chunks of 256).
-static int chunk_rule(int64_t B, int64_t heads, int dim, int64_t bound, int64_t window, int64_t sinks) {
+// the launch is one round of workgroups (256 compute units hold two each).
+// Without a window the sequences of a batch are seldom all as long as the
+// longest: half a round more is allowed for.  Past one round of 2048, chunks
+// short enough to even out the last round.  Measured in us, heads of 128 and
+// groups of 5 where nothing else is said:
+//   5 x 4099 slots, 8 heads, fp16          128: 21, 256: 18, 384: 21
+//   8 rows, window 1024, 8 heads of 96     256: 17, 384: 17, 512: 19
+//   4 trees of up to 8191, 8 heads of 64   256: 36, 384: 27, 512: 30
+//   16 sequences up to 16384, int8         1024: 92, 1280: 80, 2048: 100
+//   32 sequences, window 4096, fp16        1024: 131, 1280: 125, 2048: 137
+// A sequence that fits one short chunk needs no join (300 slots: 9.5 us
+// against 11.7 with chunks of 256).
+static int chunk_rule(int64_t pairs, bool batch, int64_t bound, int64_t window, int64_t sinks) {
     if (bound <= 512) return static_cast<int>((bound + 127) / 128 * 128);
+    const int64_t room = batch && !window ? 768 : 512;
     for (int c = 256; c <= 2048; c += 128) {
-        int64_t room = attn_wide(dim, c) ? 256 : 512;
-        if (B > 1 && !window) room += room / 2;
-        const int64_t pairs = B * heads;
         // of a window that lies anywhere: window / c + 1 chunks on average
         const int64_t units = window && window + sinks < bound ? pairs * ((sinks + c - 1) / c + 1) + pairs * window / c
                                                                : pairs * ((bound + c - 1) / c);
@@ -272,10 +270,9 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     a->window = at->window;
     a->sinks = at->sinks;
     a->max_len = at->max_len;
-    a->chunk = at->chunk ? at->chunk : chunk_rule(bt->B, d.heads, d.dim, p->bound, at->window, at->sinks);
+    a->chunk = at->chunk ? at->chunk : chunk_rule(static_cast<int64_t>(bt->B) * d.heads, bt->B > 1, p->bound, at->window, at->sinks);
     const int64_t chunks = chunks_within(p->bound, at->window, at->sinks, a->chunk);
     a->chunks = static_cast<int32_t>(chunks);
-    a->wide = attn_wide(d.dim, a->chunk);
     a->scale = at->scale * 1.44269504088896340736f;
     p->rt = attn_tiles_per_wave(d.dim, a->rows);
     a->tiles = (a->rows + 16 * p->rt - 1) / (16 * p->rt);

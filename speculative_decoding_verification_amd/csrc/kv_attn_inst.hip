@@ -264,15 +264,19 @@ __device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to) {
     __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, 0, ONCE ? 2 : 0);
 }
 
-// Waves and their rings.  Where the registers of two waves fit a SIMD (int8,
-// and fp16 up to 128: bf16's queries take half as much again) a compute unit
-// holds eight with 16 KB of ring each, else four with 32 KB.  WIDE: all of
-// them in one workgroup instead of two.
-template <int TYPE, int D, int RT, bool WIDE>
+// Waves and their rings, for two workgroups a compute unit: where the
+// registers of two waves fit a SIMD (int8, and fp16 up to 128: bf16's queries
+// take half as much again) a workgroup has four with 16 KB of ring each, else
+// two with 32 KB.  A function of the type and dim alone: the waves share a
+// chunk's blocks, so a row's sums depend on it.  (fp16 with two of 32 KB:
+// trees of up to 8191 slots 35 against 28 us, 32 windows of 4096 142 against
+// 134; all waves in one workgroup: 5 x 4099 slots 19.6 against 18.2, a single
+// row's 300 slots 9.1 against 9.5.)
+template <int TYPE, int D, int RT>
 struct Shape {
     using Kd = Kind<TYPE>;
     static constexpr bool TWO = TYPE == SV_KV_I8 || (TYPE == SV_KV_F16 && D <= 128);
-    static constexpr int W = (TWO ? 4 : 2) * (WIDE ? 2 : 1);    // waves
+    static constexpr int W = TWO ? 4 : 2;                       // waves
     static constexpr int HALF = 32 * D * Kd::esz;               // bytes of a block's keys, or values
     static constexpr int LOADS = HALF / 1024;                   // transfers of a half
     static constexpr int SCALES = TYPE == SV_KV_I8 ? 1 : 0;     // and one of both scales with the keys
@@ -460,11 +464,11 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs &a, int u) {
     return Unit{-1, 0, 0};
 }
 
-template <int TYPE, int D, int RT, bool WIDE>
-__global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (Shape<TYPE, D, RT, WIDE>::TWO ? 2 : 1)) void kv_attn_kernel(
+template <int TYPE, int D, int RT>
+__global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::TWO ? 2 : 1)) void kv_attn_kernel(
     AttnArgs a) {
     using Kd = Kind<TYPE>;
-    using S = Shape<TYPE, D, RT, WIDE>;
+    using S = Shape<TYPE, D, RT>;
     fetch_args<sizeof(AttnArgs)>();
     constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz, W = S::W, LD = S::LD, ROWS = S::ROWS;
     constexpr bool ONCE = D <= 128 && RT < 4;  // one row group
@@ -864,42 +868,32 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT, WIDE>::W), (Shape<TYPE, D,
 }
 
 // Launches a variant: a workgroup per chunk that there can be, and row group.
-template <int TYPE, int D, int RT, bool WIDE>
+template <int TYPE, int D, int RT>
 static int launch_one(const AttnArgs &a, int64_t units, hipStream_t st) {
-    using S = Shape<TYPE, D, RT, WIDE>;
+    using S = Shape<TYPE, D, RT>;
     static_assert(S::LDS <= kMaxLds, "LDS");
     static std::atomic<int> allowed{0};
     if (S::LDS > 65536 && !allowed.load()) {
-        const int rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT, WIDE>),
+        const int rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT>),
                                                      hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS),
                                  "kv_attention: LDS size");
         if (rc) return rc;
         allowed.store(1);
     }
     const unsigned grid = static_cast<unsigned>((units + 7) / 8 * 8 * a.tiles);
-    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT, WIDE>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
+    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
     return hip_check(hipGetLastError(), "kv_attention launch");
-}
-
-template <int TYPE, int D, int RT>
-static int launch_rows(const AttnArgs &a, int64_t units, hipStream_t st) {
-    if constexpr (D > 224)
-        return launch_one<TYPE, D, RT, true>(a, units, st);
-    else if constexpr (D <= 64)
-        return launch_one<TYPE, D, RT, false>(a, units, st);
-    else
-        return a.wide ? launch_one<TYPE, D, RT, true>(a, units, st) : launch_one<TYPE, D, RT, false>(a, units, st);
 }
 
 template <int TYPE, int D>
 static int launch_dim(const AttnArgs &a, int rt, int64_t units, hipStream_t st) {
     if constexpr (D <= 64) {
-        if (rt == 4) return launch_rows<TYPE, D, 4>(a, units, st);
+        if (rt == 4) return launch_one<TYPE, D, 4>(a, units, st);
     }
     if constexpr (D <= 128) {
-        if (rt == 2) return launch_rows<TYPE, D, 2>(a, units, st);
+        if (rt == 2) return launch_one<TYPE, D, 2>(a, units, st);
     }
-    return launch_rows<TYPE, D, 1>(a, units, st);
+    return launch_one<TYPE, D, 1>(a, units, st);
 }
 
 template <int TYPE>
