@@ -217,8 +217,9 @@ __global__ __launch_bounds__(kBookThreads) void kv_reserve_kernel(KvDev kv, sv_k
 constexpr int kSkip = 0x7FFFFFFF;
 __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int *from, int *cnt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int fc = min(max(ld_dev(kv.ctl), 0), kv.n_pages);  // until the last store below
+    int held = -1;  // the first entry of the lane, read once: only its own wave changes it
     for (int pass = 0; pass < 4; pass++) {
-        const int fc = min(max(ld_dev(kv.ctl), 0), kv.n_pages);
         for (int b = wave; b < n; b += kBookWaves) {
             int have = pass == 3 ? cnt[b] : 0;
             if (from[b] != kSkip) {
@@ -226,7 +227,10 @@ __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int
                 int32_t *row = kv.table + static_cast<int64_t>(sid) * kv.width;
                 for (int64_t at = from[b]; at < kv.width; at += 64) {
                     const int64_t e = at + lane;
-                    const int page = e < kv.width ? gld(row + e) : -1;
+                    const bool first = b == wave && at == from[b];
+                    int page = held;
+                    if (!first || pass == 0) page = e < kv.width ? gld(row + e) : -1;
+                    if (first) held = page;
                     if (!__any(page >= 0)) break;  // a row's pages come first
                     const bool ok = page >= 0 && page < kv.n_pages;
                     const int claim = -1 - static_cast<int>(static_cast<int64_t>(b) * kv.width + e);
@@ -262,7 +266,7 @@ __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int
             __syncthreads();
         }
     }
-    if (tid == 0) st_dev(kv.ctl, min(max(ld_dev(kv.ctl), 0) + cnt[SV_KV_MAX_SEQS], kv.n_pages));
+    if (tid == 0) st_dev(kv.ctl, min(fc + cnt[SV_KV_MAX_SEQS], kv.n_pages));
 }
 
 __global__ __launch_bounds__(kBookThreads) void kv_release_kernel(KvDev kv, const int32_t *ids, int n) {
