@@ -872,13 +872,19 @@ template <int TYPE, int D, int RT>
 static int launch_one(const AttnArgs &a, int64_t units, hipStream_t st) {
     using S = Shape<TYPE, D, RT>;
     static_assert(S::LDS <= kMaxLds, "LDS");
-    static std::atomic<int> allowed{0};
-    if (S::LDS > 65536 && !allowed.load()) {
-        const int rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT>),
-                                                     hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS),
-                                 "kv_attention: LDS size");
+    if constexpr (S::LDS > 65536) {  // above the default, allowed once for each device
+        static std::atomic<uint64_t> allowed{0};
+        int dev = 0;
+        int rc = hip_check(hipGetDevice(&dev), "kv_attention: device");
         if (rc) return rc;
-        allowed.store(1);
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (!(allowed.load() & bit)) {
+            rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT>),
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS),
+                           "kv_attention: LDS size");
+            if (rc) return rc;
+            allowed.fetch_or(bit);
+        }
     }
     const unsigned grid = static_cast<unsigned>((units + 7) / 8 * 8 * a.tiles);
     hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);

@@ -632,6 +632,27 @@ def test_a_row_of_many_and_long_chunks(kind, window, sinks):
         c.kv.lens.copy_(ints(c.lens))
 
 
+@pytest.mark.parametrize("kind,window,sinks", [("f16", 0, 0), ("i8", 150, 9)])
+def test_many_sequences(kind, window, sinks):
+    """More sequences than a wave has lanes, of lengths from 0 on, one of them
+    named twice and one out of range."""
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.integers(0, 700, 150)]
+    lens[3] = lens[77] = 0
+    c = Case(KINDS[kind], 2, 2, 32, 64, lens, 2, n_new=[1 + b % 2 for b in range(150)], window=window, sinks=sinks)
+    for chunk in (0, 128):
+        got = c.run(chunk=chunk)
+        c.check(got, chunk=chunk or 4096)
+    seq = [149, 20, 20, 150, 64] + list(range(70))
+    plan = c.kv.attention(4, len(seq), 2, scale=c.scale, window=window, sinks=sinks, chunk=128)
+    q = np.stack([c.q[min(s, 149)] for s in seq])
+    out = torch().full((len(seq), 2, 4, 32), 77.0, device="cuda")
+    plan.run(1, dev(q), out, seq=ints(seq), n_new=ints([1 + s % 2 for s in seq]))
+    for i, s in enumerate(seq):
+        want = np.full((2, 4, 32), 77, np.float32) if s == 150 else got[s]
+        assert np.array_equal(host(out)[i], want), (i, s)
+
+
 def test_more_chunks_than_a_join_holds():
     """1094 chunks, whose weights pass the join's table."""
     c = Case(km.F16, 1, 2, 32, 256, [140000, 139900], 1, seed=5)
