@@ -529,12 +529,15 @@ int sv_kv_status(const sv_kv *kv, uint32_t *status);
  * holds one makes the outputs that depend on it NaN or infinite.
  *
  * fp32 accuracy: q and the weights p enter the matrix instructions as two
- * (fp16) or three (bf16) parts each, so their products are exact to about
- * 2^-22, and all sums and softmax statistics are fp32.
+ * (fp16, int8) or three (bf16) parts each, so their products are exact to
+ * about 2^-22 (fp16, int8: weights, for int8 times their value's scale, below
+ * 2^-15 of a row's largest keep fewer bits, 2^-39 of that at worst), and all
+ * sums and softmax statistics are fp32.  An int8 row whose visible values are
+ * all below 2^-73 in magnitude may keep fewer bits.
  *
  * The length is cut into chunks (`chunk` slots; 0 = a rule of B, heads,
- * max_len, window and sinks), each an independent softmax, joined in chunk
- * order.  A row's result depends on its own q, position and visible slots
+ * max_len, window and sinks), each an independent softmax, joined in an
+ * order given by the chunks' numbers.  A row's result depends on its own q, position and visible slots
  * and on the chunk length only: not on M, on the other rows and sequences,
  * or on where pages lie, so a row of a round equals that row run alone bit
  * for bit when both calls have the same chunk length. */
