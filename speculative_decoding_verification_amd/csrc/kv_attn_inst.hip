@@ -274,14 +274,16 @@ __device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to) {
     __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, 0, ONCE ? 2 : 0);
 }
 
-// Waves and their rings, for two workgroups a compute unit: where the
+// Waves and their rings, for two workgroups a compute unit: four where the
 // registers of two waves fit a SIMD (int8, and fp16 up to 128: bf16's queries
-// take half as much again) a workgroup has four with 16 KB of ring each, else
-// two with 32 KB.  A function of the type and dim alone: the waves share a
-// chunk's blocks, so a row's sums depend on it.  (fp16 with two of 32 KB:
-// trees of up to 8191 slots 35 against 28 us, 32 windows of 4096 142 against
-// 134; all waves in one workgroup: 5 x 4099 slots 19.6 against 18.2, a single
-// row's 300 slots 9.1 against 9.5.)
+// take half as much again), else two.  A function of the type and dim alone:
+// the waves share a chunk's blocks, so a row's sums depend on it.  (fp16 with
+// two: trees of up to 8191 slots 35 against 28 us, 32 windows of 4096 142
+// against 134; all waves in one workgroup: 5 x 4099 slots 19.6 against 18.2,
+// a single row's 300 slots 9.1 against 9.5.)  A ring holds one block, or 8 KB
+// of smaller ones: with more on its way a load only waits longer behind the
+// others (16 KB for int8 and 32 KB for bf16: window of 1024 17.0 against 16.2
+// us, int8 batch 81.7 against 79.7).
 template <int TYPE, int D, int RT>
 struct Shape {
     using Kd = Kind<TYPE>;
@@ -291,8 +293,7 @@ struct Shape {
     static constexpr int LOADS = HALF / 1024;                   // transfers of a half
     static constexpr int SCALES = TYPE == SV_KV_I8 ? 1 : 0;     // and one of both scales with the keys
     // halves of a wave's ring, at least a block
-    static constexpr int RING = TWO ? 16384 : 32768;
-    static constexpr int FIT = RING / HALF / 2 * 2;
+    static constexpr int FIT = 8192 / HALF / 2 * 2;
     static constexpr int N = FIT < 2 ? 2 : FIT > 8 ? 8 : FIT;
     // [half][wave], then the scales [block][wave]
     static constexpr int SCALES_AT = N * W * HALF, RING_BYTES = SCALES_AT + N / 2 * W * 256 * SCALES;
@@ -303,13 +304,10 @@ struct Shape {
     static_assert(LEAVE_K < 64 && LEAVE_V < 64, "the wait counter has six bits");
     static constexpr int ROWS = 16 * RT, LD = D + 4;
     // the fp32 rows that the queries are made of, and the angles of up to 16
-    // positions: in the halves past the first block where they fit, else in
-    // the ring's beginning, which is then filled after they are used
-    static constexpr int FIRST = (N - 2) * W * HALF >= (ROWS + 16) * D * 4 ? 1 : 0;  // blocks requested before
-    static constexpr int STAGED = FIRST * 2 * W * HALF, ANGLES = STAGED + ROWS * D * 4;
-    static_assert(ANGLES + 16 * D * 4 <= SCALES_AT, "staging");
+    // positions, before the ring is filled
+    static constexpr int ANGLES = ROWS * D * 4, STAGED = ANGLES + 16 * D * 4;
     static constexpr int SUMS = W * ROWS * LD * 4;              // the waves' sums, after the blocks
-    static constexpr int LDS = RING_BYTES > SUMS ? RING_BYTES : SUMS;
+    static constexpr int MOST = RING_BYTES > SUMS ? RING_BYTES : SUMS, LDS = MOST > STAGED ? MOST : STAGED;
 };
 
 // Queries are staged as they lie, a row's quads of four elements exchanged by
@@ -397,8 +395,7 @@ __device__ __forceinline__ void turn_rows(const AttnArgs &a, int len, int b, int
 }
 
 // The queries of a row tile as the second operand of S^T = K Q^T, from the n
-// staged rows (by reads in asm: the ring's transfers are on their way; lanes
-// past the last row take that one), for fp16 multiplied by the power of two
+// staged rows (lanes past the last row take that one), for fp16 multiplied by the power of two
 // that brings the row's largest magnitude into [2^12, 2^13); the row's scores
 // are multiplied by the returned power of two to undo that.
 template <int TYPE, int D>
@@ -568,39 +565,28 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         advance();
     };
     auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
-    const uint32_t staged = ring + S::STAGED, angles = ring + S::ANGLES;
+    const uint32_t angles = ring + S::ANGLES;
     const int n_rows = min(ROWS, rows - row0);
-    stage_rows<D, W>(a, len, b, head, row0, n_rows, wave, staged, angles);
-    if (S::FIRST && any) {
-        request_k();
-        turn();
-        request_v();
-        turn();
-        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * S::LOADS + S::SCALES) : "memory");  // all but the block
-    } else {
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    }
+    stage_rows<D, W>(a, len, b, head, row0, n_rows, wave, ring, angles);
 
     // ---- queries, once every wave's pieces are there
-    asm volatile("s_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0)\n s_barrier" ::: "memory");
     if (a.rope.mode != SV_ROPE_NONE) {
-        turn_rows<D, 64 * W>(a, len, b, row0, n_rows, staged, angles);
+        turn_rows<D, 64 * W>(a, len, b, row0, n_rows, ring, angles);
         asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
     }
     typename Kd::KVec qf[RT][NC][Kd::kq];
     float rs[RT];
 #pragma unroll
-    for (int t = 0; t < RT; t++) rs[t] = take_queries<TYPE, D>(staged, 16 * t, n_rows, a.scale, qf[t]);
-    if constexpr (S::FIRST < S::N / 2) {
-        asm volatile("s_barrier" ::: "memory");  // every wave has its queries
-        if (any) {
+    for (int t = 0; t < RT; t++) rs[t] = take_queries<TYPE, D>(ring, 16 * t, n_rows, a.scale, qf[t]);
+    asm volatile("s_barrier" ::: "memory");  // every wave has its queries
+    if (any) {
 #pragma unroll
-            for (int i = S::FIRST; i < S::N / 2; i++) {
-                request_k();
-                turn();
-                request_v();
-                turn();
-            }
+        for (int i = 0; i < S::N / 2; i++) {
+            request_k();
+            turn();
+            request_v();
+            turn();
         }
     }
 
