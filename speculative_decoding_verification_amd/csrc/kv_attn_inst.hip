@@ -303,11 +303,19 @@ struct Shape {
     static constexpr int LEAVE_V = N / 2 * (LOADS + SCALES) + (N / 2 - 1) * LOADS;
     static_assert(LEAVE_K < 64 && LEAVE_V < 64, "the wait counter has six bits");
     static constexpr int ROWS = 16 * RT, LD = D + 4;
-    // the fp32 rows that the queries are made of, and the angles of up to 16
-    // positions, before the ring is filled
-    static constexpr int ANGLES = ROWS * D * 4, STAGED = ANGLES + 16 * D * 4;
+    // The fp32 rows that the queries are made of, and the angles of up to 16
+    // positions.  EARLY: behind the first keys, which are requested before
+    // they are used, or behind the scales; else in the ring's beginning.  (us,
+    // early against late: 5 x 4099 slots 17.3 against 17.8, trees 24.7 against
+    // 25.3, window of 4096 123.6 against 125; two waves a workgroup, 5 x
+    // 131001 slots 96.5 against 94.3; one tile of rows, 300 slots 9.9 against
+    // 9.7.)
+    static constexpr int ROWS_BYTES = ROWS * D * 4, BYTES = ROWS_BYTES + 16 * D * 4;
+    static constexpr int AT = !SCALES || W * HALF + BYTES <= SCALES_AT ? W * HALF : RING_BYTES;
+    static constexpr bool EARLY = TWO && RT > 1 && AT + BYTES <= kMaxLds - 2048;
+    static constexpr int STAGED = EARLY ? AT : 0, ANGLES = STAGED + ROWS_BYTES, STAGED_END = STAGED + BYTES;
     static constexpr int SUMS = W * ROWS * LD * 4;              // the waves' sums, after the blocks
-    static constexpr int MOST = RING_BYTES > SUMS ? RING_BYTES : SUMS, LDS = MOST > STAGED ? MOST : STAGED;
+    static constexpr int MOST = RING_BYTES > SUMS ? RING_BYTES : SUMS, LDS = MOST > STAGED_END ? MOST : STAGED_END;
 };
 
 // Queries are staged as they lie, a row's quads of four elements exchanged by
@@ -395,7 +403,8 @@ __device__ __forceinline__ void turn_rows(const AttnArgs &a, int len, int b, int
 }
 
 // The queries of a row tile as the second operand of S^T = K Q^T, from the n
-// staged rows (lanes past the last row take that one), for fp16 multiplied by the power of two
+// staged rows (by reads in asm: the ring's transfers are on their way; lanes
+// past the last row take that one), for fp16 multiplied by the power of two
 // that brings the row's largest magnitude into [2^12, 2^13); the row's scores
 // are multiplied by the returned power of two to undo that.
 template <int TYPE, int D>
@@ -565,26 +574,35 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         advance();
     };
     auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
-    const uint32_t angles = ring + S::ANGLES;
+    const uint32_t staged = ring + S::STAGED, angles = ring + S::ANGLES;
     const int n_rows = min(ROWS, rows - row0);
-    stage_rows<D, W>(a, len, b, head, row0, n_rows, wave, ring, angles);
+    stage_rows<D, W>(a, len, b, head, row0, n_rows, wave, staged, angles);
+    if (S::EARLY && any) {
+        request_k();
+        turn();
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::LOADS + S::SCALES) : "memory");  // all but the keys
+    } else {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    }
 
     // ---- queries, once every wave's pieces are there
-    asm volatile("s_waitcnt vmcnt(0)\n s_barrier" ::: "memory");
+    asm volatile("s_barrier" ::: "memory");
     if (a.rope.mode != SV_ROPE_NONE) {
-        turn_rows<D, 64 * W>(a, len, b, row0, n_rows, ring, angles);
+        turn_rows<D, 64 * W>(a, len, b, row0, n_rows, staged, angles);
         asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
     }
     typename Kd::KVec qf[RT][NC][Kd::kq];
     float rs[RT];
 #pragma unroll
-    for (int t = 0; t < RT; t++) rs[t] = take_queries<TYPE, D>(ring, 16 * t, n_rows, a.scale, qf[t]);
+    for (int t = 0; t < RT; t++) rs[t] = take_queries<TYPE, D>(staged, 16 * t, n_rows, a.scale, qf[t]);
     asm volatile("s_barrier" ::: "memory");  // every wave has its queries
     if (any) {
 #pragma unroll
         for (int i = 0; i < S::N / 2; i++) {
-            request_k();
-            turn();
+            if (i > 0 || !S::EARLY) {
+                request_k();
+                turn();
+            }
             request_v();
             turn();
         }
