@@ -491,7 +491,8 @@ int sv_kv_read(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const i
  * grows by the number kept, and the pages past it are freed.  A sequence
  * whose accepted is negative (a round that failed) keeps its len and gives
  * its spare pages back; one whose count exceeds its rows, or whose path is
- * not as above, is left as it was (SV_KV_BAD_COMMIT). tree is not read. */
+ * not as above, is left as it was (SV_KV_BAD_COMMIT).  B * width must be
+ * below 2^31.  tree is not read. */
 int sv_kv_commit(const sv_kv *kv, const sv_kv_batch *batch, const int32_t *accepted, int32_t stride,
                  const int32_t *path, void *stream);
 
@@ -505,7 +506,8 @@ int sv_kv_commit(const sv_kv *kv, const sv_kv_batch *batch, const int32_t *accep
 int sv_kv_fork(const sv_kv *kv, const int32_t *src, const int32_t *dst, int32_t n, void *stream);
 
 /* Drops sequences: their pages lose a holder each, a page without holders
- * becomes free, and len is 0.  Indices out of range are passed over. */
+ * becomes free, and len is 0.  Indices out of range are passed over.
+ * n * width must be below 2^31. */
 int sv_kv_release(const sv_kv *kv, const int32_t *ids, int32_t n, void *stream);
 
 /* Moves the held pages with the highest ids to the free ones with the
@@ -537,10 +539,11 @@ int sv_kv_status(const sv_kv *kv, uint32_t *status);
  *
  * The length is cut into chunks (`chunk` slots; 0 = a rule of B, heads,
  * max_len, window and sinks), each an independent softmax, joined in an
- * order given by the chunks' numbers.  A row's result depends on its own q, position and visible slots
- * and on the chunk length only: not on M, on the other rows and sequences,
- * or on where pages lie, so a row of a round equals that row run alone bit
- * for bit when both calls have the same chunk length. */
+ * order given by the chunks' numbers.  A row's result depends on its own q,
+ * position and visible slots and on the chunk length only: not on M, on the
+ * other rows and sequences, or on where pages lie, so a row of a round
+ * equals that row run alone bit for bit when both calls have the same chunk
+ * length. */
 typedef struct {
     int32_t q_heads;        /* a multiple of heads, at most 64 times */
     float scale;            /* > 0, usually 1 / sqrt(dim) */

@@ -945,6 +945,7 @@ extern "C" int sv_kv_commit(const sv_kv *kv, const sv_kv_batch *batch, const int
     if (rc) return rc;
     SV_REQUIRE(accepted && stride >= 1, SV_ERR_ARG, "kv_commit: accepted must not be NULL and stride at least 1");
     SV_REQUIRE(!path || bt.M <= 32, SV_ERR_ARG, "kv_commit: a path needs M <= 32");
+    SV_REQUIRE(static_cast<int64_t>(bt.B) * d.width < (1ll << 31), SV_ERR_SHAPE, "kv_commit: B * width must be below 2^31");
     SV_REQUIRE(aligned(accepted, 4) && (!path || aligned(path, 4)), SV_ERR_ALIGN,
                "kv_commit: int32 buffers must be 4-byte aligned");
     if (path)

@@ -89,7 +89,8 @@ __global__ __launch_bounds__(512) void kv_attn_join_kernel(AttnArgs a) {
     // its share: that of the places loaded ahead, which past the sinks are
     // `jump - first` ahead of their index
     const int share = (group + (sp.jump - sp.first)) % kShares;
-    for (int from = 0; from < n && top != -INFINITY; from += kWeights) {
+    if (top == -INFINITY) top = 0.0f;  // nothing visible, or only NaN: the sums are 0, or NaN
+    for (int from = 0; from < n; from += kWeights) {
         const int upto = min(n - from, kWeights);
         for (int i = tid; i < upto; i += threads) {
             const bool held = from + i == tid;
@@ -165,7 +166,8 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_rows_kernel(AttnArgs a) {
             v[k] = f4{0.0f, 0.0f, 0.0f, 0.0f};
             s[k] = 0.0f;
         }
-        for (int nth = 0; nth < 2 && top != -INFINITY; nth++) {
+        if (top == -INFINITY) top = 0.0f;  // as above
+        for (int nth = 0; nth < 2; nth++) {
             const Run run(sp, n, nth);
             // rounds of one chunk of each share
             for (int c0 = run.from - ((run.from + run.shift) & (kShares - 1)); c0 < run.to; c0 += kShares) {
@@ -237,7 +239,9 @@ static int chunk_rule(int64_t pairs, bool batch, int64_t bound, int64_t window, 
                                                                : pairs * ((bound + c - 1) / c);
         if (units <= room) return c;
     }
-    return 1280;
+    int c = 1280;  // and of a pool of very long sequences, no more than 2^17
+    while (c < (1 << 23) && pairs * chunks_within(bound, window, sinks, c) > (1 << 17)) c *= 2;
+    return c;
 }
 
 struct Plan {
@@ -282,7 +286,7 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     a->by_heads = div_by(d.heads);
     a->by_turns = div_by(std::max(1, a->rope.rot / 8));
     p->units = static_cast<int64_t>(bt->B) * d.heads * chunks;
-    SV_REQUIRE(p->units * a->tiles < (1ll << 24), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
+    SV_REQUIRE(p->units * a->tiles < (1ll << 23), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
     p->bytes = p->o_m = p->o_l = 0;
     if (chunks > 1) {
         const size_t parts = static_cast<size_t>(bt->B) * d.heads * chunks * a->rows;

@@ -234,8 +234,9 @@ class KvCache:
     def attention(self, q_heads: int, B: int, M: int, scale=None, window: int = 0, sinks: int = 0, max_len: int = 0,
                   chunk: int = 0) -> "Attention":
         """The attention of calls of up to B sequences of M rows, with a
-        workspace of its own (so two captured graphs that may run at once
-        take one each)."""
+        workspace of its own: calls that may run at once, in two captured
+        graphs or on two streams, take one each, and a plan is kept until
+        what it enqueued on a stream other than its creation's has run."""
         return Attention(self, q_heads, B, M, scale, window, sinks, max_len, chunk)
 
 

@@ -527,6 +527,21 @@ def test_a_value_that_is_not_finite_reaches_only_its_element(kind):
     assert np.array_equal(got[0, :4][..., rest], want[0, :4][..., rest])
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_query_that_is_not_finite(kind):
+    """A NaN or an infinity in q makes its own row's outputs NaN, with one
+    chunk and with several, and no other's."""
+    for B, group in ((1, 3), (8, 64)):
+        c = Case(KINDS[kind], 2, group, 64, 32, [500] * B, 3)
+        clean = {chunk: c.run(chunk=chunk) for chunk in (128, 1024)}
+        c.q[0, 1, 2, 7], c.q[0, 2, 0, 3] = np.nan, np.inf
+        for chunk, want in clean.items():
+            got = c.run(chunk=chunk)
+            assert np.isnan(got[0, 1, 2]).all() and np.isnan(got[0, 2, 0]).all()
+            got[0, 1, 2], got[0, 2, 0] = want[0, 1, 2], want[0, 2, 0]
+            assert np.array_equal(got, want)
+
+
 def test_pages_that_are_not_there():
     """Entries of -1 or outside the pool: their slots are not visible."""
     for bad in (-1, 40, 1 << 30, -(1 << 31)):

@@ -113,6 +113,7 @@ def test_rows_and_paths():
     refused(L.sv_kv_fork(r(kv), None, F, 1, None), sv.SV_ERR_ARG)
     refused(L.sv_kv_release(r(kv), None, 1, None), sv.SV_ERR_ARG)
     refused(L.sv_kv_release(r(cache(width=1 << 20)), F, 4096, None), sv.SV_ERR_SHAPE)
+    refused(L.sv_kv_commit(r(cache(width=1 << 20)), r(batch(B=4096)), F, 1, None, None), sv.SV_ERR_SHAPE)
     refused(L.sv_kv_compact(r(kv), F, 1199, None), sv.SV_ERR_WORKSPACE)
     refused(L.sv_kv_compact(r(kv), None, 1200, None), sv.SV_ERR_WORKSPACE)
     refused(L.sv_kv_status(r(kv), None), sv.SV_ERR_ARG)
