@@ -286,6 +286,51 @@ def test_room_that_is_not_there():
     p.same()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("start", [0, 27, 63])
+def test_long_paths(kind, start):
+    """Paths of up to 31 of 32 rows: more than are moved at once, over block
+    and page ends, in every layer."""
+    p = Pair(KINDS[kind], 3, 96, 32, 20, 3, 6, layers=2)
+    rng = np.random.default_rng(start)
+    paths = [list(range(1, 32)), list(range(1, 32, 2)), [0, 1, 2, 5, 6, 7, 8, 9, 10, 20, 21, 22, 23, 30]]
+    if start:
+        k, v = rows(rng, 3, start, 3, 96)
+        p.kv.reserve(start)
+        p.m.reserve(start, [0, 1, 2])
+        for layer in range(2):
+            p.kv.append(layer, dev(k), dev(v))
+        p.m.append(k, v, [0, 1, 2])
+        p.kv.commit(start, ints([start - 1] * 3))
+        p.m.commit(start, [start - 1] * 3, [0, 1, 2])
+    k, v = rows(rng, 3, 32, 3, 96)
+    p.kv.reserve(32)
+    p.m.reserve(32, [0, 1, 2])
+    for layer in range(2):
+        p.kv.append(layer, dev(k), dev(v))
+    p.m.append(k, v, [0, 1, 2])
+    acc, path = [len(x) - 1 for x in paths], np.array([x + [0] * (32 - len(x)) for x in paths], np.int32)
+    p.kv.commit(32, ints(acc), path=ints(path))
+    p.m.commit(32, acc, [0, 1, 2], path=path)
+    p.same()
+    for layer in range(2):
+        p.same_rows(layer)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_keys_or_values_alone(kind):
+    kv = sv.KvCache(KINDS[kind], 1, 2, 64, 32, 4, 1, 4)
+    k, v = rows(np.random.default_rng(1), 1, 50, 2, 64)
+    kv.reserve(50)
+    kv.append(0, dev(k), dev(v))
+    both = [torch().zeros((1, 50, 2, 64), device="cuda") for _ in "kv"]
+    kv.read(0, *both)
+    for i in range(2):
+        one = torch().zeros((1, 50, 2, 64), device="cuda")
+        kv.read(0, **{("k_out", "v_out")[i]: one})
+        assert np.array_equal(host(one), host(both[i])) and (host(one) != 0).any()
+
+
 def test_pages_shared_and_copied():
     """Forks share the pages that are full and own a copy of the last one, in
     every layer; what one appends the others do not see; a shared page goes
