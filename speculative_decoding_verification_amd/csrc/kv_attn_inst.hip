@@ -28,13 +28,13 @@
 // that what is in flight costs no registers; the ring's halves (a block's
 // keys, its values) are refilled as soon as they are in registers.  Measured
 // with the join, heads of 128 and groups of 5, a read alone reaching 7.1 TB/s:
-//   131001 slots of 8 heads, 5 rows, bf16    537 MB in 97 us, 5.5 TB/s
-//   32 windows of 4096, 5 rows, fp16         523 MB in 125 us, 4.2 TB/s: the
+//   131001 slots of 8 heads, 5 rows, bf16    537 MB in 95 us, 5.7 TB/s
+//   32 windows of 4096, 5 rows, fp16         523 MB in 124 us, 4.2 TB/s: the
 //     last, partly filled round of workgroups
-//   16 sequences up to 16384, int8           284 MB in 80 us, 3.5 TB/s: the
+//   16 sequences up to 16384, int8           284 MB in 79 us, 3.6 TB/s: the
 //     same, and the arithmetic of a wave per block (64 matrix and about 400
 //     vector instructions) that two waves a SIMD do not hide
-// Short calls are bound by latency: of 14 us for 4099 slots about 6 go by
+// Short calls are bound by latency: of 13.5 us for 4099 slots about 5 go by
 // before a wave has its first block (lengths, page, queries, angles), 3 for
 // its blocks and 3 for the sums of the waves.
 #include <atomic>
