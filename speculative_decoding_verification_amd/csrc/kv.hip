@@ -213,7 +213,8 @@ __global__ __launch_bounds__(kBookThreads) void kv_reserve_kernel(KvDev kv, sv_k
 // entry naming it (places of the list in order, then entries): all entries
 // give up their hold, then each entry of a page without holders claims it by
 // an atomic minimum of -(1 + order), so which claim wins does not depend on
-// timing.
+// timing.  The callers clear cnt[SV_KV_MAX_SEQS] ahead of a barrier: whether
+// there is an entry at all, later the pages freed.
 constexpr int kSkip = 0x7FFFFFFF;
 __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int *from, int *cnt) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -232,6 +233,7 @@ __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int
                     if (!first || pass == 0) page = e < kv.width ? gld(row + e) : -1;
                     if (first) held = page;
                     if (!__any(page >= 0)) break;  // a row's pages come first
+                    if (pass == 0 && lane == 0) cnt[SV_KV_MAX_SEQS] = 1;
                     const bool ok = page >= 0 && page < kv.n_pages;
                     const int claim = -1 - static_cast<int>(static_cast<int64_t>(b) * kv.width + e);
                     if (pass == 0) {
@@ -259,6 +261,7 @@ __device__ void drop_pages(const KvDev &kv, const int32_t *seq, int n, const int
         }
         drain();
         __syncthreads();
+        if (pass == 0 && cnt[SV_KV_MAX_SEQS] == 0) return;  // most commits leave no page to drop: 4.6 -> 2.9 us
         if (pass == 2) {
             const int total = scan_counts(cnt, n);
             // pass 3 reads the old count before anyone stores the new one
@@ -273,6 +276,7 @@ __global__ __launch_bounds__(kBookThreads) void kv_release_kernel(KvDev kv, cons
     fetch_args<sizeof(KvDev) + 16>();
     __shared__ int from[SV_KV_MAX_SEQS];
     __shared__ int cnt[SV_KV_MAX_SEQS + 1];
+    if (threadIdx.x == 0) cnt[SV_KV_MAX_SEQS] = 0;
     for (int b = threadIdx.x >> 6; b < n; b += kBookWaves) {
         const int sid = first_sid(ids, b, kv.seqs);
         if ((threadIdx.x & 63) == 0) {
@@ -305,6 +309,7 @@ __global__ __launch_bounds__(kBookThreads) void kv_commit_kernel(KvDev kv, sv_kv
     fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + 24>();
     __shared__ int from[SV_KV_MAX_SEQS];
     __shared__ int cnt[SV_KV_MAX_SEQS + 1];
+    if (threadIdx.x == 0) cnt[SV_KV_MAX_SEQS] = 0;
     const int64_t cap = static_cast<int64_t>(kv.width) * kv.page;
     for (int b = threadIdx.x >> 6; b < bt.B; b += kBookWaves) {
         const int sid = first_sid(bt.seq, b, kv.seqs), kept = kept_rows(bt, accepted, stride, path, b);
