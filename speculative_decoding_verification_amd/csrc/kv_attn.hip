@@ -223,13 +223,13 @@ static int64_t chunks_within(int64_t bound, int64_t window, int64_t sinks, int64
 // longest: half a round more is allowed for.  Past one round of 2048, chunks
 // short enough to even out the last round.  Measured in us, heads of 128 and
 // groups of 5 where nothing else is said:
-//   5 x 4099 slots, 8 heads, fp16          128: 21, 256: 18, 384: 21
-//   8 rows, window 1024, 8 heads of 96     256: 17, 384: 17, 512: 19
-//   4 trees of up to 8191, 8 heads of 64   256: 36, 384: 27, 512: 30
-//   16 sequences up to 16384, int8         1024: 92, 1280: 80, 2048: 100
-//   32 sequences, window 4096, fp16        1024: 131, 1280: 125, 2048: 137
-// A sequence that fits one short chunk needs no join (300 slots: 9.5 us
-// against 11.7 with chunks of 256).
+//   5 x 4099 slots, 8 heads, fp16          128: 20, 256: 17, 384: 21
+//   8 rows, window 1024, 8 heads of 96     128: 16, 256: 16, 512: 18
+//   4 trees of up to 8191, 8 heads of 64   256: 33, 384: 25, 512: 28
+//   16 sequences up to 16384, int8         1024: 85, 1280: 80, 2048: 92
+//   32 sequences, window 4096, fp16        1024: 125, 1280: 123, 2048: 132
+// A sequence that fits one short chunk needs no join (300 slots: 9.7 us
+// against 11.8 with chunks of 256).
 static int chunk_rule(int64_t pairs, bool batch, int64_t bound, int64_t window, int64_t sinks) {
     if (bound <= 512) return static_cast<int>((bound + 127) / 128 * 128);
     const int64_t room = batch && !window ? 768 : 512;
