@@ -606,7 +606,7 @@ __device__ __forceinline__ float rot_second(float x0, float x1, float c, float s
 // 8 heads of 128 take 5.8 us, 4 prompts of up to 3000 rows 32 us (keys and
 // values by one workgroup, rotated in LDS: 8.5 and 38).
 constexpr int kPad = 4;  // floats past a staged row, against bank conflicts
-template <int TYPE>
+template <int TYPE, int D>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_kv_batch bt, const float *k,
                                                         const float *v, sv_kv_rope rope) {
     fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + sizeof(sv_kv_rope) + 24>();
@@ -632,7 +632,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_
     const int hi = static_cast<int>(min(len + n - blk * kBlk, int64_t(kBlk)));     // one past its last new slot
     if (lo >= hi) return;
     const int page = kv_page_of(kv, sid, blk >> kv.blk_shift);  // not waited for yet
-    const int D = kv.dim, ld = D + kPad, quads = D / 4;
+    constexpr int ld = D + kPad, quads = D / 4;
     const float *x = what ? v : k;
     // rotated on the way, a quad at a time, where its pairs are whole
     const int rot = what ? 0 : rope.rot, half = rot / 2;
@@ -796,7 +796,7 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_
 // Rows out of the cache: a workgroup per block of 32 slots and head, as
 // above: pieces of the block to LDS, rows from LDS to fp32.  5 rows of 8
 // heads 4 us, 8124 rows of 8 heads 18 us.
-template <int TYPE>
+template <int TYPE, int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(KvDev kv, int layer, sv_kv_batch bt, const int32_t *start,
                                                       float *k_out, float *v_out) {
     fetch_args<sizeof(KvDev) + sizeof(sv_kv_batch) + 32>();
@@ -814,7 +814,7 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvDev kv, int layer, sv_kv
     const int page = blk < 0 ? -1 : kv_page_of(kv, sid, blk >> kv.blk_shift);
     const uint8_t *from =
         page < 0 ? nullptr : kv_block(kv, layer, page, head, static_cast<int>(blk & ((1 << kv.blk_shift) - 1)));
-    const int D = kv.dim, ld = D + kPad, quads = D / 4;
+    constexpr int ld = D + kPad, quads = D / 4;
     float *out = what ? v_out : k_out;
     if (from) {
         for (int i = tid; i < 4 * D; i += 256) {  // 32 (D / 8) pieces of the key, 4 D of the value: as many
@@ -852,6 +852,29 @@ __global__ __launch_bounds__(256) void kv_read_kernel(KvDev kv, int layer, sv_kv
         u32x4 z = {__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(x.z), __float_as_uint(x.w)};
         gst(reinterpret_cast<u32x4 *>(out + ((static_cast<int64_t>(b) * bt.M + m) * kv.heads + head) * D + 4 * c), z);
     }
+}
+
+// The kernels of a cache's type and head dimension.
+using AppendFn = void (*)(KvDev, int, sv_kv_batch, const float *, const float *, sv_kv_rope);
+using ReadFn = void (*)(KvDev, int, sv_kv_batch, const int32_t *, float *, float *);
+struct RowFns {
+    AppendFn append;
+    ReadFn read;
+};
+template <int TYPE>
+static RowFns row_fns_of(int dim) {
+    static constexpr RowFns fns[] = {
+        {kv_append_kernel<TYPE, 32>, kv_read_kernel<TYPE, 32>},   {kv_append_kernel<TYPE, 64>, kv_read_kernel<TYPE, 64>},
+        {kv_append_kernel<TYPE, 96>, kv_read_kernel<TYPE, 96>},   {kv_append_kernel<TYPE, 128>, kv_read_kernel<TYPE, 128>},
+        {kv_append_kernel<TYPE, 160>, kv_read_kernel<TYPE, 160>}, {kv_append_kernel<TYPE, 192>, kv_read_kernel<TYPE, 192>},
+        {kv_append_kernel<TYPE, 224>, kv_read_kernel<TYPE, 224>}, {kv_append_kernel<TYPE, 256>, kv_read_kernel<TYPE, 256>}};
+    static_assert(sizeof(fns) / sizeof(fns[0]) == kMaxDim / 32, "a kernel for every head dimension");
+    return fns[dim / 32 - 1];
+}
+static RowFns row_fns(const KvDev &d) {
+    return d.type == SV_KV_F16    ? row_fns_of<SV_KV_F16>(d.dim)
+           : d.type == SV_KV_BF16 ? row_fns_of<SV_KV_BF16>(d.dim)
+                                  : row_fns_of<SV_KV_I8>(d.dim);
 }
 
 // Blocks of 32 slots that M rows can touch, from any slot on.
@@ -910,9 +933,7 @@ extern "C" int sv_kv_append(const sv_kv *kv, int32_t layer, const sv_kv_batch *b
     const sv_kv_rope r = rope ? *rope : sv_kv_rope{};
     const size_t lds = kBlk * (d.dim + kPad) * sizeof(float);
     const dim3 grid(static_cast<unsigned>(gx), batch->B, 2);
-    auto kernel = d.type == SV_KV_F16 ? kv_append_kernel<SV_KV_F16>
-                  : d.type == SV_KV_BF16 ? kv_append_kernel<SV_KV_BF16> : kv_append_kernel<SV_KV_I8>;
-    hipLaunchKernelGGL(kernel, grid, dim3(256), lds, as_stream(stream), d, layer, *batch, k, v, r);
+    hipLaunchKernelGGL(row_fns(d).append, grid, dim3(256), lds, as_stream(stream), d, layer, *batch, k, v, r);
     return hip_check(hipGetLastError(), "kv_append launch");
 }
 
@@ -932,9 +953,7 @@ extern "C" int sv_kv_read(const sv_kv *kv, int32_t layer, const sv_kv_batch *bat
     const int64_t gx = row_blocks(bt.M) * d.heads;
     SV_REQUIRE(gx < (1ll << 24), SV_ERR_SHAPE, "kv_read: too large");
     const size_t lds = kBlk * (d.dim + kPad) * sizeof(float);
-    auto kernel = d.type == SV_KV_F16 ? kv_read_kernel<SV_KV_F16>
-                  : d.type == SV_KV_BF16 ? kv_read_kernel<SV_KV_BF16> : kv_read_kernel<SV_KV_I8>;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(gx), bt.B, k_out && v_out ? 2 : 1), dim3(256), lds,
+    hipLaunchKernelGGL(row_fns(d).read, dim3(static_cast<unsigned>(gx), bt.B, k_out && v_out ? 2 : 1), dim3(256), lds,
                        as_stream(stream), d, layer, bt, start, k_out, v_out);
     return hip_check(hipGetLastError(), "kv_read launch");
 }
