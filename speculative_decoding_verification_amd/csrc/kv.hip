@@ -603,8 +603,9 @@ __device__ __forceinline__ float rot_second(float x0, float x1, float c, float s
 // of a value, so that neighbouring lanes write neighbouring 16-byte pieces
 // although the fp32 rows are read along the head dimension.  Bound by
 // latency for the rows of a round, by memory bandwidth for a prompt: 5 rows of
-// 8 heads of 128 take 5.8 us, 4 prompts of up to 3000 rows 32 us (keys and
-// values by one workgroup, rotated in LDS: 8.5 and 38).
+// 8 heads of 128 take 5.6 us, 4 prompts of up to 3000 rows 30 us (keys and
+// values by one workgroup, rotated in LDS: 8.5 and 38; the head dimension an
+// argument: 5.8 and 32).
 constexpr int kPad = 4;  // floats past a staged row, against bank conflicts
 template <int TYPE, int D>
 __global__ __launch_bounds__(256) void kv_append_kernel(KvDev kv, int layer, sv_kv_batch bt, const float *k,
