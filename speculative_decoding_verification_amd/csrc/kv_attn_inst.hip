@@ -20,7 +20,9 @@
 // fp16 and go with it; there a weight carries its value's scale d_j, and m is
 // the maximum of s_j + log2 d_j, so that the weights end at 1 whatever the
 // scales are (scales below 2^-80 count as that in m: sums of such values
-// alone keep fewer bits).
+// alone keep fewer bits).  Scores beyond 2^24 in base 2 leave no room in m for
+// the 2^15 or the scale; such rows go without them (see kExact), int8 ones
+// through an fp32 path of their own.
 //
 // Bound by memory for long caches: a block of 32 slots is 128 dim bytes (64
 // dim for int8) and is read once.  Each wave keeps the next blocks on their
@@ -71,6 +73,8 @@ struct Kind<SV_KV_I8> {
 };
 
 constexpr float kLeastScale = -80.0f;
+// Whole numbers up to here stay exact with 15 taken off.
+constexpr float kExact = 16777200.0f;  // 2^24 - 16
 
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 __device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
@@ -706,6 +710,10 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
 #pragma unroll
             for (int e = 0; e < 8; e++) lift[e] = fmaxf(__builtin_amdgcn_logf(vs[e]), kLeastScale);
         }
+        // The running maximum is taken up to a whole number: what it changes
+        // by scales exactly, and seldom changes at all.
+        float most[RT];
+        bool far[RT];
 #pragma unroll
         for (int t = 0; t < RT; t++) {
             auto with_scale = [&](int e) { return TYPE == SV_KV_I8 ? __builtin_fmaf(p[t][e], rs[t], lift[e]) : p[t][e]; };
@@ -713,14 +721,40 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
 #pragma unroll
             for (int e = 1; e < 8; e++) top = fmaxf(top, with_scale(e));
             top = row_max(top);
-            // The running maximum is taken up to a whole number: what it
-            // changes by scales exactly, and seldom changes at all.
-            const float now = fmaxf(mx[t], ceilf(TYPE == SV_KV_I8 ? top : top * rs[t]));
+            most[t] = ceilf(TYPE == SV_KV_I8 ? top : top * rs[t]);
+            far[t] = fabsf(most[t]) > kExact;
+        }
+        bool any_far = false;  // int8: a finite maximum too large for its scale
+        if constexpr (TYPE == SV_KV_I8) {
+#pragma unroll
+            for (int t = 0; t < RT; t++) any_far |= far[t] && fabsf(most[t]) < INFINITY;
+            any_far = __any(any_far);
+            if (any_far) {
+                // The scales are lost in such a sum: the maximum is that of
+                // the scores, and the weights with their scales are taken in
+                // fp32 below.
+#pragma unroll
+                for (int t = 0; t < RT; t++) {
+                    float s = p[t][0];
+#pragma unroll
+                    for (int e = 1; e < 8; e++) s = fmaxf(s, p[t][e]);
+                    s = row_max(s);
+                    most[t] = far[t] ? ceilf(s * rs[t]) : most[t];
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; t++) {
+            // For fp16 products the maximum is held 15 too low, so that
+            // weights go up to 2^15; not where fp32 would round that (by up
+            // to 16, and 2^16 is past fp16): there scores are whole numbers
+            // apart, and weights up to 1 keep what is known of them.
+            if (TYPE != SV_KV_BF16 && !far[t]) most[t] -= 15.0f;
+            const float now = fmaxf(mx[t], most[t]);
             const float base = now == -INFINITY ? 0.0f : now;
             const float keep = __builtin_amdgcn_exp2f(mx[t] - base);
             mx[t] = now;
-            // weights for fp16 products are taken times 2^15 (l too, so it cancels)
-            const float less = TYPE == SV_KV_BF16 ? -base : 15.0f - base;
+            const float less = -base;
             float sum = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; e++) {
@@ -783,6 +817,43 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
                             if (f & 0x80000000u) vr[i].w[e] &= 0x0000FFFFu;
                         }
                 }
+            }
+        }
+        if constexpr (TYPE == SV_KV_I8) {
+            if (any_far) {
+                // weights with scales that the maximum does not bound: in
+                // fp32, slot by slot
+                const int at_lane = fresh(lane), to_col = at_lane & 15, to_g = at_lane >> 4;
+#pragma unroll 1
+                for (int s = 0; s < kBlk; s++) {
+                    float w[RT];
+                    bool none = true;
+#pragma unroll
+                    for (int t = 0; t < RT; t++) {
+                        w[t] = p[t][0];
+#pragma unroll
+                        for (int e = 1; e < 8; e++) w[t] = (s & 7) == e ? p[t][e] : w[t];
+                        w[t] = far[t] ? w[t] : 0.0f;
+                        w[t] = __uint_as_float(__builtin_amdgcn_ds_bpermute(4 * (16 * (s >> 3) + to_col), __float_as_uint(w[t])));
+                        none &= w[t] == 0.0f;
+                    }
+                    if (__all(none)) continue;
+                    const uint8_t *v = blk + 32 * D + ((s >> 3) * D + 4 * to_g) * 8 + (s & 7);
+#pragma unroll
+                    for (int i = 0; i < ND; i++) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float y = static_cast<float>(static_cast<int8_t>(gld(v + (16 * i + k) * 8)));
+#pragma unroll
+                            for (int t = 0; t < RT; t++) o[t][i][k] += w[t] * y;
+                        }
+                        asm volatile("" ::: "memory");  // a few loads at a time, for the registers' sake
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < RT; t++)
+#pragma unroll
+                    for (int e = 0; e < 8; e++) p[t][e] = far[t] ? 0.0f : p[t][e];
             }
         }
         {
