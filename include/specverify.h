@@ -528,7 +528,9 @@ int sv_kv_status(const sv_kv *kv, uint32_t *status);
  * only if its position lies less than `window` before the row's own, or is
  * one of the first `sinks` positions.  Only visible slots count: what
  * others hold, infinities and NaN too, changes nothing; a visible row that
- * holds one makes the outputs that depend on it NaN or infinite.
+ * holds one makes the outputs that depend on it NaN or infinite, and so does
+ * what fp32 cannot hold: q times scale * log2(e) from 2^127 on, a score
+ * (times log2(e)), a sum of weights (of at most 1 each) times values.
  *
  * fp32 accuracy: q and the weights p enter the matrix instructions as two
  * (fp16, int8) or three (bf16) parts each, so their products are exact to

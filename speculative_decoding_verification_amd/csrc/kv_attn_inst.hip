@@ -433,7 +433,8 @@ __device__ __forceinline__ float take_queries(uint32_t staged, int from, int n, 
     if constexpr (__is_same(typename Kd::KVec, h8)) {
         top = row_max(top);
         const int ex = static_cast<int>(__float_as_uint(top) >> 23);  // biased; 255 = not finite
-        const int up = ex == 0 || ex == 255 ? 0 : max(-100, min(100, 12 - (ex - 127)));
+        // -115 at least, so that both powers are normal numbers
+        const int up = ex == 0 || ex == 255 ? 0 : min(100, 12 - (ex - 127));
         const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
         back = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
 #pragma unroll

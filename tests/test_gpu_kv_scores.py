@@ -182,3 +182,20 @@ def largest(q, k, v, n):
             w = np.exp(s - s.max())
             out[m, g] = (w / w.sum() * top[:seen]).max()
     return out
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("power", [100, 114, 115, 116, 117, 118, 120, 123, 126])
+def test_very_large_queries(kind, power):
+    """Queries up to the last power of two of fp32, whose scores still fit
+    it: keys of -1, 0 and 1 in the element that is not 0."""
+    rng = np.random.default_rng(power)
+    for first in (rng.integers(-1, 2, 300), -np.ones(300)):
+        k = np.zeros((300, 64), np.float32)
+        k[:, 0], k[:, 2] = first, 127
+        c = Filled(KINDS[kind], k, values(rng, kind, 300, 64), 3, 5)
+        q = np.zeros((3, 5, 64), np.float32)
+        q[..., 0] = 2.0 ** power
+        q[0, 0, 1] = 2.0 ** (power - 30)
+        for chunk in (128, 512):
+            c.check(q, chunk)
