@@ -490,9 +490,10 @@ int sv_kv_read(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const i
  * moves to slot len + i in every layer); NULL keeps rows 0, 1, ...  len
  * grows by the number kept, and the pages past it are freed.  A sequence
  * whose accepted is negative (a round that failed) keeps its len and gives
- * its spare pages back; one whose count exceeds its rows, or whose path is
- * not as above, is left as it was (SV_KV_BAD_COMMIT).  B * width must be
- * below 2^31.  tree is not read. */
+ * its spare pages back; one whose count exceeds its rows, whose path is not
+ * as above, or whose last row kept had no slot to be written to, is left as
+ * it was (SV_KV_BAD_COMMIT).  B * width must be below 2^31.  tree is not
+ * read. */
 int sv_kv_commit(const sv_kv *kv, const sv_kv_batch *batch, const int32_t *accepted, int32_t stride,
                  const int32_t *path, void *stream);
 

@@ -312,12 +312,17 @@ __global__ __launch_bounds__(kBookThreads) void kv_commit_kernel(KvDev kv, sv_kv
     if (threadIdx.x == 0) cnt[SV_KV_MAX_SEQS] = 0;
     const int64_t cap = static_cast<int64_t>(kv.width) * kv.page;
     for (int b = threadIdx.x >> 6; b < bt.B; b += kBookWaves) {
-        const int sid = first_sid(bt.seq, b, kv.seqs), kept = kept_rows(bt, accepted, stride, path, b);
+        int row = 0;
+        const int sid = first_sid(bt.seq, b, kv.seqs), kept = kept_rows(bt, accepted, stride, path, b, &row);
+        const int last = path ? __shfl(row, max(kept, 1) - 1) : kept - 1;  // the last row kept
         if ((threadIdx.x & 63) == 0) {
             from[b] = kSkip;
             if (sid >= 0) {
-                const int64_t len = kv_len_of(kv, sid) + kept;
-                if (kept < 0 || len > cap || (kept > 0 && kv_page_of(kv, sid, (len - 1) >> kv.page_shift) < 0)) {
+                // a row that append dropped, for want of a page, is not kept
+                const int64_t old = kv_len_of(kv, sid), len = old + kept;
+                if (kept < 0 || len > cap ||
+                    (kept > 0 && (kv_page_of(kv, sid, (len - 1) >> kv.page_shift) < 0 ||
+                                  kv_page_of(kv, sid, (old + last) >> kv.page_shift) < 0))) {
                     kv_flag(kv, SV_KV_BAD_COMMIT);
                 } else {
                     gst(kv.len + sid, static_cast<int32_t>(len));
@@ -371,7 +376,8 @@ __global__ __launch_bounds__(256) void kv_commit_move_kernel(KvDev kv, sv_kv_bat
             const int p0 = own ? kv_page_of(kv, sid, s0 >> kv.page_shift) : -1;
             const int p1 = own ? kv_page_of(kv, sid, s1 >> kv.page_shift) : -1;
             // the bookkeeping refuses what does not fit; nothing moves then
-            const bool ok = len + kept <= static_cast<int64_t>(kv.width) * kv.page && __shfl(p1, kept - 1) >= 0;
+            const bool ok = len + kept <= static_cast<int64_t>(kv.width) * kv.page && __shfl(p0, kept - 1) >= 0 &&
+                            __shfl(p1, kept - 1) >= 0;
             const bool moved = ok && own && row != lane && p0 >= 0 && p1 >= 0;
             const unsigned long long m = __ballot(moved);
             n = __popcll(m);
