@@ -25,7 +25,11 @@ With an AttnShape the stack keeps that history: each layer appends its rows'
 k and v to a paged key-value cache and attends over it, and the attention's
 epilogue requantises o's input (b = Q8A32(attention * g2)).  The cycle then
 also reserves the rows' pages and, after acceptance, commits the rows that
-were kept, so consecutive cycles continue one sequence on the device.
+were kept, so consecutive cycles continue one sequence on the device.  A
+cycle whose rows found no room (the cache is full) is a failed round: its
+`out` is -1 throughout, as an error of the acceptance calls is, its logits
+mean nothing and the sequence keeps its length; so are the cycles after it
+until VerifyStack.check() has reported why.
 """
 
 from __future__ import annotations
@@ -39,7 +43,8 @@ import numpy as np
 
 from . import (SV_EP_PAIR, SV_EP_QUANT, SV_Q4_K, SV_Q6_K, SV_Q8_0, Pass, accept_greedy, act, epilogue,
                gguf_bytes, head_logits, phase, quantize_act_q8, repack_weights, repacked_bytes, verify_matvec, weight,
-               SV_KV_F16, SV_ROPE_HALVES, SV_ROPE_NONE, KvCache, Rope, rope_table)
+               SV_ERR_SHAPE, SV_KV_F16, SV_KV_NO_PAGES, SV_KV_TOO_LONG, SV_ROPE_HALVES, SV_ROPE_NONE, KvCache, Rope,
+               SpecVerifyError, rope_table)
 
 
 @dataclass
@@ -205,6 +210,7 @@ class VerifyStack:
         self.out = t.zeros((M + 1,), dtype=t.int32, device="cuda")
         self.kv, self.rope, self._attns = None, None, {}
         if shape.attn is not None:
+            self._refused = t.zeros((1,), dtype=t.bool, device="cuda")
             a = shape.attn
             width = -(-(a.max_len + M) // a.page)
             self.kv = KvCache(a.kv_type, shape.layers, a.kv_heads, a.dim, a.page, width, 1, width)
@@ -230,10 +236,24 @@ class VerifyStack:
                  ep=act_v.ep(SV_EP_QUANT, self.layers[li].gammas["g2"]))
 
     def _commit(self, M: int):
-        """Keeps the rows that acceptance kept (all of them without a head)."""
+        """Keeps the rows that acceptance kept (all of them without a head),
+        none where the cache has refused a call since the last check()."""
         if self.head is None:
             self.out[:1].fill_(M - 1)
+        _torch().ne(self.kv.ctl[1:2], 0, out=self._refused)
+        self.out[:M + 1].masked_fill_(self._refused, -1)
         self.kv.commit(M, self.out[:M + 1])
+
+    def check(self):
+        """Raises SpecVerifyError if the cache refused a call since the last
+        check; synchronises.  The cycles since then failed (out is -1); the
+        next one starts from the rows that are in the cache."""
+        bits = self.kv.status() if self.kv is not None else 0
+        if bits:
+            why = [name for name, bit in (("no free page", SV_KV_NO_PAGES), ("the sequence is as long as the cache",
+                                                                             SV_KV_TOO_LONG)) if bits & bit]
+            raise SpecVerifyError(SV_ERR_SHAPE, f"stack: cycles failed, {' and '.join(why) or 'the cache refused a call'}"
+                                                f" (status {bits})")
 
     # ----------------------------------------------------------- phases
     def _specs(self, M: int):
