@@ -188,7 +188,7 @@ class KvCache:
         counts in column 0 (the outputs of the acceptance calls; [n] for
         one sequence); path int32 [B, M]: the rows kept, or None."""
         B = self._places(seq) if path is None else path.shape[0]
-        if accepted.ndim == 1 and accepted.numel() != B and B != 1:
+        if accepted.ndim < 2 and accepted.numel() != B and B != 1:
             raise _bad(f"kv: accepted must hold {B} counts")
         if accepted.ndim > 2 or (accepted.ndim == 2 and accepted.shape[0] != B) or accepted.numel() < 1:
             raise _bad(f"kv: accepted must be [{B}] or [{B}, n]")
