@@ -58,7 +58,7 @@ __device__ __forceinline__ Span span_of(const AttnArgs &a, int len, int n) {
     const int cap = a.kv.width * a.kv.page;
     s.total = s.len + s.n < cap ? s.len + s.n : cap;
     s.lo = a.window && s.len >= a.window ? s.len - a.window + 1 : 0;
-    s.end = a.by_chunk(s.total + a.chunk - 1);
+    s.end = s.total ? a.by_chunk(s.total - 1) + 1 : 0;  // total + chunk may pass 2^31
     s.first = 0;
     s.jump = 0;
     if (s.lo > a.sinks) {
