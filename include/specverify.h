@@ -414,7 +414,7 @@ typedef struct {
     int32_t n_pages;
     int32_t seqs;     /* rows of the page table, at most SV_KV_MAX_SEQS */
     int32_t width;    /* page table entries per sequence; seqs * width < 2^31 */
-    void *data;       /* sv_kv_data_bytes bytes, 256-byte aligned */
+    void *data;       /* sv_kv_data_bytes bytes (below 2^48), 256-byte aligned */
     int32_t *table;   /* [seqs][width] page ids, -1 = none; the valid entries of a row come first */
     int32_t *len;     /* [seqs] committed positions */
     int32_t *refs;    /* [n_pages] sequences holding the page */

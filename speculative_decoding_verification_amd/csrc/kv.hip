@@ -33,6 +33,7 @@ int kv_check(const sv_kv *kv, const char *who_, KvDev *o) {
                    static_cast<int64_t>(kv->layers) * kv->heads < (1 << 23),
                SV_ERR_SHAPE, who + ": layers must be in [1, 4096], layers * heads below 2^23");
     SV_REQUIRE(kv->n_pages >= 1 && kv->n_pages <= kKvMaxPages, SV_ERR_SHAPE, who + ": n_pages must be in [1, 2^24]");
+    SV_REQUIRE(sv_kv_data_bytes(kv), SV_ERR_SHAPE, who + ": the pool must be below 2^48 bytes");
     SV_REQUIRE(kv->seqs >= 1 && kv->seqs <= SV_KV_MAX_SEQS && kv->width >= 1 &&
                    static_cast<int64_t>(kv->seqs) * kv->width < (1ll << 31) &&
                    static_cast<int64_t>(kv->width) * kv->page < (1ll << 31) - 65536,
@@ -898,7 +899,10 @@ extern "C" size_t sv_kv_page_bytes(int32_t type, int32_t heads, int32_t dim, int
 
 extern "C" size_t sv_kv_data_bytes(const sv_kv *kv) {
     if (!kv || kv->layers < 1 || kv->layers > kKvMaxLayers || kv->n_pages < 1 || kv->n_pages > kKvMaxPages) return 0;
-    return static_cast<size_t>(kv->layers) * kv->n_pages * sv_kv_page_bytes(kv->type, kv->heads, kv->dim, kv->page);
+    const size_t page = sv_kv_page_bytes(kv->type, kv->heads, kv->dim, kv->page);
+    const size_t pages = static_cast<size_t>(kv->layers) * kv->n_pages;  // at most 2^36
+    if (!page || static_cast<int64_t>(kv->layers) * kv->heads >= (1 << 23) || pages >= kKvMaxBytes / page) return 0;
+    return pages * page;
 }
 
 extern "C" int sv_kv_init(const sv_kv *kv, void *stream) {

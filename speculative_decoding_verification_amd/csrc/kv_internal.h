@@ -10,6 +10,7 @@ constexpr int kBlk = 32;             // slots of a block
 constexpr int kMaxDim = 256;
 constexpr int kKvMaxPages = 1 << 24;
 constexpr int kKvMaxLayers = 4096, kKvMaxHeads = 4096;
+constexpr size_t kKvMaxBytes = size_t(1) << 48;  // of a pool: offsets and sizes stay exact
 
 // Bytes of one block (32 slots of one head).
 __host__ __device__ inline uint32_t kv_block_bytes(int type, int dim) {
