@@ -534,10 +534,11 @@ int sv_kv_status(const sv_kv *kv, uint32_t *status);
  * (times log2(e)), a sum of weights (of at most 1 each) times values.
  *
  * fp32 accuracy: q and the weights p enter the matrix instructions as two
- * (fp16, int8) or three (bf16) parts each, so their products are exact to
- * about 2^-22 (fp16, int8: weights, for int8 times their value's scale, below
- * 2^-15 of a row's largest keep fewer bits, 2^-39 of that at worst), and all
- * sums and softmax statistics are fp32.  An int8 row whose visible values are
+ * (fp16, int8) or three (bf16) parts each, so each is exact to 2^-23, a step
+ * of fp32 (fp16, int8: weights, for int8 times their value's scale, below
+ * 2^-15 of a row's largest keep fewer bits, 2^-39 of that at worst; where a
+ * row's scores pass 2^24 in base 2 an fp16 cache's weights are exact to 2^-25
+ * of the largest), and all sums and softmax statistics are fp32.  An int8 row whose visible values are
  * all below 2^-73 in magnitude may keep fewer bits.
  *
  * The length is cut into chunks (`chunk` slots; 0 = a rule of B, heads,
@@ -553,7 +554,8 @@ typedef struct {
     int32_t window;         /* 0 = none */
     int32_t sinks;          /* >= 0; only with a window */
     int32_t max_len;        /* no sequence's len + new rows exceeds it (0: width * page); it sizes
-                               the launch and the workspace */
+                               the launch, the workspace and, with chunk 0, the chunks: a call
+                               whose sequences are far shorter than the table row is faster with it */
     int32_t chunk;          /* 0, or a multiple of 128 */
     const sv_kv_rope *rope; /* rotates q for its row's position, or NULL */
 } sv_kv_attn;

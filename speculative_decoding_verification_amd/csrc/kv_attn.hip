@@ -205,7 +205,8 @@ __global__ __launch_bounds__(kJoin) void kv_attn_join_rows_kernel(AttnArgs a) {
 
 // Rows from which the second kernel is taken: with ten workgroups of one row
 // to a compute unit (us: 3200 rows of 128 in 13 chunks 10.5 against 8.0, 2048
-// rows of 64 in 22 chunks 8.4 against 9.0).
+// rows of 64 in 22 chunks 8.4 against 9.0; these two differ in dim and chunks
+// as well, and nothing between them was measured).
 constexpr int64_t kManyRows = 2560;
 
 // Chunks that a sequence can have: of its whole length, or of what a window
@@ -218,11 +219,14 @@ static int64_t chunks_within(int64_t bound, int64_t window, int64_t sinks, int64
 }
 
 // Slots of a chunk when the caller leaves the choice: the shortest with which
-// the launch is one round of workgroups (256 compute units hold two each).
+// the launch is one round of workgroups (256 compute units hold two each), for
+// sequences of the length that max_len, or else the table row, allows.  Far
+// shorter ones leave most of the chip idle: 4099 slots take 17.3 us with their
+// own length as max_len, and 40.6 in a table row of 131072 without it.
 // Without a window the sequences of a batch are seldom all as long as the
 // longest: half a round more is allowed for.  Past one round of 2048, chunks
-// short enough to even out the last round.  Measured in us, heads of 128 and
-// groups of 5 where nothing else is said:
+// short enough to even out the last round (two cases, the last ones below).
+// Measured in us, heads of 128 and groups of 5 where nothing else is said:
 //   5 x 4099 slots, 8 heads, fp16          128: 20, 256: 17, 384: 21
 //   8 rows, window 1024, 8 heads of 96     128: 16, 256: 16, 512: 18
 //   4 trees of up to 8191, 8 heads of 64   256: 33, 384: 25, 512: 28

@@ -16,7 +16,14 @@
 //
 // Precision: the fp32 q and weights enter as sums of parts, two for fp16 (q
 // scaled by a power of two per row, the weights by 2^15, so that the second
-// part stays a normal number) and three for bf16.  int8 codes are exact in
+// part stays a normal number) and three for bf16.  Three bf16 parts are exact.
+// The first fp16 part leaves a whole number of at most 2^12 steps of fp32, and
+// the second takes all of it but, in a quarter of the values, the last step: a
+// factor is at most 2^-23 off, as after one rounding more of fp32.  A third
+// part would be exact and costs registers and half as many products again
+// (us: 5 x 4099 slots 17.2 against 18.8, trees 24.6 against 36.7, wide window
+// 124 against 155, int8 batch 80.5 against 89.6); the outputs of all measured
+// cases are closer to 64 bits than those of plain fp32 sums without it.  int8 codes are exact in
 // fp16 and go with it; there a weight carries its value's scale d_j, and m is
 // the maximum of s_j + log2 d_j, so that the weights end at 1 whatever the
 // scales are (scales below 2^-80 count as that in m: sums of such values
@@ -33,9 +40,11 @@
 //   131001 slots of 8 heads, 5 rows, bf16    537 MB in 95 us, 5.7 TB/s
 //   32 windows of 4096, 5 rows, fp16         523 MB in 124 us, 4.2 TB/s: the
 //     last, partly filled round of workgroups
-//   16 sequences up to 16384, int8           284 MB in 79 us, 3.6 TB/s: the
-//     same, and the arithmetic of a wave per block (64 matrix and about 400
-//     vector instructions) that two waves a SIMD do not hide
+//   16 sequences up to 16384, int8           284 MB in 80 us, 3.5 TB/s: the
+//     same (on average 1.3 of the two waves a SIMD are there), and waits: the
+//     SIMDs issue vector instructions (600 a block and wave, 64 of them matrix
+//     ones) in 45 % of the time, their matrix units are busy in 18 %, and a
+//     wave waits for loads and barriers in 29 % of its own
 // Short calls are bound by latency: of 13.5 us for 4099 slots about 5 go by
 // before a wave has its first block (lengths, page, queries, angles), 3 for
 // its blocks and 3 for the sums of the waves.
@@ -492,7 +501,12 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
     using S = Shape<TYPE, D, RT>;
     fetch_args<sizeof(AttnArgs)>();
     constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz, W = S::W, LD = S::LD, ROWS = S::ROWS;
-    constexpr bool ONCE = D <= 128 && RT < 4;  // one row group
+    // Read past the caches.  Meant for blocks that one row group reads, which
+    // dim and row tiles do not quite say: from 33 rows on, dims of 96 and 128
+    // have several groups, whose second reading the placement below would let
+    // L2 serve (80 rows of 128 over 8191 slots take 38 us), and up to 64 rows of
+    // at most 64 are one.
+    constexpr bool ONCE = D <= 128 && RT < 4;
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ float s_m[W][ROWS], s_l[W][ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
