@@ -550,7 +550,7 @@ int sv_kv_status(const sv_kv *kv, uint32_t *status);
  * length. */
 typedef struct {
     int32_t q_heads;        /* a multiple of heads, at most 64 times */
-    float scale;            /* > 0, usually 1 / sqrt(dim) */
+    float scale;            /* > 0, at most 2.3e38; usually 1 / sqrt(dim) */
     int32_t window;         /* 0 = none */
     int32_t sinks;          /* >= 0; only with a window */
     int32_t max_len;        /* no sequence's len + new rows exceeds it (0: width * page); it sizes

@@ -258,7 +258,8 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     SV_REQUIRE(at, SV_ERR_ARG, "kv_attention: NULL arguments");
     SV_REQUIRE(at->q_heads >= 1 && at->q_heads % d.heads == 0 && at->q_heads / d.heads <= 64, SV_ERR_SHAPE,
                "kv_attention: q_heads must be a multiple of heads, at most 64 times");
-    SV_REQUIRE(at->scale > 0.0f && at->scale <= 3.0e38f, SV_ERR_ARG, "kv_attention: scale must be positive and finite");
+    SV_REQUIRE(at->scale > 0.0f && at->scale <= 2.3e38f, SV_ERR_ARG,
+               "kv_attention: scale must be positive and at most 2.3e38");  // times log2(e) it is finite
     SV_REQUIRE(at->window >= 0 && at->sinks >= 0 && at->sinks < (1 << 30), SV_ERR_ARG,
                "kv_attention: window and sinks must not be negative, sinks below 2^30");
     SV_REQUIRE(at->window > 0 || at->sinks == 0, SV_ERR_ARG, "kv_attention: sinks need a window");

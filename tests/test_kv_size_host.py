@@ -1,4 +1,4 @@
-"""Sizes of pools that no memory holds are refused, not wrapped."""
+"""Sizes and numbers past what the arithmetic holds are refused, not wrapped."""
 
 import ctypes
 import os
@@ -30,3 +30,13 @@ def test_the_largest_pool():
     kv = cache(layers=64, heads=512, n_pages=(1 << 15) - 1, dim=256, page=256)
     assert L.sv_kv_data_bytes(r(kv)) == (1 << 48) - (1 << 33)
     assert L.sv_kv_data_bytes(r(cache(layers=4096, heads=4096))) == 0   # no call takes it
+
+
+@pytest.mark.parametrize("scale", [2.35e38, 2.4e38, 3e38, 3.4e38])
+def test_scales_that_base_two_makes_infinite(scale):
+    L, kv, b, r = sv.lib(), cache(), batch(), ctypes.byref
+    a = sv.KvAttn(40, scale, 0, 0, 0, 0, None)
+    refused(L.sv_kv_attention(r(kv), 0, r(b), r(a), F, F, None, F, 1 << 40, None), sv.SV_ERR_ARG)
+    assert L.sv_kv_attention_workspace_bytes(r(kv), r(b), r(a)) == 0
+    a = sv.KvAttn(40, 2.3e38, 0, 0, 0, 0, None)
+    assert L.sv_kv_attention_workspace_bytes(r(kv), r(b), r(a)) > 0
