@@ -112,6 +112,27 @@ int sv_unpack_weights(int32_t qtype, const void *repacked, void *gguf_dst, int64
 int sv_quantize_act_q8(const float *x, int32_t M, int64_t K, const float *gamma, int8_t *q,
                        float *d, int32_t *s16, float *sumsq, void *stream);
 
+/* The residual's addition and the RMS norm around it.  Per row
+ *   t = x + delta (one fp32 rounding; t = x without delta),  sum = t,
+ *   v = t * gamma,  r = 1 / sqrt(sum_i t_i^2 / K + eps),
+ * all fp32.  The codes q and their sums s16 are those of sv_quantize_act_q8
+ * on t and gamma, bit for bit, and so is sumsq (of t, before gamma).
+ *   fold = 1: r is left to the consumer (sv_act with sumsq_parts); d is the
+ *     quantiser's, eps is not read and y must be NULL.
+ *   fold = 0: d is the quantiser's times r, so q and d stand for the
+ *     normalised vector (sv_act without sumsq_parts); y = v * r in fp32.
+ * A row that holds an infinity or NaN, or whose sum of squares passes the
+ * range of fp32, gets what this arithmetic makes of it.
+ *   x, delta [rows][K] fp32, delta NULL for none; gamma [K] or NULL;
+ *   sum [rows][K] or NULL, may be x or delta itself (no other output may
+ *   overlap an input); y [rows][K] or NULL; q [rows][K], d [rows][K/32],
+ *   s16 [rows][K/16], sumsq [rows][K/32], all four or none; q or y is given.
+ *   K a multiple of 32, at most 32768; rows * K below 2^33.  fp32 vectors
+ *   [K] wide and 16-byte aligned, the rest 4-byte aligned. */
+int sv_add_norm_q8(const float *x, const float *delta, int64_t rows, int64_t K, const float *gamma,
+                   float eps, int32_t fold, float *sum, float *y, int8_t *q, float *d, int32_t *s16,
+                   float *sumsq, void *stream);
+
 /* ------------------------------------------------------------------ */
 /* a3/a4. Projection of M positions in one weight stream.              */
 /* ------------------------------------------------------------------ */
@@ -368,6 +389,48 @@ int sv_accept_rejection_noalloc(const float *logits, int64_t V, const float *q, 
                                 void *stream);
 
 /* ------------------------------------------------------------------ */
+/* Sampling with temperature, top-k, top-p and min-p.                  */
+/* ------------------------------------------------------------------ */
+/* How a row is sampled from. */
+typedef struct {
+    float temperature; /* >= 0, finite; 0: the top token (ties to the lowest index) */
+    int32_t top_k;     /* 0 = all */
+    float top_p;       /* in (0, 1]; 1 = all */
+    float min_p;       /* in [0, 1]; 0 = all */
+} sv_sampling;
+
+/* Per row, with w_j = exp((z_j - max z) / temperature) of its logits z: of
+ * the tokens with a finite logit, in the order of falling z (equal ones by
+ * rising index), the first top_k are kept; of these the shortest leading run
+ * whose weights reach top_p of their sum; of these the weights of at least
+ * min_p (1 is the top token's).  tokens[i] = the least j at which the running
+ * sum of the kept weights, by rising index, exceeds u[i] times their sum: the
+ * inverse CDF that sv_accept_rejection samples with.
+ *   probs: the distribution that was sampled from, 0 for what was dropped:
+ *   what sv_accept_rejection takes as a drafter's q.
+ *   kept: the logits, -inf for what was dropped: with them as its logits and
+ *   the same temperature, sv_accept_rejection accepts against the filtered
+ *   distribution.
+ * Weights are fp64 and summed as whole numbers of steps of 2^-s, s = min(51,
+ * 63 - ceil(log2 V)): exact in any order, so a row's results depend on
+ * nothing but the row.  Weights below half a step, 1e-9 of the row at most
+ * for V = 151936, are never drawn.
+ * A row that holds NaN or +inf or no finite logit, or whose settings are out
+ * of range, fails: token -1, probs and kept NaN throughout.  A u outside
+ * [0, 1) gives token -1 alone.
+ *   logits [rows] rows of V, ld elements apart (V <= ld < 2^31); 1 <= rows <=
+ *   65535, 1 <= V <= 2^24.  params (device) [n_params], 4-byte aligned:
+ *   n_params = rows, or 1 for all rows alike.  u [rows] fp64.  tokens [rows]
+ *   int32; probs, kept [rows][V] fp32, overlapping neither each other nor the
+ *   logits; each may be NULL, one is given (u may be NULL without tokens).
+ *   workspace: sv_sample_workspace_bytes(rows, V) bytes, 256-byte aligned,
+ *   not shared by calls that run concurrently; needs no initialisation. */
+size_t sv_sample_workspace_bytes(int64_t rows, int64_t V);
+int sv_sample(const float *logits, int64_t rows, int64_t V, int64_t ld, const sv_sampling *params,
+              int32_t n_params, const double *u, int32_t *tokens, float *probs, float *kept,
+              void *workspace, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
 /* Key-value cache.                                                    */
 /* ------------------------------------------------------------------ */
 /* The attention history that a pass's q, k and v projections read and
@@ -430,6 +493,8 @@ typedef struct {
 #define SV_KV_NO_SLOT 8    /* append: a row's slot has no page; the row was dropped */
 #define SV_KV_BAD_COMMIT 16 /* commit: a count or path out of range; that sequence was left as it was */
 #define SV_KV_OVER_MAX 32  /* attention: a sequence longer than max_len; its rows are NaN */
+#define SV_KV_NOT_SHARED 64 /* attention over shared slots: a sequence that does not hold the first one's pages
+                         there; its rows are NaN */
 
 /* The sequences and new rows of a call.  An index outside [0, seqs) has no
  * rows.  Where a call writes, a sequence named twice counts once (its first
@@ -571,6 +636,25 @@ typedef struct {
 size_t sv_kv_attention_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn);
 int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const sv_kv_attn *attn, const float *q,
                     float *out, const sv_epilogue *ep, void *workspace, size_t ws_bytes, void *stream);
+
+/* The same for a batch whose sequences share a prefix: the first `shared`
+ * slots of each lie in the pages of the batch's first sequence (place 0 of
+ * the batch: the forks of one prompt, whose full pages sv_kv_fork shares).
+ * Of these slots as many whole chunks as there are (shared / chunk) are read
+ * once for the rows of all sequences; the rest of each sequence is its own.
+ * shared may be less than what the sequences share, and 0; it is at most width
+ * * page, and 0 with a window.  A sequence that does not hold a shared chunk's
+ * pages as the first does, or has fewer committed slots, is refused: its rows
+ * are NaN (SV_KV_NOT_SHARED); so are all where the first is out of range.
+ * A row's bits are those of sv_kv_attention with the same chunk length, given
+ * by the caller or by a rule (chunk 0) that counts the sharing in.  The
+ * queries of rows past n_new may be read here; nothing depends on them.  The
+ * workspace is that of sv_kv_attention_shared_workspace_bytes. */
+size_t sv_kv_attention_shared_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn,
+                                              int32_t shared);
+int sv_kv_attention_shared(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const sv_kv_attn *attn,
+                           int32_t shared, const float *q, float *out, const sv_epilogue *ep, void *workspace,
+                           size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* Measurement aid (not a step of the pass).                           */

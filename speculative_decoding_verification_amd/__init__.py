@@ -22,6 +22,7 @@ SV_EP_NONE, SV_EP_QUANT, SV_EP_PAIR = 0, 1, 2
 SV_KV_F16, SV_KV_BF16, SV_KV_I8 = 1, 30, 24
 SV_ROPE_NONE, SV_ROPE_PAIRS, SV_ROPE_HALVES = 0, 1, 2
 SV_KV_NO_PAGES, SV_KV_TOO_LONG, SV_KV_BAD_FORK, SV_KV_NO_SLOT, SV_KV_BAD_COMMIT, SV_KV_OVER_MAX = 1, 2, 4, 8, 16, 32
+SV_KV_NOT_SHARED = 64
 MAX_M = 16
 
 EXPORTS = [
@@ -33,7 +34,7 @@ EXPORTS = [
     "sv_accept_rejection_noalloc", "sv_read_bandwidth", "sv_kv_page_bytes", "sv_kv_data_bytes", "sv_kv_init",
     "sv_kv_reserve", "sv_kv_append", "sv_kv_read", "sv_kv_commit", "sv_kv_fork", "sv_kv_release",
     "sv_kv_compact_workspace_bytes", "sv_kv_compact", "sv_kv_status", "sv_kv_attention_workspace_bytes",
-    "sv_kv_attention",
+    "sv_kv_attention", "sv_kv_attention_shared_workspace_bytes", "sv_kv_attention_shared", "sv_add_norm_q8", "sv_sample_workspace_bytes", "sv_sample",
 ]
 
 
@@ -147,8 +148,17 @@ def lib():
                              ("sv_kv_status", i32, [kv, ctypes.POINTER(ctypes.c_uint32)]),
                              ("sv_kv_attention_workspace_bytes", sz, [kv, bt, ctypes.POINTER(KvAttn)]),
                              ("sv_kv_attention", i32, [kv, i32, bt, ctypes.POINTER(KvAttn), P, P,
-                                                       ctypes.POINTER(Epilogue), P, sz, P])):
+                                                       ctypes.POINTER(Epilogue), P, sz, P]),
+                             ("sv_kv_attention_shared_workspace_bytes", sz, [kv, bt, ctypes.POINTER(KvAttn), i32]),
+                             ("sv_kv_attention_shared", i32, [kv, i32, bt, ctypes.POINTER(KvAttn), i32, P, P,
+                                                              ctypes.POINTER(Epilogue), P, sz, P])):
             getattr(L, f).restype, getattr(L, f).argtypes = res, args
+        L.sv_add_norm_q8.restype = ctypes.c_int
+        L.sv_add_norm_q8.argtypes = [P, P, i64, i64, P, ctypes.c_float, i32, P, P, P, P, P, P, P]
+        L.sv_sample_workspace_bytes.restype = sz
+        L.sv_sample_workspace_bytes.argtypes = [i64, i64]
+        L.sv_sample.restype = ctypes.c_int
+        L.sv_sample.argtypes = [P, i64, i64, i64, P, i32, P, P, P, P, P, sz, P]
         for f in ("sv_repack_weights", "sv_unpack_weights", "sv_quantize_act_q8", "sv_verify_matvec",
                   "sv_head_logits", "sv_accept_greedy", "sv_accept_rejection", "sv_accept_rejection_noalloc",
                   "sv_pass_create",
@@ -394,3 +404,4 @@ def read_bandwidth(src, sink, stream=None):
 
 
 from .kv import KvCache, Rope, kv_page_bytes, rope_table  # noqa: E402,F401
+from .decode import add_norm_q8, sample, sample_workspace, sampling_params  # noqa: E402,F401

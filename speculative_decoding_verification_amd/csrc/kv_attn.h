@@ -39,6 +39,15 @@ struct AttnArgs {
     Div by_group, by_chunk, by_tiles, by_heads, by_turns;  // by_turns: by rot / 8
 };
 
+// The arguments of a call whose sequences hold the same pages in their first
+// `shared` chunks: row R of the call is row R - b * rows of sequence b.
+struct AttnShared : AttnArgs {
+    int32_t shared;        // chunks
+    int32_t shared_tiles;  // row groups of all sequences' rows
+    int32_t shared_grid;   // workgroups of the shared chunks, the first of the launch
+    Div by_rows, by_m, by_shared_tiles;
+};
+
 // What a sequence's rows see, in whole chunks.  Slots fit 32 bits (width *
 // page is below 2^31 - 65536).
 struct Span {
@@ -179,8 +188,13 @@ constexpr int kMaxLds = 79 * 1024;  // two workgroups a compute unit
 // 131001 slots, 95 against 148 in one twice, int8 batch 79 against 93).
 inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 || dim > 64 ? 2 : 4; }
 
+// Units: (sequence, head, chunk), in a call that shares chunks those of the
+// sequences' own chunks.
 int attn_launch_f16(const AttnArgs &a, int rt, int64_t units, hipStream_t st);
 int attn_launch_bf16(const AttnArgs &a, int rt, int64_t units, hipStream_t st);
 int attn_launch_i8(const AttnArgs &a, int rt, int64_t units, hipStream_t st);
+int attn_launch_f16(const AttnShared &a, int rt, int64_t units, hipStream_t st);
+int attn_launch_bf16(const AttnShared &a, int rt, int64_t units, hipStream_t st);
+int attn_launch_i8(const AttnShared &a, int rt, int64_t units, hipStream_t st);
 
 }  // namespace sv

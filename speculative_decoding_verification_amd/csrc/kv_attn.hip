@@ -248,13 +248,23 @@ static int chunk_rule(int64_t pairs, bool batch, int64_t bound, int64_t window, 
     return c;
 }
 
+// The same where `shared` slots are taken once for all rows, in `tiles` row
+// groups.
+static int chunk_rule_shared(int64_t heads, int64_t B, int64_t tiles, int64_t own_tiles, int64_t bound, int64_t shared) {
+    for (int c = 256; c <= 16384 && c <= shared; c += 128) {
+        const int64_t units = heads * (tiles * (shared / c) + B * own_tiles * ((bound - shared / c * c + c - 1) / c));
+        if (units <= 512) return c;
+    }
+    return 2048;
+}
+
 struct Plan {
     int64_t bound, units;
     int rt;
     size_t o_m, o_l, bytes;
 };
 
-static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, AttnArgs *a, Plan *p) {
+static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, int64_t shared, AttnShared *a, Plan *p) {
     SV_REQUIRE(at, SV_ERR_ARG, "kv_attention: NULL arguments");
     SV_REQUIRE(at->q_heads >= 1 && at->q_heads % d.heads == 0 && at->q_heads / d.heads <= 64, SV_ERR_SHAPE,
                "kv_attention: q_heads must be a multiple of heads, at most 64 times");
@@ -279,18 +289,37 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     a->window = at->window;
     a->sinks = at->sinks;
     a->max_len = at->max_len;
-    a->chunk = at->chunk ? at->chunk : chunk_rule(static_cast<int64_t>(bt->B) * d.heads, bt->B > 1, p->bound, at->window, at->sinks);
+    a->scale = at->scale * 1.44269504088896340736f;
+    SV_REQUIRE(shared >= 0 && shared <= cap, SV_ERR_ARG, "kv_attention: shared must be in [0, width * page]");
+    SV_REQUIRE(shared == 0 || at->window == 0, SV_ERR_ARG, "kv_attention: a window and shared slots do not go together");
+    shared = std::min(shared, p->bound);
+    const int64_t all_rows = static_cast<int64_t>(bt->B) * a->rows;
+    int rt = attn_tiles_per_wave(d.dim, static_cast<int>(all_rows));
+    auto tiles_of = [&](int64_t rows) { return (rows + 16 * rt - 1) / (16 * rt); };
+    a->chunk = at->chunk;
+    if (!a->chunk && shared >= 256 && bt->B > 1)
+        a->chunk = chunk_rule_shared(d.heads, bt->B, tiles_of(all_rows), tiles_of(a->rows), p->bound, shared);
+    if (!a->chunk) a->chunk = chunk_rule(static_cast<int64_t>(bt->B) * d.heads, bt->B > 1, p->bound, at->window, at->sinks);
     const int64_t chunks = chunks_within(p->bound, at->window, at->sinks, a->chunk);
     a->chunks = static_cast<int32_t>(chunks);
-    a->scale = at->scale * 1.44269504088896340736f;
-    p->rt = attn_tiles_per_wave(d.dim, a->rows);
-    a->tiles = (a->rows + 16 * p->rt - 1) / (16 * p->rt);
+    // one sequence, or one chunk, shares nothing
+    a->shared = bt->B > 1 && chunks > 1 ? static_cast<int32_t>(shared / a->chunk) : 0;
+    if (!a->shared) rt = attn_tiles_per_wave(d.dim, a->rows);
+    p->rt = rt;
+    a->tiles = static_cast<int32_t>(tiles_of(a->rows));
+    a->shared_tiles = static_cast<int32_t>(tiles_of(all_rows));
+    const int64_t shared_grid = (static_cast<int64_t>(a->shared) * d.heads + 7) / 8 * 8 * a->shared_tiles;
+    SV_REQUIRE(shared_grid < (1ll << 23), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
+    a->shared_grid = static_cast<int32_t>(shared_grid);
+    a->by_rows = div_by(a->rows);
+    a->by_m = div_by(bt->M);
+    a->by_shared_tiles = div_by(a->shared_tiles);
     a->by_group = div_by(a->group);
     a->by_chunk = div_by(a->chunk);
     a->by_tiles = div_by(a->tiles);
     a->by_heads = div_by(d.heads);
     a->by_turns = div_by(std::max(1, a->rope.rot / 8));
-    p->units = static_cast<int64_t>(bt->B) * d.heads * chunks;
+    p->units = static_cast<int64_t>(bt->B) * d.heads * (chunks - a->shared);
     SV_REQUIRE(p->units * a->tiles < (1ll << 23), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
     p->bytes = p->o_m = p->o_l = 0;
     if (chunks > 1) {
@@ -306,25 +335,36 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
 
 using namespace sv;
 
-extern "C" size_t sv_kv_attention_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn) {
+extern "C" size_t sv_kv_attention_shared_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn,
+                                                         int32_t shared) {
     KvDev d;
-    AttnArgs a{};
+    AttnShared a{};
     Plan p;
     if (kv_check(kv, "kv_attention", &d) || kv_check_batch(d, batch, "kv_attention", SV_MAX_M) ||
-        plan_of(d, batch, attn, &a, &p))
+        plan_of(d, batch, attn, shared, &a, &p))
         return 0;
     return p.bytes;
+}
+
+extern "C" size_t sv_kv_attention_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn) {
+    return sv_kv_attention_shared_workspace_bytes(kv, batch, attn, 0);
 }
 
 extern "C" int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const sv_kv_attn *attn,
                                const float *q, float *out, const sv_epilogue *ep, void *workspace, size_t ws_bytes,
                                void *stream) {
+    return sv_kv_attention_shared(kv, layer, batch, attn, 0, q, out, ep, workspace, ws_bytes, stream);
+}
+
+extern "C" int sv_kv_attention_shared(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, const sv_kv_attn *attn,
+                                      int32_t shared, const float *q, float *out, const sv_epilogue *ep, void *workspace,
+                                      size_t ws_bytes, void *stream) {
     KvDev d;
-    AttnArgs a{};
+    AttnShared a{};
     Plan p;
     int rc = kv_check(kv, "kv_attention", &d);
     if (!rc) rc = kv_check_batch(d, batch, "kv_attention", SV_MAX_M);
-    if (!rc) rc = plan_of(d, batch, attn, &a, &p);
+    if (!rc) rc = plan_of(d, batch, attn, shared, &a, &p);
     if (rc) return rc;
     SV_REQUIRE(layer >= 0 && layer < d.layers, SV_ERR_ARG, "kv_attention: layer out of range");
     const bool quant = ep && ep->mode != SV_EP_NONE;
@@ -354,14 +394,18 @@ extern "C" int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch
         a.part_l = reinterpret_cast<float *>(ws + p.o_l);
     }
     hipStream_t st = as_stream(stream);
-    rc = d.type == SV_KV_F16    ? attn_launch_f16(a, p.rt, p.units, st)
-         : d.type == SV_KV_BF16 ? attn_launch_bf16(a, p.rt, p.units, st)
-                                : attn_launch_i8(a, p.rt, p.units, st);
+    auto launch = [&](const auto &args) {
+        return d.type == SV_KV_F16    ? attn_launch_f16(args, p.rt, p.units, st)
+               : d.type == SV_KV_BF16 ? attn_launch_bf16(args, p.rt, p.units, st)
+                                      : attn_launch_i8(args, p.rt, p.units, st);
+    };
+    rc = a.shared ? launch(a) : launch(static_cast<const AttnArgs &>(a));
     if (rc || a.chunks == 1) return rc;
     const int of = kJoin / (d.dim / 4);
     if (static_cast<int64_t>(a.rows) * d.heads * batch->B >= kManyRows)
-        hipLaunchKernelGGL(kv_attn_join_rows_kernel, dim3((a.rows + of - 1) / of, d.heads, batch->B), dim3(kJoin), 0, st, a);
+        hipLaunchKernelGGL(kv_attn_join_rows_kernel, dim3((a.rows + of - 1) / of, d.heads, batch->B), dim3(kJoin), 0, st, static_cast<const AttnArgs &>(a));
     else
-        hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(kShares * (d.dim / 4)), 0, st, a);
+        hipLaunchKernelGGL(kv_attn_join_kernel, dim3(a.rows, d.heads, batch->B), dim3(kShares * (d.dim / 4)), 0, st,
+                           static_cast<const AttnArgs &>(a));
     return hip_check(hipGetLastError(), "kv_attention join launch");
 }

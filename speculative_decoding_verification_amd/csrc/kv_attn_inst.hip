@@ -343,18 +343,36 @@ __device__ __forceinline__ const float *query_of(const AttnArgs &a, int b, int h
     return a.q + ((static_cast<int64_t>(b) * a.bt.M + m) * a.q_heads + head * a.group + (r - m * a.group)) * a.kv.dim;
 }
 
+// Position of new row m of sequence b, whose length is `len`.
+__device__ __forceinline__ int place_of(const AttnArgs &a, int len, int b, int m) {
+    return len + (a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m);
+}
+// The same where sequences share chunks: rows m are numbered through all
+// sequences (b and len are not used).
+__device__ __forceinline__ int place_of(const AttnShared &a, int, int, int m) {
+    const int b = a.by_m(m), sid = a.bt.seq ? gld(a.bt.seq + b) : b;
+    const int len = sid >= 0 && sid < a.kv.seqs ? static_cast<int>(kv_len_of(a.kv, sid)) : 0;
+    return place_of(static_cast<const AttnArgs &>(a), len, b, m - b * a.bt.M);
+}
+
+// Positions whose angles are staged: as many as one sequence has rows.  Tiles
+// of several sequences' rows may have more; then they are read where they are.
+__device__ __forceinline__ bool angles_staged(const AttnArgs &a, int row0, int n) {
+    return a.rope.rot % 8 == 0 && a.by_group(row0 + n - 1) - a.by_group(row0) < SV_MAX_M;
+}
+
 // Requests n rows' queries and, unless a rotation's quads of pairs are not
 // whole, the angles of their positions [position][rot].
-template <int D, int W>
-__device__ __forceinline__ void stage_rows(const AttnArgs &a, int len, int b, int head, int row0, int n, int wave,
+template <int D, int W, typename Args>
+__device__ __forceinline__ void stage_rows(const Args &a, int len, int b, int head, int row0, int n, int wave,
                                            uint32_t staged, uint32_t angles) {
     const int lane = threadIdx.x & 63;
-    if (a.rope.mode != SV_ROPE_NONE && a.rope.rot % 8 == 0) {
+    if (a.rope.mode != SV_ROPE_NONE && angles_staged(a, row0, n)) {
         const int m0 = a.by_group(row0), of = a.by_group(row0 + n - 1) - m0 + 1;
-        int depth = m0 + lane;
-        if (a.bt.tree && lane < of) depth = __popc(row_mask(a, b, depth) & ((1u << depth) - 1));
+        int at = 0;
+        if (lane < of) at = place_of(a, len, b, m0 + lane);
         for (int i = wave; i < of; i += W) {
-            const int pos = min(len + __builtin_amdgcn_readlane(depth, i), a.rope.n_pos - 1);
+            const int pos = min(__builtin_amdgcn_readlane(at, i), a.rope.n_pos - 1);
             if (lane < a.rope.rot / 4)
                 to_lds<false>(reinterpret_cast<const uint8_t *>(a.rope.table + static_cast<int64_t>(pos) * a.rope.rot + 4 * lane),
                               angles + i * a.rope.rot * 4);
@@ -370,15 +388,15 @@ __device__ __forceinline__ void stage_rows(const AttnArgs &a, int len, int b, in
 }
 
 // Turns the staged rows by their angles, four pairs a thread and step.
-template <int D, int THREADS>
-__device__ __forceinline__ void turn_rows(const AttnArgs &a, int len, int b, int row0, int n, uint32_t staged,
+template <int D, int THREADS, typename Args>
+__device__ __forceinline__ void turn_rows(const Args &a, int len, int b, int row0, int n, uint32_t staged,
                                           uint32_t angles) {
     const int rot = a.rope.rot, m0 = a.by_group(row0);
-    if (rot % 8) {  // pair by pair, with the angles where they are
+    if (!angles_staged(a, row0, n)) {  // pair by pair, with the angles where they are
         for (int it = threadIdx.x; it < n * (rot / 2); it += THREADS) {
-            const int i = it / (rot / 2), p = it - i * (rot / 2), m = a.by_group(row0 + i);
-            const int depth = a.bt.tree ? __popc(row_mask(a, b, m) & ((1u << m) - 1)) : m;
-            const float *cs = a.rope.table + static_cast<int64_t>(min(len + depth, a.rope.n_pos - 1)) * rot + 2 * p;
+            const int i = it / (rot / 2), p = it - i * (rot / 2);
+            const int pos = place_of(a, len, b, a.by_group(row0 + i));
+            const float *cs = a.rope.table + static_cast<int64_t>(min(pos, a.rope.n_pos - 1)) * rot + 2 * p;
             const int e0 = a.rope.mode == SV_ROPE_PAIRS ? 2 * p : p, e1 = a.rope.mode == SV_ROPE_PAIRS ? e0 + 1 : p + rot / 2;
             SV_LDS float *x0 = (SV_LDS float *)static_cast<uintptr_t>(quad_at<D>(staged, i, e0 / 4) + e0 % 4 * 4);
             SV_LDS float *x1 = (SV_LDS float *)static_cast<uintptr_t>(quad_at<D>(staged, i, e1 / 4) + e1 % 4 * 4);
@@ -463,7 +481,8 @@ __device__ __forceinline__ float take_queries(uint32_t staged, int from, int n, 
 struct Unit {
     int b, head, c;  // b = -1 past the last
 };
-__device__ __forceinline__ Unit find_unit(const AttnArgs &a, int u) {
+// With `skip` chunks shared, u counts only those after them.
+__device__ __forceinline__ Unit find_unit(const AttnArgs &a, int u, int skip) {
     const int lane = threadIdx.x & 63;
     int passed = 0;
     for (int sinks = 0; sinks <= (a.sinks ? 1 : 0); sinks++)
@@ -477,7 +496,7 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs &a, int u) {
                     if (n) {
                         const Span sp = span_of(a, static_cast<int>(kv_len_of(a.kv, sid)), n);
                         const int chunks = chunks_of(a, sp);
-                        first = min(sp.first, chunks);
+                        first = min(sp.first + skip, chunks);
                         own = sinks ? first : chunks - first;
                     }
                 }
@@ -494,19 +513,49 @@ __device__ __forceinline__ Unit find_unit(const AttnArgs &a, int u) {
     return Unit{-1, 0, 0};
 }
 
-template <int TYPE, int D, int RT>
+__device__ __forceinline__ int shared_of(const AttnArgs &) { return 0; }
+__device__ __forceinline__ int shared_of(const AttnShared &a) { return a.shared; }
+__device__ __forceinline__ int shared_tiles_of(const AttnArgs &a) { return a.tiles; }
+__device__ __forceinline__ int shared_tiles_of(const AttnShared &a) { return a.shared_tiles; }
+__device__ __forceinline__ int by_shared_tiles(const AttnArgs &a, int x) { return a.by_tiles(x); }
+__device__ __forceinline__ int by_shared_tiles(const AttnShared &a, int x) { return a.by_shared_tiles(x); }
+
+// Marks the sequences of a tile's rows that do not hold chunk c as `sid`
+// does: another page, none, or fewer committed slots.  Their rows' results
+// are NaN, and the status says so.
+__device__ __forceinline__ void find_strangers(const AttnShared &a, int sid, bool named, int c, int row0, int n,
+                                               int threads, int *s_bad) {
+    const int b0 = a.by_rows(row0), of = a.by_rows(row0 + n - 1) - b0 + 1;
+    const int e0 = c * a.chunk >> a.kv.page_shift, entries = (((c + 1) * a.chunk - 1) >> a.kv.page_shift) - e0 + 1;
+    for (int it = threadIdx.x; it < of * entries; it += threads) {
+        const int i = it / entries, e = e0 + it - i * entries, b = b0 + i;
+        const int own = a.bt.seq ? gld(a.bt.seq + b) : b;
+        if (own < 0 || own >= a.kv.seqs || kv_rows_of(a.bt.n_new, b, a.bt.M) == 0) continue;
+        const int page = kv_page_of(a.kv, own, e);
+        if (named && page >= 0 && page == kv_page_of(a.kv, sid, e) && kv_len_of(a.kv, own) >= (c + 1) * a.chunk) continue;
+        s_bad[i] = 1;
+        kv_flag(a.kv, SV_KV_NOT_SHARED);
+    }
+}
+
+// Args: AttnArgs, or AttnShared where the sequences share their first chunks.
+// These are taken once for the rows of all sequences, 16 RT of them a
+// workgroup, in the same way as a sequence's own: a row's bits are those of
+// the call that does not share.
+template <int TYPE, int D, int RT, typename Args>
 __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::TWO ? 2 : 1)) void kv_attn_kernel(
-    AttnArgs a) {
+    Args a) {
     using Kd = Kind<TYPE>;
     using S = Shape<TYPE, D, RT>;
-    fetch_args<sizeof(AttnArgs)>();
+    constexpr bool SHARED = __is_same(Args, AttnShared);
+    fetch_args<sizeof(Args)>();
     constexpr int NC = D / 32, ND = D / 16, ESZ = Kd::esz, W = S::W, LD = S::LD, ROWS = S::ROWS;
     // Read past the caches.  Meant for blocks that one row group reads, which
     // dim and row tiles do not quite say: from 33 rows on, dims of 96 and 128
     // have several groups, whose second reading the placement below would let
     // L2 serve (80 rows of 128 over 8191 slots take 38 us), and up to 64 rows of
     // at most 64 are one.
-    constexpr bool ONCE = D <= 128 && RT < 4;
+    constexpr bool ONCE = D <= 128 && RT < 4 && !SHARED;
     extern __shared__ __align__(1024) uint8_t s_mem[];
     __shared__ float s_m[W][ROWS], s_l[W][ROWS];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -514,26 +563,49 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
     const int heads = a.kv.heads;
     // Row groups of one chunk read the same blocks: eight workgroups apart,
     // so that the same XCD takes them and its L2 serves the second reading.
-    const int x = blockIdx.x;
-    const int u8 = a.by_tiles(x / 8), tile = x / 8 - u8 * a.tiles, u = u8 * 8 + x % 8;
-    const bool alone = a.chunks == 1;  // no join: this workgroup finishes the rows
+    int x = blockIdx.x;
+    bool all = false;  // a shared chunk: rows of all sequences
+    if constexpr (SHARED) {
+        all = x < a.shared_grid;
+        if (!all) x -= a.shared_grid;
+    }
+    const int tiles = SHARED && all ? shared_tiles_of(a) : a.tiles;
+    const int u8 = SHARED && all ? by_shared_tiles(a, x / 8) : a.by_tiles(x / 8), tile = x / 8 - u8 * tiles, u = u8 * 8 + x % 8;
+    const bool alone = !SHARED && a.chunks == 1;  // no join: this workgroup finishes the rows
     Unit unit;
     if (alone) {
         unit.b = a.by_heads(u);
         unit.head = u - unit.b * heads;
         unit.c = 0;
+    } else if (SHARED && all) {
+        unit.c = a.by_heads(u);
+        unit.head = u - unit.c * heads;
+        unit.b = 0;
+        if (unit.c >= shared_of(a)) return;
     } else {
-        unit = find_unit(a, u);
+        unit = find_unit(a, u, shared_of(a));
         if (unit.b < 0) return;
     }
     const int b = unit.b, head = unit.head, c = unit.c;
     if (b >= a.bt.B) return;
-    const int sid = a.bt.seq ? __builtin_amdgcn_readfirstlane(gld(a.bt.seq + b)) : b;
-    if (sid < 0 || sid >= a.kv.seqs) return;
+    // a shared chunk's pages are those of the call's first sequence
+    int sid = a.bt.seq ? __builtin_amdgcn_readfirstlane(gld(a.bt.seq + b)) : b;
+    const bool named = sid >= 0 && sid < a.kv.seqs;
+    if (!named) {
+        if (!all) return;
+        sid = 0;
+    }
     const int len = __builtin_amdgcn_readfirstlane(static_cast<int>(kv_len_of(a.kv, sid)));
-    const Span sp = span_of(a, len, __builtin_amdgcn_readfirstlane(kv_rows_of(a.bt.n_new, b, a.bt.M)));
-    const int row0 = tile * ROWS, rows = sp.n * a.group;  // of this sequence, in use
+    Span sp = span_of(a, len, __builtin_amdgcn_readfirstlane(kv_rows_of(a.bt.n_new, b, a.bt.M)));
+    const int row0 = tile * ROWS;
+    int rows = sp.n * a.group;  // of this sequence, in use
+    if (SHARED && all) {        // every slot of the chunk is seen by every row
+        rows = a.bt.B * a.rows;
+        sp.total = sp.len = (c + 1) * a.chunk;
+    }
     if (row0 >= rows) return;
+    __shared__ int s_bad[SHARED ? ROWS : 1];  // the tile's sequences that do not share the chunk
+    if (SHARED && threadIdx.x < ROWS) s_bad[threadIdx.x] = 0;
 
     // ---- the wave's blocks: every W-th one of the chunk, but for those
     // between the sinks and every row's window
@@ -595,7 +667,9 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
     auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
     const uint32_t staged = ring + S::STAGED, angles = ring + S::ANGLES;
     const int n_rows = min(ROWS, rows - row0);
-    stage_rows<D, W>(a, len, b, head, row0, n_rows, wave, staged, angles);
+    // rows numbered through the call's sequences where these share chunks
+    const int at_b = SHARED ? 0 : b, at_row = SHARED ? b * a.rows + row0 : row0;
+    stage_rows<D, W>(a, len, at_b, head, at_row, n_rows, wave, staged, angles);
     if (S::EARLY && any) {
         request_k();
         turn();
@@ -607,7 +681,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
     // ---- queries, once every wave's pieces are there
     asm volatile("s_barrier" ::: "memory");
     if (a.rope.mode != SV_ROPE_NONE) {
-        turn_rows<D, 64 * W>(a, len, b, row0, n_rows, staged, angles);
+        turn_rows<D, 64 * W>(a, len, at_b, at_row, n_rows, staged, angles);
         asm volatile("s_waitcnt lgkmcnt(0)\n s_barrier" ::: "memory");
     }
     typename Kd::KVec qf[RT][NC][Kd::kq];
@@ -681,7 +755,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         }
 
         // ---- what is visible, and the running softmax
-        const bool edge = page < 0 || s0 + kBlk > sp.len || (a.window && s0 < whole && s0 + kBlk > a.sinks);
+        const bool edge = (page < 0 && !(SHARED && all)) || s0 + kBlk > sp.len || (a.window && s0 < whole && s0 + kBlk > a.sinks);
         // slots of the lane group that any row of the tile sees, and those that all see
         uint32_t any_sees = edge ? 0u : 0xFFu, all_see = 0xFFu;
         uint32_t seen[RT];  // slots of the lane group that the lane's row sees
@@ -931,11 +1005,24 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         for (int i = 0; i < ND; i++)
             *reinterpret_cast<f4 *>(s_o + (wave * ROWS + 16 * t + col) * LD + 16 * i + 4 * g) = o[t][i];
     }
+    if constexpr (SHARED) {
+        if (all) find_strangers(a, sid, named, c, row0, n_rows, 64 * W, s_bad);
+    }
     __syncthreads();
     const int n = min(ROWS, rows - row0);
-    const int64_t part = ((static_cast<int64_t>(b) * heads + head) * a.chunks + c) * a.rows + row0;
+    const int64_t part0 = ((static_cast<int64_t>(b) * heads + head) * a.chunks + c) * a.rows + row0;
     for (int i = threadIdx.x; i < n * (D / 4); i += 64 * W) {
         const int r = i / (D / 4), d = i % (D / 4) * 4;
+        int64_t part = part0;
+        bool bad = false;
+        if constexpr (SHARED) {
+            if (all) {
+                const int of = a.by_rows(row0 + r), own = row0 + r - of * a.rows;
+                bad = s_bad[of - a.by_rows(row0)];
+                part = ((static_cast<int64_t>(of) * heads + head) * a.chunks + c) * a.rows + own - r;
+                if (own >= kv_rows_of(a.bt.n_new, of, a.bt.M) * a.group) continue;
+            }
+        }
         float top = s_m[0][r];
 #pragma unroll
         for (int w = 1; w < W; w++) top = fmaxf(top, s_m[w][r]);
@@ -956,7 +1043,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         } else {
             *(SV_GLOBAL f4 *)(a.part_o + (part + r) * D + d) = v;
             if (d == 0) {
-                gst(a.part_m + part + r, top);
+                gst(a.part_m + part + r, bad ? NAN : top);
                 gst(a.part_l + part + r, sum);
             }
         }
@@ -968,8 +1055,8 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
 }
 
 // Launches a variant: a workgroup per chunk that there can be, and row group.
-template <int TYPE, int D, int RT>
-static int launch_one(const AttnArgs &a, int64_t units, hipStream_t st) {
+template <int TYPE, int D, int RT, typename Args>
+static int launch_one(const Args &a, int64_t units, hipStream_t st) {
     using S = Shape<TYPE, D, RT>;
     static_assert(S::LDS <= kMaxLds, "LDS");
     if constexpr (S::LDS > 65536) {  // above the default, allowed once for each device
@@ -979,50 +1066,54 @@ static int launch_one(const AttnArgs &a, int64_t units, hipStream_t st) {
         if (rc) return rc;
         const uint64_t bit = dev < 64 ? 1ull << dev : 0;
         if (!(allowed.load() & bit)) {
-            rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT>),
+            rc = hip_check(hipFuncSetAttribute(reinterpret_cast<const void *>(&kv_attn_kernel<TYPE, D, RT, Args>),
                                                hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS),
                            "kv_attention: LDS size");
             if (rc) return rc;
             allowed.fetch_or(bit);
         }
     }
-    const unsigned grid = static_cast<unsigned>((units + 7) / 8 * 8 * a.tiles);
-    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
+    unsigned grid = static_cast<unsigned>((units + 7) / 8 * 8 * a.tiles);
+    if constexpr (__is_same(Args, AttnShared)) grid += a.shared_grid;
+    hipLaunchKernelGGL((kv_attn_kernel<TYPE, D, RT, Args>), dim3(grid), dim3(64 * S::W), S::LDS, st, a);
     return hip_check(hipGetLastError(), "kv_attention launch");
 }
 
-template <int TYPE, int D>
-static int launch_dim(const AttnArgs &a, int rt, int64_t units, hipStream_t st) {
+template <int TYPE, int D, typename Args>
+static int launch_dim(const Args &a, int rt, int64_t units, hipStream_t st) {
     if constexpr (D <= 64) {
-        if (rt == 4) return launch_one<TYPE, D, 4>(a, units, st);
+        if (rt == 4) return launch_one<TYPE, D, 4, Args>(a, units, st);
     }
     if constexpr (D <= 128) {
-        if (rt == 2) return launch_one<TYPE, D, 2>(a, units, st);
+        if (rt == 2) return launch_one<TYPE, D, 2, Args>(a, units, st);
     }
-    return launch_one<TYPE, D, 1>(a, units, st);
+    return launch_one<TYPE, D, 1, Args>(a, units, st);
 }
 
-template <int TYPE>
-static int launch_type(const AttnArgs &a, int rt, int64_t units, hipStream_t st) {
+template <int TYPE, typename Args>
+static int launch_type(const Args &a, int rt, int64_t units, hipStream_t st) {
     switch (a.kv.dim) {
-        case 32: return launch_dim<TYPE, 32>(a, rt, units, st);
-        case 64: return launch_dim<TYPE, 64>(a, rt, units, st);
-        case 96: return launch_dim<TYPE, 96>(a, rt, units, st);
-        case 128: return launch_dim<TYPE, 128>(a, rt, units, st);
-        case 160: return launch_dim<TYPE, 160>(a, rt, units, st);
-        case 192: return launch_dim<TYPE, 192>(a, rt, units, st);
-        case 224: return launch_dim<TYPE, 224>(a, rt, units, st);
-        case 256: return launch_dim<TYPE, 256>(a, rt, units, st);
+        case 32: return launch_dim<TYPE, 32, Args>(a, rt, units, st);
+        case 64: return launch_dim<TYPE, 64, Args>(a, rt, units, st);
+        case 96: return launch_dim<TYPE, 96, Args>(a, rt, units, st);
+        case 128: return launch_dim<TYPE, 128, Args>(a, rt, units, st);
+        case 160: return launch_dim<TYPE, 160, Args>(a, rt, units, st);
+        case 192: return launch_dim<TYPE, 192, Args>(a, rt, units, st);
+        case 224: return launch_dim<TYPE, 224, Args>(a, rt, units, st);
+        case 256: return launch_dim<TYPE, 256, Args>(a, rt, units, st);
     }
     return fail(SV_ERR_SHAPE, "kv_attention: unsupported head dimension");
 }
 
 #if SV_INST_KV == 1
 int attn_launch_f16(const AttnArgs &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_F16>(a, rt, units, st); }
+int attn_launch_f16(const AttnShared &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_F16>(a, rt, units, st); }
 #elif SV_INST_KV == 30
 int attn_launch_bf16(const AttnArgs &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_BF16>(a, rt, units, st); }
+int attn_launch_bf16(const AttnShared &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_BF16>(a, rt, units, st); }
 #else
 int attn_launch_i8(const AttnArgs &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_I8>(a, rt, units, st); }
+int attn_launch_i8(const AttnShared &a, int rt, int64_t units, hipStream_t st) { return launch_type<SV_KV_I8>(a, rt, units, st); }
 #endif
 
 }  // namespace sv

@@ -232,25 +232,29 @@ class KvCache:
         return v.value
 
     def attention(self, q_heads: int, B: int, M: int, scale=None, window: int = 0, sinks: int = 0, max_len: int = 0,
-                  chunk: int = 0) -> "Attention":
+                  chunk: int = 0, shared: int = 0) -> "Attention":
         """The attention of calls of up to B sequences of M rows, with a
         workspace of its own: calls that may run at once, in two captured
         graphs or on two streams, take one each, and a plan is kept until
-        what it enqueued on a stream other than its creation's has run."""
-        return Attention(self, q_heads, B, M, scale, window, sinks, max_len, chunk)
+        what it enqueued on a stream other than its creation's has run.
+        shared: the first slots of every sequence that lie in the pages of
+        the call's first sequence (forks of one prompt share its full
+        pages); they are read once for all."""
+        return Attention(self, q_heads, B, M, scale, window, sinks, max_len, chunk, shared)
 
 
 class Attention:
-    """sv_kv_attention for one shape of call: see KvCache.attention."""
+    """sv_kv_attention (with shared slots sv_kv_attention_shared) for one
+    shape of call: see KvCache.attention."""
 
-    def __init__(self, kv: KvCache, q_heads, B, M, scale, window, sinks, max_len, chunk):
+    def __init__(self, kv: KvCache, q_heads, B, M, scale, window, sinks, max_len, chunk, shared=0):
         sv = _sv()
-        self.kv, self.q_heads, self.B, self.M = kv, q_heads, B, M
+        self.kv, self.q_heads, self.B, self.M, self.shared = kv, q_heads, B, M, shared
         self.c = sv.KvAttn(q_heads, 1.0 / math.sqrt(kv.dim) if scale is None else scale, window, sinks, max_len,
                            chunk, None)
         b = sv.KvBatch(B, M, kv.lens.data_ptr() if B > kv.seqs else None)
         # a size of 0 is also the answer to an invalid shape: run() says which
-        self._n = int(kv._lib.sv_kv_attention_workspace_bytes(kv._ref, ctypes.byref(b), ctypes.byref(self.c)))
+        self._n = int(kv._lib.sv_kv_attention_shared_workspace_bytes(kv._ref, ctypes.byref(b), ctypes.byref(self.c), shared))
         self._ws = None
         if self._n:
             buf = kv._torch.empty(self._n + 256, dtype=kv._torch.uint8, device=kv.device)
@@ -270,6 +274,6 @@ class Attention:
         self.c.rope = None if rope is None else ctypes.addressof(rope.c)
         if rope is not None and rope.device is not None and rope.device != kv.device:
             raise _bad(f"kv: the rope table must be on {kv.device}")
-        kv._call(kv._lib.sv_kv_attention, layer, ctypes.byref(b), ctypes.byref(self.c), qp,
+        kv._call(kv._lib.sv_kv_attention_shared, layer, ctypes.byref(b), ctypes.byref(self.c), self.shared, qp,
                  kv._tensor(out, "out", f32), None if ep is None else ctypes.byref(ep),
                  None if self._ws is None else self._ws.data_ptr(), self._n, stream=stream)
