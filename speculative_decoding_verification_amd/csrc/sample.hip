@@ -48,11 +48,13 @@ typedef unsigned long long u64;
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));  // rows may begin anywhere
 
 constexpr int kRow = 1024;               // threads of a row's workgroup
+constexpr int kFinish = 256;             // and where a row's list is all it reads
 constexpr int kScan = 512;               // threads of a chunk's
 constexpr int kQuads = 8;                // quads of a chunk that a thread holds
 constexpr int kChunk = kScan * kQuads * 4;
-constexpr int kPer = 4, kList = kRow * kPer;  // listed elements that a row's workgroup holds
+constexpr int kList = 4096;              // listed elements that a row's workgroup holds
 constexpr int kBins = 1024;
+constexpr int kLevel = 512;              // parts that a range of keys is cut into
 constexpr int kDigits = 2048;
 constexpr int kSlots = 256;              // rows that are under way at once
 constexpr int kFlatGrid = 1024;          // workgroups of the passes over flat rows
@@ -95,6 +97,7 @@ struct SampleArgs {
     int32_t shift;    // weights in steps of 2^-shift
     int32_t row0, rows;
     int32_t chunks, cap;  // of a row; list entries of a chunk
+    int32_t group;        // chunks of a scanning workgroup
     const double *u;
     int32_t *tokens;
     float *probs, *kept;
@@ -127,29 +130,34 @@ __device__ __forceinline__ Settings settings_of(const SampleArgs &a, int r) {
     return s;
 }
 
-// 2^y for y <= 1000 or so (relative error about 2^-52; below 2^-1080: 0):
-// y = n + f, |f| <= 1/2, and the power series of 2^f up to f^12, whose rest is
-// below (ln 2 / 2)^13 / 13! = 2e-16.
+// 2^y for y <= 1000 (relative error 2^-50; below 2^-1080: 0): y = n + f, |f| <=
+// 1/2, 2^f = 1 + f q(f), and q of degree 9 through the ten Chebyshev points of
+// that range, worked out in 60 digits.
 __device__ __forceinline__ double exp2_of(double y) {
+    constexpr double kRound = 6755399441055744.0;  // 1.5 * 2^52
     y = fmax(y, -1100.0);
-    const double n = rint(y), x = (y - n) * 0.69314718055994530942;
-    double s = 1.0 / 479001600.0;
-    s = fma(s, x, 1.0 / 39916800.0);
-    s = fma(s, x, 1.0 / 3628800.0);
-    s = fma(s, x, 1.0 / 362880.0);
-    s = fma(s, x, 1.0 / 40320.0);
-    s = fma(s, x, 1.0 / 5040.0);
-    s = fma(s, x, 1.0 / 720.0);
-    s = fma(s, x, 1.0 / 120.0);
-    s = fma(s, x, 1.0 / 24.0);
-    s = fma(s, x, 1.0 / 6.0);
-    s = fma(s, x, 0.5);
-    s = fma(s, x, 1.0);
-    s = fma(s, x, 1.0);
-    return ldexp(s, static_cast<int>(n));
+    const double t = y + kRound, f = y - (t - kRound);
+    double q = 7.070977866508139e-09;
+    q = fma(q, f, 1.0205905413765595e-07);
+    q = fma(q, f, 1.3215451633221434e-06);
+    q = fma(q, f, 1.5252672924850737e-05);
+    q = fma(q, f, 0.00015403530424776529);
+    q = fma(q, f, 0.0013333558200794592);
+    q = fma(q, f, 0.009618129107618665);
+    q = fma(q, f, 0.05550410866465167);
+    q = fma(q, f, 0.24022650695910075);
+    q = fma(q, f, 0.6931471805599462);
+    return ldexp(fma(q, f, 1.0), static_cast<int>(__double_as_longlong(t)));
 }
 __device__ __forceinline__ double weight_of(float z, float one, double per) {
     return exp2_of((static_cast<double>(z) - static_cast<double>(one)) * per);
+}
+// The same relative to the sample's largest value, in one rounding less: a
+// factor that all weights of a row share does not matter.  shift_of = -ref *
+// per; not for (z - ref) * per past 1000.
+__device__ __forceinline__ double shift_of(float ref, double per) { return -(static_cast<double>(ref) * per); }
+__device__ __forceinline__ double loose_weight(float z, double per, double shift) {
+    return exp2_of(fma(static_cast<double>(z), per, shift));
 }
 // w in [0, 1] to the nearest multiple of 2^-shift: 2^(52 - shift) + w leaves
 // the multiple in the low bits of its fraction.
@@ -175,34 +183,68 @@ struct Border {
 __device__ __forceinline__ Border no_border() { return Border{float_key(-INFINITY), 0}; }
 
 // ------------------------------------------------- sums over a workgroup
+// By moves within the registers (rows of 16 lanes, then across them): a lane
+// exchange through LDS would wait for its six steps one by one.
+template <int CTRL, int ROWS, typename T>
+__device__ __forceinline__ T moved(T v, T other) {  // `other` where the move gives no value
+    constexpr int N = sizeof(T) / 4;
+    uint32_t w[N], o[N];
+    __builtin_memcpy(w, &v, sizeof(T));
+    __builtin_memcpy(o, &other, sizeof(T));
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        w[i] = __builtin_amdgcn_update_dpp(static_cast<int>(o[i]), static_cast<int>(w[i]), CTRL, ROWS, 0xF, false);
+    __builtin_memcpy(&v, w, sizeof(T));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T lane_of(T v, int lane) {
+    constexpr int N = sizeof(T) / 4;
+    uint32_t w[N];
+    __builtin_memcpy(w, &v, sizeof(T));
+#pragma unroll
+    for (int i = 0; i < N; i++) w[i] = __builtin_amdgcn_readlane(static_cast<int>(w[i]), lane);
+    __builtin_memcpy(&v, w, sizeof(T));
+    return v;
+}
+// v of the lanes up to and with this one, joined by f; none joins to nothing.
+template <typename T, typename F>
+__device__ __forceinline__ T wave_join(T v, T none, F f) {
+    v = f(v, moved<0x111, 0xF>(v, none));  // row_shr 1, 2, 4, 8
+    v = f(v, moved<0x112, 0xF>(v, none));
+    v = f(v, moved<0x114, 0xF>(v, none));
+    v = f(v, moved<0x118, 0xF>(v, none));
+    v = f(v, moved<0x142, 0xA>(v, none));  // row_bcast 15, 31
+    return f(v, moved<0x143, 0xC>(v, none));
+}
+template <typename T>
+__device__ __forceinline__ T wave_scan(T v) {
+    return wave_join(v, T(0), [](T a, T b) { return a + b; });
+}
 template <typename T>
 __device__ __forceinline__ T wave_sum(T v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    return lane_of(wave_scan(v), 63);
 }
 __device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-    return v;
+    return lane_of(wave_join(v, -INFINITY, [](float a, float b) { return fmaxf(a, b); }), 63);
 }
-template <typename T>
-__device__ __forceinline__ T wave_scan(T v) {  // sum of the lanes up to and with this one
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const T t = __shfl_up(v, o, 64);
-        if (lane >= o) v += t;
-    }
-    return v;
+// The same, NaN if one is NaN.
+__device__ __forceinline__ float most_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float wave_most(float v) {
+    return lane_of(wave_join(v, -INFINITY, [](float a, float b) { return most_of(a, b); }), 63);
+}
+__device__ __forceinline__ uint32_t wave_least(uint32_t v) {
+    return lane_of(wave_join(v, ~0u, [](uint32_t a, uint32_t b) { return min(a, b); }), 63);
+}
+__device__ __forceinline__ int wave_or(int v) {
+    return lane_of(wave_join(v, 0, [](int a, int b) { return a | b; }), 63);
 }
 // Sum over the threads before this one; *all is that over all.  `room` holds a
-// value for each wave; it may be used again after the next barrier.
+// value for each wave and is not in use.
 template <int THREADS, typename T>
-__device__ __forceinline__ T block_scan(T *room, T v, T *all) {
+__device__ __forceinline__ T scan_once(T *room, T v, T *all) {
     const int wave = threadIdx.x >> 6;
     const T upto = wave_scan(v);
-    __syncthreads();
     if ((threadIdx.x & 63) == 63) room[wave] = upto;
     __syncthreads();
     T before = 0, sum = 0;
@@ -214,112 +256,137 @@ __device__ __forceinline__ T block_scan(T *room, T v, T *all) {
     *all = sum;
     return before + upto - v;
 }
+template <int THREADS, typename T>
+__device__ __forceinline__ T block_scan(T *room, T v, T *all) {
+    __syncthreads();
+    return scan_once<THREADS>(room, v, all);
+}
 
+template <int THREADS>
 struct RowShared {
+    static constexpr int W = THREADS / 64;
     union {
-        u64 hist[kDigits];
-        struct {
-            float z[kList];
-            int32_t j[kList];
-        } list;
+        u64 hist[THREADS == kRow ? kDigits : 1];  // of slow rows
+        u64 sums[THREADS == kRow ? kRow : 1];     // of chunks
     };
-    uint32_t count[kBins];
-    union {
-        u64 wave[kRow / 64];
-        double wave_f[kRow / 64];
-    };
-    u64 above, amount;
+    // Amounts and numbers of the parts of a range, three in turn: a level
+    // clears the next one's and has one barrier.
+    u64 amount[3][kLevel];
+    uint32_t number[3][kLevel];
+    u64 wave[W], wave_n[W], wave_kept[W];
+    double wave_f[W];
+    float wave_top[W];
+    uint32_t wave_low[W];
+    int32_t wave_flags[W];
+    u64 above;
     double base;
-    uint32_t lo, hi;
-    int32_t digit, at, last, flags;
+    int32_t digit, at, last;
     int32_t offsets[kRow + 1];
 };
 
 // --------------------------------------- a border among listed elements
-// Thread t holds elements kPer t .. of a list that is in the order of the
-// indices; `in` says which are eligible.  Border of the first `want` (of their
-// amounts) of them in falling order; want <= the sum.
-template <bool MASS>
-__device__ Border border_of(RowShared &sh, const uint32_t (&key)[kPer], const int32_t (&j)[kPer], const bool (&in)[kPer],
-                            const u64 (&amount)[kPer], u64 want) {
-    const int tid = threadIdx.x;
+// Elements of a list in the order of the indices, each thread's own ones
+// consecutive: thread t holds those from per * t on.
+template <int THREADS>
+struct Listed {
+    static constexpr int PER = kList / THREADS;
+    uint32_t key[PER];
+    int32_t j[PER];
+    u64 steps[PER];
+    uint32_t in, over;  // bits: eligible; weight of at least min_p
+    int per;
+};
+
+// Border of the first `want` (elements, or steps) of the eligible ones in
+// falling order; want <= their sum, their keys in [lo, hi].  A level cuts the
+// range into 512 parts; every wave finds the part with the border by itself.
+// *turn: which of the three parts' counts the next level uses, 0 at first, with
+// amount[0] and number[0] cleared.
+template <int THREADS, bool MASS>
+__device__ Border border_of(RowShared<THREADS> &sh, int *turn, const Listed<THREADS> &l, u64 want, uint32_t lo, uint32_t hi) {
+    constexpr int PER = Listed<THREADS>::PER, each = kLevel / 64;
+    const int tid = threadIdx.x, lane = tid & 63;
     u64 above = 0;
-    uint32_t lo = ~0u, hi = 0;
-    __syncthreads();
-    if (tid == 0) {
-        sh.lo = ~0u;
-        sh.hi = 0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kPer; i++)
-        if (in[i]) {
-            lo = min(lo, key[i]);
-            hi = max(hi, key[i]);
+    for (;;) {
+        const int bits = hi > lo ? 32 - __clz(hi - lo) : 0, low = bits > 9 ? bits - 9 : 0;
+        const int now = *turn, next = now == 2 ? 0 : now + 1;
+        *turn = next;
+        for (int i = tid; i < kLevel; i += THREADS) {
+            sh.number[next][i] = 0;
+            sh.amount[next][i] = 0;
         }
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-        lo = min(lo, static_cast<uint32_t>(__shfl_xor(lo, o, 64)));
-        hi = max(hi, static_cast<uint32_t>(__shfl_xor(hi, o, 64)));
-    }
-    if ((tid & 63) == 0) {
-        atomicMin(&sh.lo, lo);
-        atomicMax(&sh.hi, hi);
-    }
-    __syncthreads();
-    lo = sh.lo;
-    hi = sh.hi;
-    for (;;) {
-        const int bits = hi > lo ? 32 - __clz(hi - lo) : 0, low = bits > 10 ? bits - 10 : 0;
-        __syncthreads();
-        sh.hist[tid] = 0;
-        sh.count[tid] = 0;
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kPer; i++)
-            if (in[i] && key[i] >= lo && key[i] <= hi) {
-                const int d = (key[i] - lo) >> low;
-                atomicAdd(&sh.count[d], 1u);
-                if (MASS) atomicAdd(&sh.hist[d], amount[i]);
+        for (int i = 0; i < PER; i++)
+            if (i < l.per && (l.in >> i & 1) && l.key[i] >= lo && l.key[i] <= hi) {
+                const int d = (l.key[i] - lo) >> low;
+                atomicAdd(&sh.number[now][d], 1u);
+                if (MASS) atomicAdd(&sh.amount[now][d], l.steps[i]);
             }
         __syncthreads();
-        const int d = kBins - 1 - tid;
-        const u64 h = MASS ? sh.hist[d] : sh.count[d];
-        u64 all;
-        const u64 before = above + block_scan<kRow>(sh.wave, h, &all);
-        if (before < want && before + h >= want) {
-            sh.digit = d;
-            sh.above = before;
-            sh.amount = h;
+        // lane i: the parts from the (8 i)-th highest on
+        u64 h[each], sum = 0;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            const int d = kLevel - 1 - lane * each - i;
+            h[i] = MASS ? sh.amount[now][d] : sh.number[now][d];
+            sum += h[i];
         }
-        __syncthreads();
-        lo += static_cast<uint32_t>(sh.digit) << low;
+        u64 before = above + wave_scan(sum) - sum;
+        const int at = __ffsll(__ballot(before < want && before + sum >= want)) - 1;
+        int d = 0;
+        u64 of = 0;
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            if (!found && before + h[i] >= want) {
+                found = true;
+                d = kLevel - 1 - lane * each - i;
+                of = h[i];
+            }
+            if (!found) before += h[i];
+        }
+        d = lane_of(d, at);
+        above = lane_of(before, at);
+        of = lane_of(of, at);
+        const uint32_t number = sh.number[now][d];
+        lo += static_cast<uint32_t>(d) << low;
         hi = min(hi, lo + ((1u << low) - 1));
-        above = sh.above;
-        const int number = sh.count[sh.digit];
-        // one element, or all of the digit's: nothing is left to be told apart
-        if (low > 0 && (number == 1 || (!MASS && above + sh.amount == want))) return Border{lo, INT32_MAX};
+        // one element, or all of the part's: nothing is left to be told apart
+        if (low > 0 && (number == 1 || (!MASS && above + of == want))) return Border{lo, INT32_MAX};
         if (low > 0) continue;
-        const u64 each = sh.amount / number, need = (want - above + each - 1) / each;
-        if (need >= static_cast<u64>(number)) return Border{lo, INT32_MAX};
+        const u64 one = of / number, need = (want - above + one - 1) / one;
+        if (need >= number) return Border{lo, INT32_MAX};
         // the first `need` of the equal ones
-        u64 mine = 0;
+        u64 mine = 0, all;
 #pragma unroll
-        for (int i = 0; i < kPer; i++) mine += in[i] && key[i] == lo;
-        u64 upto = block_scan<kRow>(sh.wave, mine, &all);
+        for (int i = 0; i < PER; i++) mine += (l.in >> i & 1) && l.key[i] == lo;
+        u64 upto = block_scan<THREADS>(sh.wave, mine, &all);
 #pragma unroll
-        for (int i = 0; i < kPer; i++)
-            if (in[i] && key[i] == lo && ++upto == need) sh.at = j[i] + 1;
+        for (int i = 0; i < PER; i++)
+            if ((l.in >> i & 1) && l.key[i] == lo && ++upto == need) sh.at = l.j[i] + 1;
         __syncthreads();
-        return Border{lo, sh.at};
+        const int cut = sh.at;
+        __syncthreads();
+        return Border{lo, cut};
     }
+}
+
+// The narrower of two borders, of which b tells apart only what a keeps.
+__device__ __forceinline__ Border both(Border a, Border b) {
+    return b.key > a.key ? b : Border{a.key, b.key == a.key ? min(a.cut, b.cut) : a.cut};
+}
+template <int THREADS>
+__device__ __forceinline__ void cut_to(Listed<THREADS> &l, Border b) {
+#pragma unroll
+    for (int i = 0; i < Listed<THREADS>::PER; i++)
+        if (!b.keeps(l.key[i], l.j[i])) l.in &= ~(1u << i);
 }
 
 // -------------------------------------- a border from the row, bit by bit
 // Moves the border so that the first `want` (of falling order) of what it
 // keeps remain: of `want` elements, or of steps of weight.
 template <bool MASS>
-__device__ void select(const SampleArgs &a, RowShared &sh, const float *row, float top, double per, u64 want,
+__device__ void select(const SampleArgs &a, RowShared<kRow> &sh, const float *row, float top, double per, u64 want,
                        Border *border) {
     const int tid = threadIdx.x;
     const Border from = *border;
@@ -389,7 +456,7 @@ __device__ __forceinline__ u64 threshold(double u, u64 total) {
 }
 // The first element of [j0, j1) at which the running sum of kept weights,
 // `passed` before them, exceeds `past`.
-__device__ int token_in(const SampleArgs &a, RowShared &sh, const float *row, int j0, int j1, u64 passed, u64 past,
+__device__ int token_in(const SampleArgs &a, RowShared<kRow> &sh, const float *row, int j0, int j1, u64 passed, u64 past,
                         Border border, float top, const Settings &s) {
     const int tid = threadIdx.x;
     for (; j0 < j1; j0 += kRow) {
@@ -409,7 +476,7 @@ __device__ int token_in(const SampleArgs &a, RowShared &sh, const float *row, in
     return sh.at;
 }
 
-__device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale, int token) {
+__device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale) {
     if (threadIdx.x) return;
     RowState st{};
     st.kind = kDone;
@@ -418,7 +485,10 @@ __device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, 
     st.cut = border.cut;
     st.scale = scale;
     a.state[r] = st;
-    if (a.tokens) gst(a.tokens + r, token);
+}
+__device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale, int token) {
+    done(a, r, border, top, scale);
+    if (threadIdx.x == 0 && a.tokens) gst(a.tokens + r, token);
 }
 __device__ __forceinline__ void failed(const SampleArgs &a, int r) {
     if (threadIdx.x) return;
@@ -431,7 +501,7 @@ __device__ __forceinline__ double number_of(const SampleArgs &a, int r) {
 }
 
 // A whole row by one workgroup: any case.
-__device__ void slow_row(const SampleArgs &a, RowShared &sh, int r, float top, const Settings &s) {
+__device__ void slow_row(const SampleArgs &a, RowShared<kRow> &sh, int r, float top, const Settings &s) {
     const float *row = row_of(a, r);
     const int tid = threadIdx.x;
     u64 n = 0, finite;
@@ -467,11 +537,10 @@ __device__ void slow_row(const SampleArgs &a, RowShared &sh, int r, float top, c
 struct Held {
     float z[kQuads][4];
     __device__ Held(const SampleArgs &a, const float *row, int c) {
-        const int64_t base = static_cast<int64_t>(c) * kChunk;
-        if (base + kChunk <= a.V) {
+        if ((c + 1) * kChunk <= a.V) {
 #pragma unroll
             for (int i = 0; i < kQuads; i++) {
-                const f4u v = *(const SV_GLOBAL f4u *)(row + base + (i * kScan + threadIdx.x) * 4);
+                const f4u v = *(const SV_GLOBAL f4u *)(row + c * kChunk + (i * kScan + threadIdx.x) * 4);
 #pragma unroll
                 for (int e = 0; e < 4; e++) z[i][e] = v[e];
             }
@@ -480,202 +549,226 @@ struct Held {
             for (int i = 0; i < kQuads; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const int64_t j = base + (i * kScan + threadIdx.x) * 4 + e;
-                    z[i][e] = j < a.V ? gld(row + j) : -INFINITY;
+                    const int j = c * kChunk + (i * kScan + threadIdx.x) * 4 + e;
+                    const float v = gld(row + min(j, a.V - 1));
+                    z[i][e] = j < a.V ? v : -INFINITY;
                 }
         }
     }
 };
-// Places of a thread's chosen elements in the chunk's list, which is in the
-// order of the indices.  bits[i]: chosen of quad i.  Returns their number.
-struct Places {
-    int at[kQuads];
-};
-__device__ __forceinline__ int places_of(u64 (*room)[2], const uint32_t (&bits)[kQuads], Places *out) {
-    static_assert(kQuads == 8, "two words of four counts");
-    u64 v[2] = {0, 0};
+// The chosen elements of a chunk, listed in the order of their indices.
+// masks[i][e]: the wave's lanes whose element e of quad i is chosen; room: 64
+// numbers.  Returns how many there are; its barrier comes after every wave's
+// work before the call.
+typedef u64 Masks[kQuads][4];
+__device__ __forceinline__ int list_out(const SampleArgs &a, int slot, int c, const Held &h, const Masks &masks, int *room) {
+    static_assert(kQuads * (kScan / 64) == 64, "a number for each lane");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int number[kQuads];
 #pragma unroll
-    for (int i = 0; i < kQuads; i++) v[i >> 2] += static_cast<u64>(__popc(bits[i])) << (16 * (i & 3));
-    const int wave = threadIdx.x >> 6;
-    const u64 upto[2] = {wave_scan(v[0]), wave_scan(v[1])};
+    for (int i = 0; i < kQuads; i++)
+        number[i] = __popcll(masks[i][0]) + __popcll(masks[i][1]) + __popcll(masks[i][2]) + __popcll(masks[i][3]);
+#pragma unroll
+    for (int i = 0; i < kQuads; i++)
+        if (lane == i) room[i * (kScan / 64) + wave] = number[i];
     __syncthreads();
-    if ((threadIdx.x & 63) == 63) {
-        room[wave][0] = upto[0];
-        room[wave][1] = upto[1];
-    }
-    __syncthreads();
-    u64 before[2] = {0, 0}, sum[2] = {0, 0};
-#pragma unroll
-    for (int w = 0; w < kScan / 64; w++)
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            if (w == wave) before[k] = sum[k];
-            sum[k] += room[w][k];
-        }
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < kQuads; i++) {
-        const int k = i >> 2, by = 16 * (i & 3);
-        out->at[i] = at + static_cast<int>((before[k] + upto[k] - v[k]) >> by & 0xFFFF);
-        at += static_cast<int>(sum[k] >> by & 0xFFFF);
-    }
-    return at;
-}
-__device__ __forceinline__ void list_out(const SampleArgs &a, int slot, int c, const Held &h, const uint32_t (&bits)[kQuads],
-                                         const Places &pl) {
+    const int own = room[lane], upto = wave_scan(own), all = lane_of(upto, 63);
     uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
 #pragma unroll
     for (int i = 0; i < kQuads; i++) {
-        int at = pl.at[i];
+        if (!number[i]) continue;
+        const int nth = i * (kScan / 64) + wave;
+        int at = lane_of(upto - own, nth);
 #pragma unroll
         for (int e = 0; e < 4; e++)
-            if (bits[i] >> e & 1) {
+            at += __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(masks[i][e] >> 32),
+                                            __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(masks[i][e]), 0));
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            if (masks[i][e] >> lane & 1) {
                 if (at < a.cap) list[at] = make_uint2(__float_as_uint(h.z[i][e]), c * kChunk + (i * kScan + threadIdx.x) * 4 + e);
                 at++;
             }
+        }
     }
+    return all;
 }
 
-// Elements that the list should have: some more than a top-k asks for.
-__device__ __forceinline__ int list_target(const Settings &s, int V) { return s.k < V ? max(256, min(3000, s.k + s.k / 2 + 200)) : 1024; }
+// Elements that the list should have: a thousand, or 2.5 times what a top-k
+// asks for (the threshold lets pass within 20 % or so of what it should).
+__device__ __forceinline__ int list_target(const Settings &s, int V) { return s.k < V ? min(2600, 2 * s.k + s.k / 2 + 200) : 1024; }
 
+// A workgroup takes `group` chunks one after the other, the next one's values
+// on their way.
 __global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
     __shared__ float s_sample[kScan / 64][64];
     __shared__ float s_tau, s_ref;
-    __shared__ u64 s_room[kScan / 64][2];
-    __shared__ double s_sum[kScan / 64];
-    __shared__ float s_top[kScan / 64];
-    __shared__ int s_rest;
-    const int c = blockIdx.x, slot = blockIdx.y, r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    if (c == 0 && slot == 0 && tid == 0) a.flat[0] = 0;
+    __shared__ int s_room[2][64];
+    __shared__ double s_sum[2][kScan / 64];
+    __shared__ float s_top[2][kScan / 64];
+    __shared__ int s_rest[2][kScan / 64];
+    const int slot = blockIdx.y, r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63;
+    const int c0 = blockIdx.x * a.group, c1 = min(c0 + a.group, a.chunks);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float *row = row_of(a, r);
-    const Settings s = settings_of(a, r);
-    const Held h(a, row, c);
 
-    // ---- the threshold: of 64 places of the row 64 values each (or of 8, or
-    // one), the largest of every 64 (8, 1) that lie 64 apart; of these 64 the
-    // one that the wanted part of the row's values should pass.
-    const float part = static_cast<float>(list_target(s, a.V)) / static_cast<float>(a.V);
-    const int of = part < 0.03f ? 64 : part < 0.2f ? 8 : 1;
-    float most = -INFINITY;
-    for (int i = wave; i < of; i += kScan / 64)
-        most = fmaxf(most, gld(row + static_cast<int64_t>(i) * (a.V - 64) / of + lane));
+    // ---- the threshold: of 64 places of the row (8, 1 in a short one) 64
+    // values each, the largest of those that lie at the same offset; of these
+    // 64 the one that the wanted part of the row's values should pass.
+    const int few = a.V >= 32768 ? 6 : a.V >= 12288 ? 3 : 0, of = 1 << few;
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        const int at = wave + i * (kScan / 64);  // past the last place: the first again
+        v[i] = gld(row + (static_cast<int64_t>(at < of ? at : 0) * (a.V - 64) >> few) + lane);
+    }
+    Held next(a, row, c0);
+    const Settings s = settings_of(a, r);
+    if (blockIdx.x == 0 && slot == 0 && tid == 0) a.flat[0] = 0;
+    float most = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; i++) most = fmaxf(most, v[i]);
     s_sample[wave][lane] = most;
-    if (tid == 0) s_rest = 0;
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
         for (int w = 1; w < kScan / 64; w++) most = fmaxf(most, s_sample[w][lane]);
-        const float none = powf(1.0f - part, static_cast<float>(of));
+        if (!(most > -INFINITY)) most = -INFINITY;  // NaN: the row fails
+        const float part = fminf(static_cast<float>(list_target(s, a.V)) / static_cast<float>(a.V), 0.999f);
+        const float none = __builtin_amdgcn_exp2f(__builtin_amdgcn_logf(1.0f - part) * static_cast<float>(of));
         const int nth = min(max(static_cast<int>(64.0f * (1.0f - none) + 0.5f), 1), 64) - 1;
         int rank = 0;
 #pragma unroll
         for (int i = 0; i < 64; i++) {
-            const float o = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(most), i));
+            const float o = lane_of(most, i);
             rank += o > most || (o == most && i < lane);
         }
         if (rank == nth) s_tau = most;
         if (rank == 0) s_ref = most;
     }
     __syncthreads();
-    const float tau = s_tau, ref = s_ref;
+    const float tau = s_tau, ref = s_ref, from = fmaxf(tau, -3.402823466e38f);  // finite ones alone
+    const bool summed = s.k == a.V && (s.p < 1.0 || s.least == 0.0);
+    const double less = shift_of(ref, s.per);
 
-    // ---- the chunk
-    float top = -INFINITY;
-    bool bad = false, rest = false;
-    uint32_t bits[kQuads];
+    // ---- the chunks
+    for (int c = c0; c < c1; c++) {
+        const int now = c & 1;
+        const Held h = next;
+        if (c + 1 < c1) next = Held(a, row, c + 1);
+        float top = h.z[0][0];
 #pragma unroll
-    for (int i = 0; i < kQuads; i++) {
-        bits[i] = 0;
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float z = h.z[i][e];
-            top = fmaxf(top, z);
-            bad |= !(z < INFINITY);
-            const bool some = z > -INFINITY, listed = some && z >= tau;
-            rest |= some && !listed;
-            bits[i] |= static_cast<uint32_t>(listed) << e;
+        for (int i = 0; i < kQuads; i++) {
+            top = most_of(most_of(top, h.z[i][0]), h.z[i][1]);
+            top = most_of(most_of(top, h.z[i][2]), h.z[i][3]);
         }
-    }
-    double sum = -1.0;
-    if (s.k == a.V && (s.p < 1.0 || s.least == 0.0)) {
-        sum = 0.0;
+        top = wave_most(top);
+        if (!(top < INFINITY)) top = NAN;
+        Masks masks;
 #pragma unroll
         for (int i = 0; i < kQuads; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) sum += weight_of(h.z[i][e], ref, s.per);
-        sum = wave_sum(sum);
-    }
-    top = wave_max(top);
-    if (__any(bad)) top = NAN;
-    rest = __any(rest);
-    if (lane == 0) {
-        s_sum[wave] = sum;
-        s_top[wave] = top;
-        if (rest) s_rest = 1;
-    }
-    Places pl;
-    const int n = places_of(s_room, bits, &pl);  // its barriers: the waves' values are there
-    list_out(a, slot, c, h, bits, pl);
-    if (tid == 0) {
-        ChunkRec rec{};
-        rec.top = s_top[0];
-        for (int w = 1; w < kScan / 64; w++) rec.top = rec.top != rec.top || s_top[w] != s_top[w] ? NAN : fmaxf(rec.top, s_top[w]);
-        rec.n = n;
-        rec.rest = s_rest;
-        rec.tau = tau;
-        rec.ref = ref;
-        rec.sum = s_sum[0];
-        for (int w = 1; w < kScan / 64; w++) rec.sum += sum < 0.0 ? 0.0 : s_sum[w];
-        a.recs[static_cast<int64_t>(slot) * a.chunks + c] = rec;
+            for (int e = 0; e < 4; e++) masks[i][e] = __ballot(h.z[i][e] >= from);
+        // any that are finite and not listed: most often the first ones tell
+        bool rest = false;
+#pragma unroll
+        for (int e = 0; e < 4; e++) rest |= h.z[0][e] < from && h.z[0][e] > -INFINITY;
+        int some = __any(rest);
+        if (!some) {
+#pragma unroll
+            for (int i = 1; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) rest |= h.z[i][e] < from && h.z[i][e] > -INFINITY;
+            some = __any(rest);
+        }
+        double sum = -1.0;
+        if (summed) {
+            sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sum += loose_weight(h.z[i][e], s.per, less);
+            sum = wave_sum(sum);
+        }
+        if (lane == 0) {
+            s_sum[now][wave] = sum;
+            s_top[now][wave] = top;
+            s_rest[now][wave] = some;
+        }
+        const int n = list_out(a, slot, c, h, masks, s_room[now]);
+        if (tid == 0) {
+            ChunkRec rec{};
+            rec.top = s_top[now][0];
+            rec.sum = s_sum[now][0];
+            rec.rest = s_rest[now][0];
+            for (int w = 1; w < kScan / 64; w++) {
+                rec.top = most_of(rec.top, s_top[now][w]);
+                rec.sum += s_sum[now][w];
+                rec.rest |= s_rest[now][w];
+            }
+            rec.n = n;
+            rec.tau = tau;
+            rec.ref = ref;
+            a.recs[static_cast<int64_t>(slot) * a.chunks + c] = rec;
+        }
     }
 }
 
 // ---------------------------------------------------------------- finish
-// A list of a row, kPer entries a thread; entries past it are not `in`.
-struct Listed {
-    uint32_t key[kPer];
-    int32_t j[kPer];
-    bool in[kPer];
-    float z[kPer];
-};
-// The chunks' lists one behind the other, through LDS: sh.offsets says where
-// each begins.
-__device__ __forceinline__ void take_lists(const SampleArgs &a, RowShared &sh, int slot, int n, Listed *out) {
-    const int tid = threadIdx.x, lane = tid & 63;
-    __syncthreads();
-    for (int c = tid >> 6; c < a.chunks; c += kRow / 64) {
-        const uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
-        const int at = sh.offsets[c], of = sh.offsets[c + 1] - at;
-        for (int i = lane; i < of; i += 64) {
-            const uint2 v = gld8(list + i);
-            sh.list.z[at + i] = __uint_as_float(v.x);
-            sh.list.j[at + i] = static_cast<int32_t>(v.y);
+// The chunks' lists one behind the other (sh.offsets says where each begins, a
+// barrier behind), n elements in all.
+template <int THREADS>
+__device__ __forceinline__ void take_lists(const SampleArgs &a, const RowShared<THREADS> &sh, int slot, int n, float top,
+                                           const Settings &s, Listed<THREADS> *l) {
+    l->per = (n + THREADS - 1) / THREADS;
+    l->in = l->over = 0;
+    int q = threadIdx.x * l->per, c = 0;
+    if (q < n) {  // the last chunk that begins at q or before
+        int to = a.chunks;
+        while (to - c > 1) {
+            const int mid = (c + to) >> 1;
+            if (sh.offsets[mid] <= q) c = mid;
+            else to = mid;
         }
     }
-    __syncthreads();
+    uint2 v[Listed<THREADS>::PER];
 #pragma unroll
-    for (int i = 0; i < kPer; i++) {
-        const int at = tid * kPer + i;
-        out->in[i] = at < n;
-        out->z[i] = at < n ? sh.list.z[at] : -INFINITY;
-        out->j[i] = at < n ? sh.list.j[at] : 0;
-        out->key[i] = float_key(out->z[i]);
+    for (int i = 0; i < Listed<THREADS>::PER; i++) {
+        v[i] = make_uint2(0xFF800000u, 0);
+        if (i < l->per && q < n) {
+            while (sh.offsets[c + 1] <= q) c++;
+            v[i] = gld8(a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap + (q - sh.offsets[c]));
+            l->in |= 1u << i;
+            q++;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < Listed<THREADS>::PER; i++) {
+        const float z = __uint_as_float(v[i].x);
+        l->j[i] = static_cast<int32_t>(v[i].y);
+        l->key[i] = float_key(z);
+        l->steps[i] = 0;
+        if (i < l->per && (l->in >> i & 1)) {
+            const double w = weight_of(z, top, s.per);
+            l->steps[i] = steps_of(w, a.shift);
+            l->over |= static_cast<uint32_t>(w >= s.least) << i;
+        }
     }
 }
-__device__ __forceinline__ u64 sum_of(RowShared &sh, const bool (&in)[kPer], const u64 (&amount)[kPer]) {
-    u64 n = 0, all;
+template <int THREADS>
+__device__ __forceinline__ u64 steps_in(const Listed<THREADS> &l, uint32_t which) {
+    u64 n = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; i++) n += in[i] ? amount[i] : 0;
-    block_scan<kRow>(sh.wave, n, &all);
-    return all;
+    for (int i = 0; i < Listed<THREADS>::PER; i++) n += which >> i & 1 ? l.steps[i] : 0;
+    return n;
 }
 
-// The token of a row without filters: of the chunks' sums (`own`, `before`
-// them and in all) the one that the number falls into, and in it the element.
-__device__ int token_unfiltered(const SampleArgs &a, RowShared &sh, const float *row, double own, double before, double past,
-                                float ref, double per) {
-    constexpr int each = kChunk / kRow;
+// The token of a row without filters: of the chunks' sums the one that the
+// number falls into, and in it the element.  A thread's chunks are [c0, c1),
+// their sum `own` and that of those before them `before`.
+__device__ int token_unfiltered(const SampleArgs &a, RowShared<kFinish> &sh, int slot, const float *row, int c0, int c1,
+                                double own, double before, double past, float ref, double per) {
+    constexpr int each = kChunk / kFinish;
     const int tid = threadIdx.x;
     __syncthreads();
     if (tid == 0) {
@@ -683,88 +776,144 @@ __device__ int token_unfiltered(const SampleArgs &a, RowShared &sh, const float 
         sh.last = 0;
     }
     __syncthreads();
-    if (tid < a.chunks && before + own > past) atomicMin(&sh.at, tid);
-    if (tid < a.chunks && own > 0.0) atomicMax(&sh.last, tid);
+    if (c0 < c1 && before + own > past) atomicMin(&sh.at, tid);
+    if (own > 0.0) atomicMax(&sh.last, tid);
     __syncthreads();
-    const int c = sh.at < INT32_MAX ? sh.at : sh.last;
-    if (tid == c) sh.base = before;
+    if (tid == (sh.at < INT32_MAX ? sh.at : sh.last)) {  // walks its chunks
+        int c = c0;
+        double base = before;
+        for (; c + 1 < c1; c++) {
+            const double next = base + a.recs[static_cast<int64_t>(slot) * a.chunks + c].sum;
+            if (next > past) break;
+            base = next;
+        }
+        sh.digit = c;
+        sh.base = base;
+    }
     __syncthreads();
     if (tid == 0) {
         sh.at = INT32_MAX;
         sh.last = 0;
     }
-    const double base = sh.base;
-    const int64_t j0 = static_cast<int64_t>(c) * kChunk + tid * each;
-    double w[each], mine = 0.0, all;
+    const double base = sh.base, less = shift_of(ref, per);
+    const int first = sh.digit * kChunk, j0 = first + tid * each;
+    double mine = 0.0, all;
+    if (first + kChunk <= a.V) {
+#pragma unroll 4
+        for (int i = 0; i < each; i += 4) {
+            const f4u z = *(const SV_GLOBAL f4u *)(row + j0 + i);
 #pragma unroll
-    for (int i = 0; i < each; i++) {
-        w[i] = j0 + i < a.V ? weight_of(gld(row + j0 + i), ref, per) : 0.0;
-        mine += w[i];
-    }
-    double upto = base + block_scan<kRow>(sh.wave_f, mine, &all);
-#pragma unroll
-    for (int i = each - 1; i >= 0; i--)
-        if (w[i] > 0.0) {
-            atomicMax(&sh.last, static_cast<int>(j0 + i));
-            break;
+            for (int e = 0; e < 4; e++) mine += loose_weight(z[e], per, less);
         }
-    bool found = false;
-#pragma unroll
-    for (int i = 0; i < each; i++) {
-        upto += w[i];
-        if (!found && w[i] > 0.0 && upto > past) {
-            atomicMin(&sh.at, static_cast<int>(j0 + i));
-            found = true;
+    } else {
+#pragma unroll 4
+        for (int i = 0; i < each; i++) {
+            const float z = gld(row + min(j0 + i, a.V - 1));
+            mine += j0 + i < a.V ? loose_weight(z, per, less) : 0.0;
         }
     }
+    const double upto = base + block_scan<kFinish>(sh.wave_f, mine, &all);
+    // the first thread that passes it; if roundings leave none, the last one
+    // with a weight
+    if (mine > 0.0 && upto + mine > past) atomicMin(&sh.at, tid);
+    if (mine > 0.0) atomicMax(&sh.last, tid);
     __syncthreads();
-    return sh.at < INT32_MAX ? sh.at : sh.last;
+    const int who = sh.at < INT32_MAX ? sh.at : sh.last;
+    if (tid == who) sh.base = upto;
+    __syncthreads();
+    // its 64 elements, one a lane
+    static_assert(each == 64, "a lane for each element");
+    const int j = first + who * each + (tid & 63);
+    const double w = j < a.V ? loose_weight(gld(row + j), per, less) : 0.0;
+    const double run = sh.base + wave_scan(w);
+    const u64 over = __ballot(w > 0.0 && run > past), some = __ballot(w > 0.0);
+    return first + who * each + (over ? __ffsll(over) - 1 : 63 - __clzll(some));
 }
 
-// WHOLE: the row fits the registers and is its own list.
+// WHOLE: the row is its own list.
 template <bool WHOLE>
-__global__ __launch_bounds__(kRow) void sample_finish_kernel(SampleArgs a) {
-    __shared__ RowShared sh;
-    const int slot = blockIdx.x, r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63;
+__global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
+    __shared__ RowShared<kFinish> sh;
+    constexpr int PER = Listed<kFinish>::PER, W = kFinish / 64;
+    const int slot = blockIdx.x, r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const float *row = row_of(a, r);
-    const Settings s = settings_of(a, r);
     enum { kBad = 1, kOver = 2, kRest = 4 };
+    int turn = 0;
+    for (int i = tid; i < kLevel; i += kFinish) {
+        sh.number[0][i] = 0;
+        sh.amount[0][i] = 0;
+    }
 
     // ---- what the chunks say, or the row itself
-    Listed l;
-    ChunkRec rec{};
-    float top = -INFINITY;
+    Listed<kFinish> l;
+    float z[WHOLE ? PER : 1];
+    float top = -INFINITY, ref = 0.0f, tau = INFINITY;
+    uint32_t low = ~0u;
     int flags = 0;
     u64 mine = 0;
+    double own = 0.0;
+    const int span = WHOLE ? (a.V + kFinish - 1) / kFinish : (a.chunks + kFinish - 1) / kFinish;
+    const int c0 = min(tid * span, a.chunks), c1 = min(c0 + span, a.chunks);
     if (WHOLE) {
+        l.per = span;
+        l.in = l.over = 0;
 #pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            l.j[i] = tid * kPer + i;
-            l.z[i] = l.j[i] < a.V ? gld(row + l.j[i]) : -INFINITY;
-            l.in[i] = l.z[i] > -INFINITY;
-            l.key[i] = float_key(l.z[i]);
-            if (!(l.z[i] < INFINITY)) flags = kBad;
-            top = fmaxf(top, l.z[i]);
-            mine += l.in[i];
+        for (int i = 0; i < PER; i++) {
+            l.j[i] = tid * span + i;
+            z[i] = i < span && l.j[i] < a.V ? gld(row + l.j[i]) : -INFINITY;
         }
-    } else if (tid < a.chunks) {
-        rec = a.recs[static_cast<int64_t>(slot) * a.chunks + tid];
-        top = rec.top;
-        flags = (rec.top != rec.top ? kBad : 0) | (rec.n > a.cap ? kOver : 0) | (rec.rest ? kRest : 0);
-        mine = static_cast<u64>(rec.n);
+#pragma unroll
+        for (int i = 0; i < PER; i++) {
+            l.key[i] = float_key(z[i]);
+            if (!(z[i] < INFINITY)) flags = kBad;
+            if (z[i] > -INFINITY) {
+                l.in |= 1u << i;
+                low = min(low, l.key[i]);
+            }
+            top = fmaxf(top, z[i]);
+        }
+        mine = __popc(l.in);
+    } else {
+        const ChunkRec *recs = a.recs + static_cast<int64_t>(slot) * a.chunks;
+        ref = gld(&recs->ref);
+        tau = gld(&recs->tau);
+        for (int c = c0; c < c1; c++) {
+            const ChunkRec rec = recs[c];
+            top = fmaxf(top, rec.top);
+            flags |= (rec.top != rec.top ? kBad : 0) | (rec.n > a.cap ? kOver : 0) | (rec.rest ? kRest : 0);
+            mine += static_cast<u64>(rec.n);
+            own += rec.sum;
+        }
     }
-    if (tid == 0) {
-        sh.flags = 0;
-        sh.hi = 0;
-    }
-    __syncthreads();
+    const Settings s = settings_of(a, r);
+    const double u = number_of(a, r);
     top = wave_max(top);
-    if (lane == 0) atomicMax(&sh.hi, float_key(top));
-    if (flags) atomicOr(&sh.flags, flags);
+    flags = wave_or(flags);
+    if (WHOLE) low = wave_least(low);
+    if (lane == 0) {
+        sh.wave_top[wave] = top;
+        sh.wave_flags[wave] = flags;
+        sh.wave_low[wave] = low;
+    }
+    double sum = -1.0, sum_before = 0.0;
+    if (!WHOLE) {
+        const double upto = wave_scan(own);
+        if (lane == 63) sh.wave_f[wave] = upto;
+        sum_before = upto - own;
+    }
     u64 total;
-    const u64 before = block_scan<kRow>(sh.wave, mine, &total);
-    top = value_of(sh.hi);
-    flags = sh.flags;
+    const u64 before = scan_once<kFinish>(sh.wave_n, mine, &total);
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+        top = fmaxf(top, sh.wave_top[w]);
+        flags |= sh.wave_flags[w];
+        low = min(low, sh.wave_low[w]);
+        if (!WHOLE) {
+            if (w == 0) sum = 0.0;
+            if (w == wave) sum_before += sum;
+            sum += sh.wave_f[w];
+        }
+    }
     if (!s.fine || (flags & kBad) || top == -INFINITY) {
         failed(a, r);
         return;
@@ -772,60 +921,48 @@ __global__ __launch_bounds__(kRow) void sample_finish_kernel(SampleArgs a) {
     const bool usable = WHOLE || (!(flags & kOver) && total <= kList);
     const int n = usable ? static_cast<int>(total) : 0;
     const bool rest = !WHOLE && (!usable || (flags & kRest));
-    double own = 0.0, sum_before = 0.0, sum = -1.0;
-    float ref = 0.0f, tau = INFINITY;
-    if (!WHOLE) {
-        const ChunkRec &first = a.recs[static_cast<int64_t>(slot) * a.chunks];
-        ref = gld(&first.ref);
-        if (usable) tau = gld(&first.tau);
-        own = tid < a.chunks ? rec.sum : 0.0;
-        __syncthreads();
-        sum_before = block_scan<kRow>(sh.wave_f, own, &sum);
-        if (usable) {
-            if (tid < a.chunks) sh.offsets[tid] = static_cast<int>(before);
-            if (tid == 0) sh.offsets[a.chunks] = n;
-            take_lists(a, sh, slot, n, &l);
-        } else {
+    const bool summed = !WHOLE && sum > 0.0 && (static_cast<double>(top) - static_cast<double>(ref)) * s.per < 900.0;
+    if (WHOLE) {
 #pragma unroll
-            for (int i = 0; i < kPer; i++) {
-                l.in[i] = false;
-                l.z[i] = -INFINITY;
-                l.key[i] = l.j[i] = 0;
+        for (int i = 0; i < PER; i++) {
+            l.steps[i] = 0;
+            if (i < span && (l.in >> i & 1)) {
+                const double w = weight_of(z[i], top, s.per);
+                l.steps[i] = steps_of(w, a.shift);
+                l.over |= static_cast<uint32_t>(w >= s.least) << i;
             }
         }
+    } else {
+        int at = static_cast<int>(before);
+        for (int c = c0; c < c1; c++) {
+            sh.offsets[c] = at;
+            at += a.recs[static_cast<int64_t>(slot) * a.chunks + c].n;
+        }
+        if (tid == 0) sh.offsets[a.chunks] = static_cast<int>(total);
+        __syncthreads();
+        take_lists(a, sh, slot, n, top, s, &l);
+        low = float_key(fmaxf(tau, -3.402823466e38f));
     }
-    const bool summed = sum > 0.0 && sum < INFINITY;
-    double w[kPer];
-    u64 steps[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
-        w[i] = weight_of(l.z[i], top, s.per);
-        steps[i] = l.in[i] ? steps_of(w[i], a.shift) : 0;
-    }
+    const uint32_t high = float_key(top);
 
     // ---- the border, where it is in the list
     Border border = no_border();
     bool within = !rest;  // what is kept is in the list
-    bool in[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; i++) in[i] = l.in[i];
-    auto cut_to = [&](Border b) {  // the narrower of the two: b tells apart only what is still in
-        if (b.key > border.key) border = b;
-        else if (b.key == border.key) border.cut = min(border.cut, b.cut);
-#pragma unroll
-        for (int i = 0; i < kPer; i++) in[i] = in[i] && border.keeps(l.key[i], l.j[i]);
-    };
     // min-p alone keeps it in the list (weights are monotonic to a step or two of fp64)
-    const bool low = weight_of(tau, top, s.per) * (1.0 + 1e-12) < s.least;
+    const bool short_of = usable && rest && weight_of(tau, top, s.per) * (1.0 + 1e-12) < s.least;
     int kind = kDone;
     u64 want = 0;
     if (s.k < n || (s.k == n && rest)) {
-        if (s.k < n) cut_to(border_of<false>(sh, l.key, l.j, in, steps, static_cast<u64>(s.k)));
+        if (s.k < n) {
+            border = border_of<kFinish, false>(sh, &turn, l, static_cast<u64>(s.k), low, high);
+            cut_to(l, border);
+            low = max(low, border.key);
+        }
         within = true;
     } else if (rest && s.k < a.V) {
         if (s.p < 1.0) {
             kind = kSlow;
-        } else if (!low) {
+        } else if (!short_of) {
             kind = kByCount;
             want = static_cast<u64>(s.k);
         } else {
@@ -833,7 +970,8 @@ __global__ __launch_bounds__(kRow) void sample_finish_kernel(SampleArgs a) {
         }
     }
     if (kind == kDone && s.p < 1.0) {
-        const u64 pool = sum_of(sh, in, steps);
+        u64 pool;
+        scan_once<kFinish>(sh.wave, steps_in(l, l.in), &pool);
         if (!within && !summed) {
             kind = kSlow;
         } else {
@@ -842,21 +980,22 @@ __global__ __launch_bounds__(kRow) void sample_finish_kernel(SampleArgs a) {
             want = goal < 1.0 ? 1 : static_cast<u64>(goal);
             if (within) want = min(want, pool);
             if (want <= pool) {
-                cut_to(border_of<true>(sh, l.key, l.j, in, steps, want));
+                const Border b = border_of<kFinish, true>(sh, &turn, l, want, low, high);
+                border = both(border, b);
+                cut_to(l, border);
                 within = true;
-            } else if (low) {
+            } else if (short_of) {
                 within = true;
             } else {
                 kind = kByMass;
             }
         }
     }
-    const double u = number_of(a, r);
     if (kind == kDone && !within) {
-        if (low) {
+        if (short_of) {
             within = true;
         } else if (s.least == 0.0 && summed) {
-            const int token = u >= 0.0 ? token_unfiltered(a, sh, row, own, sum_before, u * sum, ref, s.per) : -1;
+            const int token = u >= 0.0 ? token_unfiltered(a, sh, slot, row, c0, c1, own, sum_before, u * sum, ref, s.per) : -1;
             done(a, r, no_border(), top, 1.0 / (sum * weight_of(ref, top, s.per)), token);
             return;
         } else {
@@ -872,28 +1011,27 @@ __global__ __launch_bounds__(kRow) void sample_finish_kernel(SampleArgs a) {
             a.state[r] = st;
             a.flat[1 + add_dev(a.flat, 1)] = slot;
         }
-        a.bins[static_cast<int64_t>(slot) * kBins + tid] = 0;
+        for (int i = tid; i < kBins; i += kFinish) a.bins[static_cast<int64_t>(slot) * kBins + i] = 0;
         return;
     }
 
     // ---- the sum and the token
-    u64 kept = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
-        if (!in[i] || !(w[i] >= s.least)) steps[i] = 0;
-        kept += steps[i];
-    }
-    u64 all, upto = block_scan<kRow>(sh.wave, kept, &all);
+    const uint32_t keep = l.in & l.over;
+    u64 all, upto = scan_once<kFinish>(sh.wave_kept, steps_in(l, keep), &all);
     if (u >= 0.0) {
         const u64 past = threshold(u, all);
+        int token = -1;
 #pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            if (upto <= past && upto + steps[i] > past) sh.at = l.j[i];
-            upto += steps[i];
+        for (int i = 0; i < PER; i++) {
+            const u64 n = keep >> i & 1 ? l.steps[i] : 0;
+            if (upto <= past && upto + n > past) token = l.j[i];
+            upto += n;
         }
-        __syncthreads();
+        if (token >= 0 && a.tokens) gst(a.tokens + r, token);
+    } else if (tid == 0 && a.tokens) {
+        gst(a.tokens + r, -1);
     }
-    done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all), u >= 0.0 ? sh.at : -1);
+    done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all));
 }
 
 // ------------------------------------------------------------- flat rows
@@ -928,8 +1066,8 @@ __global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
 }
 
 __global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
-    __shared__ u64 s_room[kScan / 64][2], s_scan[kScan / 64], s_sum[kScan / 64], s_above;
-    __shared__ int s_bin;
+    __shared__ u64 s_scan[kScan / 64], s_sum[kScan / 64], s_above;
+    __shared__ int s_bin, s_room[64];
     const int items = gld(a.flat) * a.chunks, tid = threadIdx.x;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
@@ -962,27 +1100,22 @@ __global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
         }
         const int bin = s_bin;
         const float scale = bin_scale(s.per);
-        uint32_t bits[kQuads];
+        Masks masks;
         u64 sum = 0;
 #pragma unroll
-        for (int i = 0; i < kQuads; i++) {
-            bits[i] = 0;
+        for (int i = 0; i < kQuads; i++)
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 const float z = h.z[i][e];
-                if (!(z > -INFINITY)) continue;
-                const int b = bin_of(z, top, scale);
-                if (b == bin) bits[i] |= 1u << e;
+                const int b = z > -INFINITY ? bin_of(z, top, scale) : kBins + 1;
+                masks[i][e] = __ballot(b == bin);
                 if (b >= bin) continue;
                 const double w = weight_of(z, top, s.per);
                 if (w >= s.least) sum += steps_of(w, a.shift);
             }
-        }
         sum = wave_sum(sum);
         if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
-        Places pl;
-        const int n = places_of(s_room, bits, &pl);  // its barriers: the waves' sums are there
-        list_out(a, slot, c, h, bits, pl);
+        const int n = list_out(a, slot, c, h, masks, s_room);
         if (tid == 0) {
             ChunkRec rec{};
             rec.n = n;
@@ -998,7 +1131,7 @@ __global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
 }
 
 __global__ __launch_bounds__(kRow) void sample_settle_kernel(SampleArgs a) {
-    __shared__ RowShared sh;
+    __shared__ RowShared<kRow> sh;
     const int tid = threadIdx.x;
     if (static_cast<int>(blockIdx.x) >= gld(a.flat)) return;
     const int slot = gld(a.flat + 1 + blockIdx.x), r = a.row0 + slot;
@@ -1006,37 +1139,54 @@ __global__ __launch_bounds__(kRow) void sample_settle_kernel(SampleArgs a) {
     const Settings s = settings_of(a, r);
     ChunkRec rec{};
     if (st.kind != kSlow && tid < a.chunks) rec = a.recs[static_cast<int64_t>(slot) * a.chunks + tid];
+    for (int i = tid; i < kLevel; i += kRow) {
+        sh.number[0][i] = 0;
+        sh.amount[0][i] = 0;
+    }
     u64 total;
     // a list that does not hold its chunk's elements counts as too many
-    const u64 before = block_scan<kRow>(sh.wave, static_cast<u64>(rec.n > a.cap ? kList + 1 : rec.n), &total);
+    const u64 before = scan_once<kRow>(sh.wave_n, static_cast<u64>(rec.n > a.cap ? kList + 1 : rec.n), &total);
     if (st.kind == kSlow || total > kList) {
         slow_row(a, sh, r, st.top, s);
         return;
     }
     if (tid < a.chunks) sh.offsets[tid] = static_cast<int>(before);
     if (tid == 0) sh.offsets[a.chunks] = static_cast<int>(total);
-    Listed l;
-    take_lists(a, sh, slot, static_cast<int>(total), &l);
-    u64 steps[kPer];
-    double w[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
-        w[i] = weight_of(l.z[i], st.top, s.per);
-        steps[i] = l.in[i] ? steps_of(w[i], a.shift) : 0;
-    }
+    sh.sums[tid] = 0;
+    __syncthreads();
+    Listed<kRow> l;
+    take_lists(a, sh, slot, static_cast<int>(total), st.top, s, &l);
     Border border = no_border();
-    if (st.bin < kBins)
-        border = st.kind == kByCount ? border_of<false>(sh, l.key, l.j, l.in, steps, st.want - st.above)
-                                     : border_of<true>(sh, l.key, l.j, l.in, steps, st.want - st.above);
-    // the chunks' kept sums
-    __syncthreads();
-    sh.hist[tid] = 0;
-    __syncthreads();
+    if (st.bin < kBins) {
+        uint32_t low = ~0u, high = 0;
 #pragma unroll
-    for (int i = 0; i < kPer; i++)
-        if (l.in[i] && w[i] >= s.least && border.keeps(l.key[i], l.j[i])) atomicAdd(&sh.hist[l.j[i] / kChunk], steps[i]);
+        for (int i = 0; i < Listed<kRow>::PER; i++)
+            if (l.in >> i & 1) {
+                low = min(low, l.key[i]);
+                high = max(high, l.key[i]);
+            }
+        low = wave_least(low);
+        high = ~wave_least(~high);
+        if ((tid & 63) == 0) {
+            sh.wave_low[tid >> 6] = low;
+            sh.wave_flags[tid >> 6] = static_cast<int32_t>(high);
+        }
+        __syncthreads();
+        for (int w = 0; w < kRow / 64; w++) {
+            low = min(low, sh.wave_low[w]);
+            high = max(high, static_cast<uint32_t>(sh.wave_flags[w]));
+        }
+        int turn = 0;
+        border = st.kind == kByCount ? border_of<kRow, false>(sh, &turn, l, st.want - st.above, low, high)
+                                     : border_of<kRow, true>(sh, &turn, l, st.want - st.above, low, high);
+        cut_to(l, border);
+    }
+    // the chunks' kept sums
+#pragma unroll
+    for (int i = 0; i < Listed<kRow>::PER; i++)
+        if (l.in & l.over & 1u << i) atomicAdd(&sh.sums[l.j[i] / kChunk], l.steps[i]);
     __syncthreads();
-    const u64 own = rec.steps + sh.hist[tid];
+    const u64 own = rec.steps + sh.sums[tid];
     u64 all;
     const u64 upto = block_scan<kRow>(sh.wave, own, &all);
     const double u = number_of(a, r);
@@ -1055,32 +1205,45 @@ __global__ __launch_bounds__(kRow) void sample_settle_kernel(SampleArgs a) {
 }
 
 // --------------------------------------------------------------- outputs
-__global__ __launch_bounds__(kScan) void sample_out_kernel(SampleArgs a) {
-    const int c = blockIdx.x, r = a.row0 + blockIdx.y;
-    const Settings s = settings_of(a, r);
-    const Held h(a, row_of(a, r), c);
+constexpr int kOut = 256, kOutPiece = kOut * 8;
+__global__ __launch_bounds__(kOut) void sample_out_kernel(SampleArgs a) {
+    const int r = a.row0 + blockIdx.y;
+    const float *row = row_of(a, r);
+    const int j0 = blockIdx.x * kOutPiece + threadIdx.x * 4;
+    float z[2][4];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int j = j0 + i * kOut * 4;
+        if (j + 4 <= a.V) {
+            const f4u v = *(const SV_GLOBAL f4u *)(row + j);
+#pragma unroll
+            for (int e = 0; e < 4; e++) z[i][e] = v[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; e++) z[i][e] = j + e < a.V ? gld(row + j + e) : -INFINITY;
+        }
+    }
     const RowState st = a.state[r];
+    const Settings s = settings_of(a, r);
     const Border border{st.key, st.cut};
     const float none = st.kind == kFailed ? NAN : 0.0f, dropped = st.kind == kFailed ? NAN : -INFINITY;
     const int64_t base = static_cast<int64_t>(r) * a.V;
-    const bool whole = (c + 1) * static_cast<int64_t>(kChunk) <= a.V;
 #pragma unroll
-    for (int i = 0; i < kQuads; i++) {
-        const int64_t j = static_cast<int64_t>(c) * kChunk + (i * kScan + threadIdx.x) * 4;
+    for (int i = 0; i < 2; i++) {
+        const int j = j0 + i * kOut * 4;
         f4u p, k;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            const float z = h.z[i][e];
-            bool keep = st.kind == kDone && z > -INFINITY && border.keeps(float_key(z), static_cast<int>(j) + e);
+            bool keep = st.kind == kDone && z[i][e] > -INFINITY && border.keeps(float_key(z[i][e]), j + e);
             double w = 0.0;
             if (keep) {
-                w = weight_of(z, st.top, s.per);
+                w = weight_of(z[i][e], st.top, s.per);
                 keep = w >= s.least;
             }
             p[e] = keep ? static_cast<float>(w * st.scale) : none;
-            k[e] = keep ? z : dropped;
+            k[e] = keep ? z[i][e] : dropped;
         }
-        if (whole) {
+        if (j + 4 <= a.V) {
             if (a.probs) *(SV_GLOBAL f4u *)(a.probs + base + j) = p;
             if (a.kept) *(SV_GLOBAL f4u *)(a.kept + base + j) = k;
         } else {
@@ -1176,18 +1339,22 @@ extern "C" int sv_sample(const float *logits, int64_t rows, int64_t V, int64_t l
     for (int64_t row0 = 0; row0 < rows; row0 += p.slots) {
         a.row0 = static_cast<int32_t>(row0);
         a.rows = static_cast<int32_t>(std::min<int64_t>(p.slots, rows - row0));
-        const dim3 each(a.rows), pieces(p.chunks, a.rows);
+        const dim3 each(a.rows);
         if (p.whole) {
-            hipLaunchKernelGGL(sample_finish_kernel<true>, each, dim3(kRow), 0, st, a);
+            hipLaunchKernelGGL(sample_finish_kernel<true>, each, dim3(kFinish), 0, st, a);
         } else {
-            hipLaunchKernelGGL(sample_scan_kernel, pieces, dim3(kScan), 0, st, a);
-            hipLaunchKernelGGL(sample_finish_kernel<false>, each, dim3(kRow), 0, st, a);
+            // two workgroups a compute unit, if the rows give that many
+            a.group = std::max(1, a.rows * p.chunks / 512);
+            hipLaunchKernelGGL(sample_scan_kernel, dim3((p.chunks + a.group - 1) / a.group, a.rows), dim3(kScan), 0, st, a);
+            hipLaunchKernelGGL(sample_finish_kernel<false>, each, dim3(kFinish), 0, st, a);
             const dim3 flat(std::min(kFlatGrid, a.rows * p.chunks));
             hipLaunchKernelGGL(sample_bins_kernel, flat, dim3(kScan), 0, st, a);
             hipLaunchKernelGGL(sample_gather_kernel, flat, dim3(kScan), 0, st, a);
             hipLaunchKernelGGL(sample_settle_kernel, each, dim3(kRow), 0, st, a);
         }
-        if (probs || kept) hipLaunchKernelGGL(sample_out_kernel, pieces, dim3(kScan), 0, st, a);
+        if (probs || kept)
+            hipLaunchKernelGGL(sample_out_kernel, dim3(static_cast<unsigned>((V + kOutPiece - 1) / kOutPiece), a.rows), dim3(kOut), 0,
+                               st, a);
     }
     return hip_check(hipGetLastError(), "sample launch");
 }
