@@ -6,19 +6,6 @@
 
 namespace sv {
 
-// Division of 0 <= x < 2^31 by a number that the host knows.
-struct Div {
-    uint32_t m, sh;
-    __device__ __forceinline__ int operator()(int x) const {
-        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * m >> sh);
-    }
-};
-inline Div div_by(uint32_t d) {
-    uint32_t l = 0;
-    while ((1ull << l) < d) l++;
-    return Div{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
-}
-
 struct AttnArgs {
     KvDev kv;
     sv_kv_batch bt;
@@ -83,13 +70,6 @@ __device__ __forceinline__ int chunks_of(const AttnArgs &a, const Span &s) {
 }
 // Chunk of a launch's index c; at or past s.end: none.
 __device__ __forceinline__ int chunk_of(const Span &s, int c) { return c < s.first ? c : s.jump + (c - s.first); }
-
-// A value that the compiler takes as new, so that what follows from it is
-// formed where it is used and not kept in registers across a loop.
-__device__ __forceinline__ int fresh(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
-}
 
 __device__ __forceinline__ uint32_t row_mask(const AttnArgs &a, int b, int m) {
     return a.bt.tree ? gld(a.bt.tree + static_cast<int64_t>(b) * a.bt.M + m) : (2u << m) - 1;

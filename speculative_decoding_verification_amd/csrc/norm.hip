@@ -12,7 +12,7 @@
 // apart: lanes 4, 2 and 1 apart here, then the elements of a lane.  The row's
 // sum of squares is that of its blocks' sums, taken from LDS in an order that
 // K alone gives, so that a row's bits do not depend on the other rows.
-#include "kv_attn.h"
+#include "sv_internal.h"
 
 namespace sv {
 

@@ -17,27 +17,22 @@
 // V^2 2^-64 of the row (1e-9 for 151936).  Sums over a whole row that nothing
 // filters are fp64, in the order of its chunks.
 //
-// One pass over the logits decides nearly every row:
+// Two launches, and one pass over the logits for nearly every row:
 //   scan    a workgroup per chunk of a row: a sample of the row gives a
 //           threshold that about a thousand of its values pass; these are
 //           listed in the order of their indices, with the chunk's largest
 //           value and, if no top-k bounds what is kept, its sum of weights
 //           (relative to the sample's largest value: the row's is not known);
 //   finish  a workgroup per row: where what is kept lies within the list, the
-//           border, the sum and the token come from the list, held in
-//           registers; a row without filters takes its token from the chunks'
-//           sums and one chunk.
-// Rows whose kept set goes past the list (a flat distribution) take two more
-// passes, split over chunks as well:
-//   bins    amounts (elements, or steps of weight) by the distance from the
-//           largest value, 16 bins to a factor of 2, which gives the border's
-//           bin;
-//   gather  the elements of that bin are listed, the kept weights above it
-//           summed per chunk;
-//   settle  a workgroup per row, as finish.
+//           border, the sum and the token come from the list in LDS; a row
+//           without filters takes its token from the chunks' sums and one
+//           chunk.
+// A row whose kept set goes past the list (a flat distribution) is read twice
+// more by its workgroup: amounts (elements, or steps of weight) by the distance
+// from the largest value, which gives the border's bin; then that bin's
+// elements make a list, and the kept weights above it are summed per chunk.
 // What is left (a top-k past the list with a top-p as well, a bin of more
-// elements than a list holds) is done by a workgroup from the row itself, by
-// radix selection on the bits of z.
+// elements than a list holds) is selected on the bits of z, in nine passes.
 #include <algorithm>
 
 #include "sv_internal.h"
@@ -47,17 +42,17 @@ namespace sv {
 typedef unsigned long long u64;
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));  // rows may begin anywhere
 
-constexpr int kRow = 1024;               // threads of a row's workgroup
-constexpr int kFinish = 256;             // and where a row's list is all it reads
-constexpr int kScan = 512;               // threads of a chunk's
-constexpr int kQuads = 8;                // quads of a chunk that a thread holds
-constexpr int kChunk = kScan * kQuads * 4;
-constexpr int kList = 4096;              // listed elements that a row's workgroup holds
-constexpr int kBins = 1024;
+constexpr int kThreads = 512;             // of a workgroup
+constexpr int W = kThreads / 64;
+constexpr int kQuads = 4;                // quads of a chunk that a thread holds
+constexpr int kEach = kQuads * 4;        // elements
+constexpr int kChunk = kThreads * kEach;
+constexpr int kMaxChunks = (1 << 24) / kChunk;
+constexpr int kList = 2560;              // listed elements that a row's workgroup holds
+constexpr int kBins = 2048;
 constexpr int kLevel = 512;              // parts that a range of keys is cut into
 constexpr int kDigits = 2048;
 constexpr int kSlots = 256;              // rows that are under way at once
-constexpr int kFlatGrid = 1024;          // workgroups of the passes over flat rows
 constexpr int64_t kMaxVocab = 1 << 24;
 constexpr int64_t kMaxRows = 65535;
 
@@ -68,23 +63,15 @@ struct ChunkRec {
     int32_t rest;   // finite elements that are not listed: some, or none
     float tau, ref; // of the row: threshold of the list, the sample's largest value
     int32_t pad;
-    union {
-        double sum;  // of all weights, relative to ref; < 0: not formed
-        u64 steps;   // of the kept weights above the border's bin
-    };
+    double sum;     // of all weights, relative to ref; < 0: not formed
 };
 
-enum { kDone, kFailed, kByCount, kByMass, kNoBorder, kSlow };
-
-// A row's border and sum: what the outputs are made of, and what is known of
-// a row that is not done.
+// What the outputs of a row are made of.
 struct RowState {
-    int32_t kind, token;
+    int32_t failed;
     float top;
     uint32_t key;    // kept: keys above this one,
     int32_t cut;     // and those equal to it with a smaller index
-    int32_t bin;     // the border's
-    u64 want, above; // amounts: to be kept, and of the bins above
     double scale;    // weight times this: probability
 };
 
@@ -104,8 +91,6 @@ struct SampleArgs {
     RowState *state;  // [all rows]
     ChunkRec *recs;   // [slots][chunks]
     uint2 *lists;     // [slots][chunks][cap]: bits of z, index
-    u64 *bins;        // [slots][kBins]
-    int32_t *flat;    // number of flat rows, then their slots
 };
 
 __device__ __forceinline__ const float *row_of(const SampleArgs &a, int r) { return a.logits + static_cast<int64_t>(r) * a.ld; }
@@ -168,11 +153,9 @@ __device__ __forceinline__ u64 steps_of(double w, int shift) {
 __device__ __forceinline__ float value_of(uint32_t key) {
     return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
-__device__ __forceinline__ float bin_scale(double per) { return static_cast<float>(fmin(16.0 * per, 1e30)); }
-// Bin of a finite z, 16 to a factor of 2 in weight; the last one holds all
-// that is further.
-__device__ __forceinline__ int bin_of(float z, float top, float scale) {
-    return static_cast<int>(fminf((top - z) * scale, static_cast<float>(kBins - 1)));
+// Bin of a finite z; the last one holds all that is further.
+__device__ __forceinline__ int bin_of(float z, float top, float per_bin) {
+    return static_cast<int>(fminf((top - z) * per_bin, static_cast<float>(kBins - 1)));
 }
 
 struct Border {
@@ -241,7 +224,7 @@ __device__ __forceinline__ int wave_or(int v) {
 }
 // Sum over the threads before this one; *all is that over all.  `room` holds a
 // value for each wave and is not in use.
-template <int THREADS, typename T>
+template <typename T>
 __device__ __forceinline__ T scan_once(T *room, T v, T *all) {
     const int wave = threadIdx.x >> 6;
     const T upto = wave_scan(v);
@@ -249,25 +232,27 @@ __device__ __forceinline__ T scan_once(T *room, T v, T *all) {
     __syncthreads();
     T before = 0, sum = 0;
 #pragma unroll
-    for (int w = 0; w < THREADS / 64; w++) {
+    for (int w = 0; w < W; w++) {
         if (w == wave) before = sum;
         sum += room[w];
     }
     *all = sum;
     return before + upto - v;
 }
-template <int THREADS, typename T>
+template <typename T>
 __device__ __forceinline__ T block_scan(T *room, T v, T *all) {
     __syncthreads();
-    return scan_once<THREADS>(room, v, all);
+    return scan_once(room, v, all);
 }
 
-template <int THREADS>
 struct RowShared {
-    static constexpr int W = THREADS / 64;
     union {
-        u64 hist[THREADS == kRow ? kDigits : 1];  // of slow rows
-        u64 sums[THREADS == kRow ? kRow : 1];     // of chunks
+        struct {  // a list in the order of the indices
+            uint32_t key[kList];
+            uint32_t j[kList];  // kLow: the weight is below min_p
+            u64 steps[kList + 1];
+        };
+        u64 hist[kDigits];  // amounts of bins or digits
     };
     // Amounts and numbers of the parts of a range, three in turn: a level
     // clears the next one's and has one barrier.
@@ -276,52 +261,43 @@ struct RowShared {
     u64 wave[W], wave_n[W], wave_kept[W];
     double wave_f[W];
     float wave_top[W];
-    uint32_t wave_low[W];
-    int32_t wave_flags[W];
+    uint32_t wave_low[W], wave_high[W];
+    int32_t wave_flags[W], room[kQuads * W];
     u64 above;
     double base;
     int32_t digit, at, last;
-    int32_t offsets[kRow + 1];
+    uint16_t offsets[kMaxChunks + 1];  // of the chunks' lists in this one
 };
+static_assert(sizeof(RowShared) <= 65536 && kBins <= kDigits, "LDS");
+constexpr uint32_t kLow = 1u << 31;
 
 // --------------------------------------- a border among listed elements
-// Elements of a list in the order of the indices, each thread's own ones
-// consecutive: thread t holds those from per * t on.
-template <int THREADS>
-struct Listed {
-    static constexpr int PER = kList / THREADS;
-    uint32_t key[PER];
-    int32_t j[PER];
-    u64 steps[PER];
-    uint32_t in, over;  // bits: eligible; weight of at least min_p
-    int per;
-};
-
-// Border of the first `want` (elements, or steps) of the eligible ones in
-// falling order; want <= their sum, their keys in [lo, hi].  A level cuts the
-// range into 512 parts; every wave finds the part with the border by itself.
-// *turn: which of the three parts' counts the next level uses, 0 at first, with
-// amount[0] and number[0] cleared.
-template <int THREADS, bool MASS>
-__device__ Border border_of(RowShared<THREADS> &sh, int *turn, const Listed<THREADS> &l, u64 want, uint32_t lo, uint32_t hi) {
-    constexpr int PER = Listed<THREADS>::PER, each = kLevel / 64;
+// Border of the first `want` (elements, or steps) of those of the n listed
+// elements that `from` keeps, in falling order; want <= their sum, their keys
+// in [lo, hi].  A level cuts the range into 512 parts; every wave finds the
+// part with the border by itself.  *turn: which of the three parts' counts the
+// next level uses, 0 at first, with amount[0] and number[0] cleared.
+template <bool MASS>
+__device__ Border border_of(RowShared &sh, int *turn, int n, Border from, u64 want, uint32_t lo, uint32_t hi) {
+    constexpr int each = kLevel / 64;
     const int tid = threadIdx.x, lane = tid & 63;
     u64 above = 0;
     for (;;) {
         const int bits = hi > lo ? 32 - __clz(hi - lo) : 0, low = bits > 9 ? bits - 9 : 0;
         const int now = *turn, next = now == 2 ? 0 : now + 1;
         *turn = next;
-        for (int i = tid; i < kLevel; i += THREADS) {
+        for (int i = tid; i < kLevel; i += kThreads) {
             sh.number[next][i] = 0;
             sh.amount[next][i] = 0;
         }
-#pragma unroll
-        for (int i = 0; i < PER; i++)
-            if (i < l.per && (l.in >> i & 1) && l.key[i] >= lo && l.key[i] <= hi) {
-                const int d = (l.key[i] - lo) >> low;
+        for (int i = tid; i < n; i += kThreads) {
+            const uint32_t k = sh.key[i];
+            if (k >= lo && k <= hi && from.keeps(k, static_cast<int>(sh.j[i] & ~kLow))) {
+                const int d = (k - lo) >> low;
                 atomicAdd(&sh.number[now][d], 1u);
-                if (MASS) atomicAdd(&sh.amount[now][d], l.steps[i]);
+                if (MASS) atomicAdd(&sh.amount[now][d], sh.steps[i]);
             }
+        }
         __syncthreads();
         // lane i: the parts from the (8 i)-th highest on
         u64 h[each], sum = 0;
@@ -357,13 +333,14 @@ __device__ Border border_of(RowShared<THREADS> &sh, int *turn, const Listed<THRE
         const u64 one = of / number, need = (want - above + one - 1) / one;
         if (need >= number) return Border{lo, INT32_MAX};
         // the first `need` of the equal ones
+        const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
         u64 mine = 0, all;
-#pragma unroll
-        for (int i = 0; i < PER; i++) mine += (l.in >> i & 1) && l.key[i] == lo;
-        u64 upto = block_scan<THREADS>(sh.wave, mine, &all);
-#pragma unroll
-        for (int i = 0; i < PER; i++)
-            if ((l.in >> i & 1) && l.key[i] == lo && ++upto == need) sh.at = l.j[i] + 1;
+        for (int i = i0; i < i1; i++) mine += sh.key[i] == lo && from.keeps(lo, static_cast<int>(sh.j[i] & ~kLow));
+        u64 upto = block_scan(sh.wave, mine, &all);
+        for (int i = i0; i < i1; i++) {
+            const int j = static_cast<int>(sh.j[i] & ~kLow);
+            if (sh.key[i] == lo && from.keeps(lo, j) && ++upto == need) sh.at = j + 1;
+        }
         __syncthreads();
         const int cut = sh.at;
         __syncthreads();
@@ -375,18 +352,71 @@ __device__ Border border_of(RowShared<THREADS> &sh, int *turn, const Listed<THRE
 __device__ __forceinline__ Border both(Border a, Border b) {
     return b.key > a.key ? b : Border{a.key, b.key == a.key ? min(a.cut, b.cut) : a.cut};
 }
-template <int THREADS>
-__device__ __forceinline__ void cut_to(Listed<THREADS> &l, Border b) {
+
+// --------------------------------------------------------- a row's chunks
+// Values of a chunk as a thread holds them: quad i is the chunk's (i kThreads +
+// thread)-th.  Every quad is one load, those at the row's end from its last
+// four values; settle() then moves these to their places and puts -inf past
+// the end (apart from the load: where the two meet, the loads are waited for).
+struct Held {
+    float z[kQuads][4];
+    __device__ __forceinline__ void load(const SampleArgs &a, const float *row, int c) {
 #pragma unroll
-    for (int i = 0; i < Listed<THREADS>::PER; i++)
-        if (!b.keeps(l.key[i], l.j[i])) l.in &= ~(1u << i);
+        for (int i = 0; i < kQuads; i++) {
+            const uint32_t j = min(c * kChunk + (i * kThreads + static_cast<int>(threadIdx.x)) * 4, a.V - 4);
+            const f4u v = *(const SV_GLOBAL f4u *)(reinterpret_cast<const uint8_t *>(row) + j * 4);
+#pragma unroll
+            for (int e = 0; e < 4; e++) z[i][e] = v[e];
+        }
+    }
+    __device__ __forceinline__ void settle(const SampleArgs &a, int c) {
+        if ((c + 1) * kChunk <= a.V) return;
+#pragma unroll
+        for (int i = 0; i < kQuads; i++) {
+            const int left = a.V - (c * kChunk + (i * kThreads + static_cast<int>(threadIdx.x)) * 4);  // of the row
+            const int by = 4 - min(max(left, 0), 4);
+            const float v[4] = {z[i][0], z[i][1], z[i][2], z[i][3]};
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float x = -INFINITY;
+#pragma unroll
+                for (int k = e; k < 4; k++) x = k - e == by ? v[k] : x;
+                z[i][e] = x;
+            }
+        }
+    }
+};
+// Places of a chunk's chosen elements in a list in the order of the indices.
+// masks[i][e]: the wave's lanes whose element e of quad i is chosen; room: 32
+// numbers; at[i]: the place of the lane's first one of quad i.  Returns how
+// many there are; its barrier comes after every wave's work before the call.
+typedef u64 Masks[kQuads][4];
+__device__ __forceinline__ int places_of(const Masks &masks, int *room, int (&at)[kQuads]) {
+    static_assert(kQuads * W <= 64, "a lane for each number");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+    for (int i = 0; i < kQuads; i++) {
+        const int number = __popcll(masks[i][0]) + __popcll(masks[i][1]) + __popcll(masks[i][2]) + __popcll(masks[i][3]);
+        if (lane == i) room[i * W + wave] = number;
+    }
+    __syncthreads();
+    const int own = lane < kQuads * W ? room[lane] : 0, upto = wave_scan(own);
+#pragma unroll
+    for (int i = 0; i < kQuads; i++) {
+        at[i] = lane_of(upto - own, i * W + wave);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            at[i] += __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(masks[i][e] >> 32),
+                                               __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(masks[i][e]), 0));
+    }
+    return lane_of(upto, 63);
 }
 
 // -------------------------------------- a border from the row, bit by bit
 // Moves the border so that the first `want` (of falling order) of what it
 // keeps remain: of `want` elements, or of steps of weight.
 template <bool MASS>
-__device__ void select(const SampleArgs &a, RowShared<kRow> &sh, const float *row, float top, double per, u64 want,
+__device__ void select(const SampleArgs &a, RowShared &sh, const float *row, float top, double per, u64 want,
                        Border *border) {
     const int tid = threadIdx.x;
     const Border from = *border;
@@ -395,9 +425,9 @@ __device__ void select(const SampleArgs &a, RowShared<kRow> &sh, const float *ro
     for (int level = 0; level < 3; level++) {
         const int low = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
         __syncthreads();
-        for (int i = tid; i < kDigits; i += kRow) sh.hist[i] = 0;
+        for (int i = tid; i < kDigits; i += kThreads) sh.hist[i] = 0;
         __syncthreads();
-        for (int j = tid; j < a.V; j += kRow) {
+        for (int j = tid; j < a.V; j += kThreads) {
             const float z = gld(row + j);
             const uint32_t k = float_key(z);
             if ((k & known) != prefix || !from.keeps(k, j)) continue;
@@ -405,17 +435,22 @@ __device__ void select(const SampleArgs &a, RowShared<kRow> &sh, const float *ro
             atomicAdd(&sh.hist[(k >> low) & ((1u << bits) - 1)], n);
         }
         __syncthreads();
-        // digits in falling order, two a thread
-        const int d1 = kDigits - 1 - 2 * tid, d0 = d1 - 1;
-        const u64 h1 = sh.hist[d1], h0 = sh.hist[d0];
-        u64 all;
-        const u64 before = above + block_scan<kRow>(sh.wave, h1 + h0, &all);
-        if (before < want && before + h1 >= want) {
-            sh.digit = d1;
-            sh.above = before;
-        } else if (before + h1 < want && before + h1 + h0 >= want) {
-            sh.digit = d0;
-            sh.above = before + h1;
+        // digits in falling order
+        constexpr int each = kDigits / kThreads;
+        u64 h[each], sum = 0, all;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            h[i] = sh.hist[kDigits - 1 - each * tid - i];
+            sum += h[i];
+        }
+        u64 before = above + block_scan(sh.wave, sum, &all);
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            if (before < want && before + h[i] >= want) {
+                sh.digit = kDigits - 1 - each * tid - i;
+                sh.above = before;
+            }
+            before += h[i];
         }
         __syncthreads();
         prefix |= static_cast<uint32_t>(sh.digit) << low;
@@ -427,7 +462,7 @@ __device__ void select(const SampleArgs &a, RowShared<kRow> &sh, const float *ro
     const u64 need = (want - above + each - 1) / each;
     u64 passed = 0;
     int cut = a.V;
-    for (int j0 = 0; j0 < a.V; j0 += kRow) {
+    for (int j0 = 0; j0 < a.V; j0 += kThreads) {
         const int j = j0 + tid;
         bool is = false;
         if (j < a.V) {
@@ -435,7 +470,7 @@ __device__ void select(const SampleArgs &a, RowShared<kRow> &sh, const float *ro
             is = k == prefix && from.keeps(k, j);
         }
         u64 all;
-        const u64 before = passed + block_scan<kRow>(sh.wave, static_cast<u64>(is), &all);
+        const u64 before = passed + block_scan(sh.wave, static_cast<u64>(is), &all);
         if (is && before + 1 == need) sh.at = j + 1;
         passed += all;
         if (passed >= need) {
@@ -454,45 +489,46 @@ __device__ __forceinline__ u64 threshold(double u, u64 total) {
     const u64 t = static_cast<u64>(u * static_cast<double>(total));
     return t < total ? t : total - 1;
 }
-// The first element of [j0, j1) at which the running sum of kept weights,
-// `passed` before them, exceeds `past`.
-__device__ int token_in(const SampleArgs &a, RowShared<kRow> &sh, const float *row, int j0, int j1, u64 passed, u64 past,
-                        Border border, float top, const Settings &s) {
-    const int tid = threadIdx.x;
-    for (; j0 < j1; j0 += kRow) {
-        const int j = j0 + tid;
-        u64 n = 0, all;
-        if (j < j1) {
-            const float z = gld(row + j);
-            const double w = weight_of(z, top, s.per);
-            if (border.keeps(float_key(z), j) && w >= s.least) n = steps_of(w, a.shift);
-        }
-        const u64 before = passed + block_scan<kRow>(sh.wave, n, &all);
-        if (before <= past && before + n > past) sh.at = j;
-        passed += all;
-        if (passed > past) break;
+// Steps of a thread's consecutive elements of a chunk, kept ones alone.
+__device__ __forceinline__ u64 kept_steps(const SampleArgs &a, const float *row, int c, Border border, float top, const Settings &s,
+                                          u64 (&steps)[kEach]) {
+    const int j0 = c * kChunk + threadIdx.x * kEach;
+    u64 sum = 0;
+#pragma unroll 4
+    for (int i = 0; i < kEach; i++) {
+        const float z = gld(row + min(j0 + i, a.V - 1));
+        const double w = weight_of(z, top, s.per);
+        steps[i] = j0 + i < a.V && border.keeps(float_key(z), j0 + i) && w >= s.least ? steps_of(w, a.shift) : 0;
+        sum += steps[i];
     }
+    return sum;
+}
+// The first element of chunk c at which the running sum of kept weights,
+// `passed` before the chunk, exceeds `past`; -1 if none does, *passed moved.
+__device__ int token_in(const SampleArgs &a, RowShared &sh, const float *row, int c, u64 *passed, u64 past, Border border,
+                        float top, const Settings &s) {
+    u64 steps[kEach], all;
+    const u64 sum = kept_steps(a, row, c, border, top, s, steps);
+    u64 run = *passed + block_scan(sh.wave, sum, &all);
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        if (run <= past && run + steps[i] > past) sh.at = c * kChunk + static_cast<int>(threadIdx.x) * kEach + i;
+        run += steps[i];
+    }
+    *passed += all;
+    if (*passed <= past) return -1;
     __syncthreads();
     return sh.at;
 }
 
-__device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale) {
-    if (threadIdx.x) return;
-    RowState st{};
-    st.kind = kDone;
-    st.top = top;
-    st.key = border.key;
-    st.cut = border.cut;
-    st.scale = scale;
-    a.state[r] = st;
-}
 __device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale, int token) {
-    done(a, r, border, top, scale);
-    if (threadIdx.x == 0 && a.tokens) gst(a.tokens + r, token);
+    if (threadIdx.x) return;
+    a.state[r] = RowState{0, top, border.key, border.cut, scale};
+    if (a.tokens) gst(a.tokens + r, token);
 }
 __device__ __forceinline__ void failed(const SampleArgs &a, int r) {
     if (threadIdx.x) return;
-    a.state[r].kind = kFailed;
+    a.state[r].failed = 1;
     if (a.tokens) gst(a.tokens + r, -1);
 }
 __device__ __forceinline__ double number_of(const SampleArgs &a, int r) {
@@ -501,23 +537,23 @@ __device__ __forceinline__ double number_of(const SampleArgs &a, int r) {
 }
 
 // A whole row by one workgroup: any case.
-__device__ void slow_row(const SampleArgs &a, RowShared<kRow> &sh, int r, float top, const Settings &s) {
+__device__ void slow_row(const SampleArgs &a, RowShared &sh, int r, float top, const Settings &s) {
     const float *row = row_of(a, r);
     const int tid = threadIdx.x;
     u64 n = 0, finite;
-    for (int j = tid; j < a.V; j += kRow) n += gld(row + j) > -INFINITY;
-    block_scan<kRow>(sh.wave, n, &finite);
+    for (int j = tid; j < a.V; j += kThreads) n += gld(row + j) > -INFINITY;
+    block_scan(sh.wave, n, &finite);
     Border border = no_border();
     if (static_cast<u64>(s.k) < finite) select<false>(a, sh, row, top, s.per, static_cast<u64>(s.k), &border);
     auto sum_kept = [&](double least) {
         u64 sum = 0, all;
-        for (int j = tid; j < a.V; j += kRow) {
+        for (int j = tid; j < a.V; j += kThreads) {
             const float z = gld(row + j);
             if (!border.keeps(float_key(z), j)) continue;
             const double w = weight_of(z, top, s.per);
             if (w >= least) sum += steps_of(w, a.shift);
         }
-        block_scan<kRow>(sh.wave, sum, &all);
+        block_scan(sh.wave, sum, &all);
         return all;
     };
     if (s.p < 1.0) {
@@ -527,86 +563,27 @@ __device__ void slow_row(const SampleArgs &a, RowShared<kRow> &sh, int r, float 
     }
     const u64 total = sum_kept(s.least);
     const double u = number_of(a, r);
-    const int token = u >= 0.0 ? token_in(a, sh, row, 0, a.V, 0, threshold(u, total), border, top, s) : -1;
+    int token = -1;
+    u64 passed = 0;
+    if (u >= 0.0)
+        for (int c = 0; token < 0 && c < a.chunks; c++) token = token_in(a, sh, row, c, &passed, threshold(u, total), border, top, s);
     done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(total), token);
 }
 
 // ------------------------------------------------------------------ scan
-// Values of a chunk as a thread holds them: quad i is the chunk's (i kScan +
-// thread)-th.  Past the row's end: -inf.
-struct Held {
-    float z[kQuads][4];
-    __device__ Held(const SampleArgs &a, const float *row, int c) {
-        if ((c + 1) * kChunk <= a.V) {
-#pragma unroll
-            for (int i = 0; i < kQuads; i++) {
-                const f4u v = *(const SV_GLOBAL f4u *)(row + c * kChunk + (i * kScan + threadIdx.x) * 4);
-#pragma unroll
-                for (int e = 0; e < 4; e++) z[i][e] = v[e];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < kQuads; i++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int j = c * kChunk + (i * kScan + threadIdx.x) * 4 + e;
-                    const float v = gld(row + min(j, a.V - 1));
-                    z[i][e] = j < a.V ? v : -INFINITY;
-                }
-        }
-    }
-};
-// The chosen elements of a chunk, listed in the order of their indices.
-// masks[i][e]: the wave's lanes whose element e of quad i is chosen; room: 64
-// numbers.  Returns how many there are; its barrier comes after every wave's
-// work before the call.
-typedef u64 Masks[kQuads][4];
-__device__ __forceinline__ int list_out(const SampleArgs &a, int slot, int c, const Held &h, const Masks &masks, int *room) {
-    static_assert(kQuads * (kScan / 64) == 64, "a number for each lane");
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    int number[kQuads];
-#pragma unroll
-    for (int i = 0; i < kQuads; i++)
-        number[i] = __popcll(masks[i][0]) + __popcll(masks[i][1]) + __popcll(masks[i][2]) + __popcll(masks[i][3]);
-#pragma unroll
-    for (int i = 0; i < kQuads; i++)
-        if (lane == i) room[i * (kScan / 64) + wave] = number[i];
-    __syncthreads();
-    const int own = room[lane], upto = wave_scan(own), all = lane_of(upto, 63);
-    uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
-#pragma unroll
-    for (int i = 0; i < kQuads; i++) {
-        if (!number[i]) continue;
-        const int nth = i * (kScan / 64) + wave;
-        int at = lane_of(upto - own, nth);
-#pragma unroll
-        for (int e = 0; e < 4; e++)
-            at += __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(masks[i][e] >> 32),
-                                            __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(masks[i][e]), 0));
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            if (masks[i][e] >> lane & 1) {
-                if (at < a.cap) list[at] = make_uint2(__float_as_uint(h.z[i][e]), c * kChunk + (i * kScan + threadIdx.x) * 4 + e);
-                at++;
-            }
-        }
-    }
-    return all;
-}
-
 // Elements that the list should have: a thousand, or 2.5 times what a top-k
 // asks for (the threshold lets pass within 20 % or so of what it should).
-__device__ __forceinline__ int list_target(const Settings &s, int V) { return s.k < V ? min(2600, 2 * s.k + s.k / 2 + 200) : 1024; }
+__device__ __forceinline__ int list_target(const Settings &s, int V) { return s.k < V ? min(1600, 2 * s.k + s.k / 2 + 200) : 1024; }
 
-// A workgroup takes `group` chunks one after the other, the next one's values
-// on their way.
-__global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
-    __shared__ float s_sample[kScan / 64][64];
+// A workgroup takes `group` chunks one after the other; four of them share a
+// compute unit, and one's loads pass while the others compute.
+__global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) {
+    __shared__ float s_sample[W][64];
     __shared__ float s_tau, s_ref;
-    __shared__ int s_room[2][64];
-    __shared__ double s_sum[2][kScan / 64];
-    __shared__ float s_top[2][kScan / 64];
-    __shared__ int s_rest[2][kScan / 64];
+    __shared__ int s_room[2][kQuads * (W)];
+    __shared__ double s_sum[2][W];
+    __shared__ float s_top[2][W];
+    __shared__ int s_rest[2][W];
     const int slot = blockIdx.y, r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63;
     const int c0 = blockIdx.x * a.group, c1 = min(c0 + a.group, a.chunks);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -619,12 +596,12 @@ __global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-        const int at = wave + i * (kScan / 64);  // past the last place: the first again
+        const int at = wave + i * (W);  // past the last place: the first again
         v[i] = gld(row + (static_cast<int64_t>(at < of ? at : 0) * (a.V - 64) >> few) + lane);
     }
-    Held next(a, row, c0);
+    Held h;
+    h.load(a, row, c0);
     const Settings s = settings_of(a, r);
-    if (blockIdx.x == 0 && slot == 0 && tid == 0) a.flat[0] = 0;
     float most = v[0];
 #pragma unroll
     for (int i = 1; i < 8; i++) most = fmaxf(most, v[i]);
@@ -632,7 +609,7 @@ __global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
     __syncthreads();
     if (wave == 0) {
 #pragma unroll
-        for (int w = 1; w < kScan / 64; w++) most = fmaxf(most, s_sample[w][lane]);
+        for (int w = 1; w < W; w++) most = fmaxf(most, s_sample[w][lane]);
         if (!(most > -INFINITY)) most = -INFINITY;  // NaN: the row fails
         const float part = fminf(static_cast<float>(list_target(s, a.V)) / static_cast<float>(a.V), 0.999f);
         const float none = __builtin_amdgcn_exp2f(__builtin_amdgcn_logf(1.0f - part) * static_cast<float>(of));
@@ -654,8 +631,8 @@ __global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
     // ---- the chunks
     for (int c = c0; c < c1; c++) {
         const int now = c & 1;
-        const Held h = next;
-        if (c + 1 < c1) next = Held(a, row, c + 1);
+        if (c > c0) h.load(a, row, c);
+        h.settle(a, c);
         float top = h.z[0][0];
 #pragma unroll
         for (int i = 0; i < kQuads; i++) {
@@ -695,13 +672,26 @@ __global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
             s_top[now][wave] = top;
             s_rest[now][wave] = some;
         }
-        const int n = list_out(a, slot, c, h, masks, s_room[now]);
+        int at[kQuads];
+        const int n = places_of(masks, s_room[now], at);
+        uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
+#pragma unroll
+        for (int i = 0; i < kQuads; i++) {
+            if (!(masks[i][0] | masks[i][1] | masks[i][2] | masks[i][3])) continue;
+            const int j = c * kChunk + (i * kThreads + fresh(tid)) * 4;
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (h.z[i][e] >= from) {
+                    if (at[i] < a.cap) list[at[i]] = make_uint2(__float_as_uint(h.z[i][e]), j + e);
+                    at[i]++;
+                }
+        }
         if (tid == 0) {
             ChunkRec rec{};
             rec.top = s_top[now][0];
             rec.sum = s_sum[now][0];
             rec.rest = s_rest[now][0];
-            for (int w = 1; w < kScan / 64; w++) {
+            for (int w = 1; w < W; w++) {
                 rec.top = most_of(rec.top, s_top[now][w]);
                 rec.sum += s_sum[now][w];
                 rec.rest |= s_rest[now][w];
@@ -715,60 +705,46 @@ __global__ __launch_bounds__(kScan) void sample_scan_kernel(SampleArgs a) {
 }
 
 // ---------------------------------------------------------------- finish
+// An element into a row's list.
+__device__ __forceinline__ void enlist(const SampleArgs &a, RowShared &sh, int at, float z, int j, float top, const Settings &s) {
+    const double w = weight_of(z, top, s.per);
+    sh.key[at] = float_key(z);
+    sh.steps[at] = steps_of(w, a.shift);
+    sh.j[at] = static_cast<uint32_t>(j) | (w >= s.least ? 0u : kLow);
+}
 // The chunks' lists one behind the other (sh.offsets says where each begins, a
-// barrier behind), n elements in all.
-template <int THREADS>
-__device__ __forceinline__ void take_lists(const SampleArgs &a, const RowShared<THREADS> &sh, int slot, int n, float top,
-                                           const Settings &s, Listed<THREADS> *l) {
-    l->per = (n + THREADS - 1) / THREADS;
-    l->in = l->over = 0;
-    int q = threadIdx.x * l->per, c = 0;
-    if (q < n) {  // the last chunk that begins at q or before
-        int to = a.chunks;
-        while (to - c > 1) {
-            const int mid = (c + to) >> 1;
-            if (sh.offsets[mid] <= q) c = mid;
-            else to = mid;
-        }
-    }
-    uint2 v[Listed<THREADS>::PER];
+// barrier behind); a barrier ahead of their use.  Each chunk has as many
+// threads, four of whose loads are on their way together.
+__device__ __forceinline__ void take_lists(const SampleArgs &a, RowShared &sh, int slot, float top, const Settings &s) {
+    int by = 6;
+    while (by > 0 && a.chunks << by > kThreads) by--;
+    const int of = 1 << by, first = threadIdx.x >> by, lane = threadIdx.x & (of - 1);
+    for (int c = first; c < a.chunks; c += kThreads >> by) {
+        const int begin = sh.offsets[c], n = sh.offsets[c + 1] - begin;
+        const uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
+        for (int i0 = lane; i0 < n; i0 += 4 * of) {
+            uint2 v[4];
 #pragma unroll
-    for (int i = 0; i < Listed<THREADS>::PER; i++) {
-        v[i] = make_uint2(0xFF800000u, 0);
-        if (i < l->per && q < n) {
-            while (sh.offsets[c + 1] <= q) c++;
-            v[i] = gld8(a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap + (q - sh.offsets[c]));
-            l->in |= 1u << i;
-            q++;
-        }
-    }
+            for (int k = 0; k < 4; k++) v[k] = gld8(list + min(i0 + k * of, n - 1));
 #pragma unroll
-    for (int i = 0; i < Listed<THREADS>::PER; i++) {
-        const float z = __uint_as_float(v[i].x);
-        l->j[i] = static_cast<int32_t>(v[i].y);
-        l->key[i] = float_key(z);
-        l->steps[i] = 0;
-        if (i < l->per && (l->in >> i & 1)) {
-            const double w = weight_of(z, top, s.per);
-            l->steps[i] = steps_of(w, a.shift);
-            l->over |= static_cast<uint32_t>(w >= s.least) << i;
+            for (int k = 0; k < 4; k++)
+                if (i0 + k * of < n)
+                    enlist(a, sh, begin + i0 + k * of, __uint_as_float(v[k].x), static_cast<int>(v[k].y), top, s);
         }
     }
 }
-template <int THREADS>
-__device__ __forceinline__ u64 steps_in(const Listed<THREADS> &l, uint32_t which) {
-    u64 n = 0;
-#pragma unroll
-    for (int i = 0; i < Listed<THREADS>::PER; i++) n += which >> i & 1 ? l.steps[i] : 0;
-    return n;
+// What of a list a border and min-p keep: steps of an element.
+__device__ __forceinline__ u64 kept_of(const RowShared &sh, int i, Border border) {
+    const uint32_t j = sh.j[i];
+    return j < kLow && border.keeps(sh.key[i], static_cast<int>(j)) ? sh.steps[i] : 0;
 }
 
 // The token of a row without filters: of the chunks' sums the one that the
 // number falls into, and in it the element.  A thread's chunks are [c0, c1),
 // their sum `own` and that of those before them `before`.
-__device__ int token_unfiltered(const SampleArgs &a, RowShared<kFinish> &sh, int slot, const float *row, int c0, int c1,
+__device__ int token_unfiltered(const SampleArgs &a, RowShared &sh, int slot, const float *row, int c0, int c1,
                                 double own, double before, double past, float ref, double per) {
-    constexpr int each = kChunk / kFinish;
+    constexpr int each = kEach;
     const int tid = threadIdx.x;
     __syncthreads();
     if (tid == 0) {
@@ -812,7 +788,7 @@ __device__ int token_unfiltered(const SampleArgs &a, RowShared<kFinish> &sh, int
             mine += j0 + i < a.V ? loose_weight(z, per, less) : 0.0;
         }
     }
-    const double upto = base + block_scan<kFinish>(sh.wave_f, mine, &all);
+    const double upto = base + block_scan(sh.wave_f, mine, &all);
     // the first thread that passes it; if roundings leave none, the last one
     // with a weight
     if (mine > 0.0 && upto + mine > past) atomicMin(&sh.at, tid);
@@ -821,60 +797,236 @@ __device__ int token_unfiltered(const SampleArgs &a, RowShared<kFinish> &sh, int
     const int who = sh.at < INT32_MAX ? sh.at : sh.last;
     if (tid == who) sh.base = upto;
     __syncthreads();
-    // its 64 elements, one a lane
-    static_assert(each == 64, "a lane for each element");
+    // its elements, one a lane
+    static_assert(each <= 64, "a lane for each element");
     const int j = first + who * each + (tid & 63);
-    const double w = j < a.V ? loose_weight(gld(row + j), per, less) : 0.0;
+    const double w = (tid & 63) < each && j < a.V ? loose_weight(gld(row + j), per, less) : 0.0;
     const double run = sh.base + wave_scan(w);
     const u64 over = __ballot(w > 0.0 && run > past), some = __ballot(w > 0.0);
     return first + who * each + (over ? __ffsll(over) - 1 : 63 - __clzll(some));
 }
 
+// A value that a hundredth of a row's weights worth counting lie below: of 64
+// places of the row 64 values each, the least of those at the same offset, and
+// of these 64 the middle one.  Below 2^-64 of the largest nothing counts.
+__device__ float bottom_of(const SampleArgs &a, RowShared &sh, const float *row, float top, double per) {
+    float *least = reinterpret_cast<float *>(sh.hist);  // [waves][64]: the list has been used
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const double from = static_cast<double>(top) - 64.0 / per;
+    float low = INFINITY;
+    for (int i = wave; i < 64; i += kThreads / 64) {
+        const float z = gld(row + (static_cast<int64_t>(i) * (a.V - 64) >> 6) + lane);
+        if (static_cast<double>(z) > from) low = fminf(low, z);
+    }
+    __syncthreads();
+    least[threadIdx.x] = low;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 64; w++) low = fminf(low, least[64 * w + lane]);
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < 64; i++) {
+        const float o = lane_of(low, i);
+        rank += o < low || (o == low && i < lane);
+    }
+    return lane_of(low, __ffsll(__ballot(rank == 32)) - 1);
+}
+
+enum Kind { kWithin, kByCount, kByMass, kNoBorder, kSlow };
+
+// A row whose kept set is not in the list: the first `want` elements or steps,
+// or what min-p leaves.  *turn as for border_of.
+__device__ void flat_row(const SampleArgs &a, RowShared &sh, int r, float top, const Settings &s, Kind kind, u64 want, int *turn) {
+    const float *row = row_of(a, r);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // ---- the border's bin; past all of them if what is wanted is more than there is
+    int bin = kBins;
+    u64 above = 0;
+    float per_bin = 0.0f;
+    if (kind != kNoBorder) {
+        per_bin = static_cast<float>(kBins - 1) / fmaxf(top - bottom_of(a, sh, row, top, s.per), 1e-30f);
+        __syncthreads();
+        for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+        if (tid == 0) {
+            sh.digit = kBins;
+            sh.above = 0;
+        }
+        __syncthreads();
+        for (int c = 0; c < a.chunks; c++) {
+            Held h;
+            h.load(a, row, c);
+            h.settle(a, c);
+#pragma unroll
+            for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float z = h.z[i][e];
+                    if (!(z > -INFINITY)) continue;
+                    const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
+                    atomicAdd(&sh.hist[bin_of(z, top, per_bin)], n);
+                }
+        }
+        __syncthreads();
+        constexpr int each = kBins / kThreads;
+        u64 b[each], sum = 0, all;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            b[i] = sh.hist[tid * each + i];
+            sum += b[i];
+        }
+        u64 before = block_scan(sh.wave, sum, &all);
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            if (before < want && before + b[i] >= want) {
+                sh.digit = tid * each + i;
+                sh.above = before;
+            }
+            before += b[i];
+        }
+        __syncthreads();
+        bin = sh.digit;
+        above = sh.above;
+        __syncthreads();
+    }
+    // ---- its elements listed, what is kept above it summed (the chunks' sums
+    // in the scratch of the row's lists, which are not needed any more)
+    u64 *sums = reinterpret_cast<u64 *>(a.lists + static_cast<int64_t>(r - a.row0) * a.chunks * a.cap);
+    uint32_t low = ~0u, high = 0;
+    int n = 0;
+    for (int c = 0; c < a.chunks; c++) {
+        Held h;
+        h.load(a, row, c);
+        h.settle(a, c);
+        Masks masks;
+        u64 sum = 0;
+#pragma unroll
+        for (int i = 0; i < kQuads; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float z = h.z[i][e];
+                const int b = z > -INFINITY ? bin_of(z, top, per_bin) : kBins + 1;
+                masks[i][e] = __ballot(b == bin);
+                if (b >= bin) continue;
+                const double w = weight_of(z, top, s.per);
+                if (w >= s.least) sum += steps_of(w, a.shift);
+            }
+        sum = wave_sum(sum);
+        __syncthreads();  // the last chunk's numbers have been read
+        if (lane == 0) sh.wave_kept[wave] = sum;
+        if (tid == 0) sh.offsets[c] = static_cast<uint16_t>(n);
+        const int base = n;
+        int at[kQuads];
+        n += places_of(masks, sh.room, at);
+#pragma unroll
+        for (int i = 0; i < kQuads; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float z = h.z[i][e];
+                if (!(z > -INFINITY) || bin_of(z, top, per_bin) != bin) continue;
+                if (base + at[i] < kList) {
+                    enlist(a, sh, base + at[i], z, c * kChunk + (i * kThreads + tid) * 4 + e, top, s);
+                    low = min(low, float_key(z));
+                    high = max(high, float_key(z));
+                }
+                at[i]++;
+            }
+        if (n > kList) break;
+        if (tid == 0) {
+            sum = 0;
+            for (int w = 0; w < W; w++) sum += sh.wave_kept[w];
+            sums[c] = sum;
+        }
+    }
+    __syncthreads();
+    if (n > kList) {
+        slow_row(a, sh, r, top, s);
+        return;
+    }
+    if (tid == 0) sh.offsets[a.chunks] = static_cast<uint16_t>(n);
+    low = wave_least(low);
+    high = ~wave_least(~high);
+    if (lane == 0) {
+        sh.wave_low[wave] = low;
+        sh.wave_high[wave] = high;
+    }
+    __syncthreads();
+    for (int w = 0; w < W; w++) {
+        low = min(low, sh.wave_low[w]);
+        high = max(high, sh.wave_high[w]);
+    }
+    Border border = no_border();
+    if (bin < kBins)
+        border = kind == kByCount ? border_of<false>(sh, turn, n, border, want - above, low, high)
+                                  : border_of<true>(sh, turn, n, border, want - above, low, high);
+    // ---- the kept steps of the list before each of its elements, in the place of its own
+    const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+    u64 kept = 0, all;
+    for (int i = i0; i < i1; i++) kept += kept_of(sh, i, border);
+    u64 run = block_scan(sh.wave, kept, &all);
+    for (int i = i0; i < i1; i++) {
+        const u64 mass = kept_of(sh, i, border);
+        sh.steps[i] = run;
+        run += mass;
+    }
+    if (tid == 0) sh.steps[n] = all;
+    __syncthreads();
+    // ---- the chunk, and in it the token
+    constexpr int span = kMaxChunks / kThreads;
+    u64 own[span], sum = 0;
+#pragma unroll
+    for (int k = 0; k < span; k++) {
+        const int c = tid * span + k;
+        own[k] = c < a.chunks ? sums[c] + sh.steps[sh.offsets[c + 1]] - sh.steps[sh.offsets[c]] : 0;
+        sum += own[k];
+    }
+    u64 upto = block_scan(sh.wave, sum, &all);
+    const double u = number_of(a, r);
+    int token = -1;
+    if (u >= 0.0) {
+        const u64 past = threshold(u, all);
+#pragma unroll
+        for (int k = 0; k < span; k++) {
+            if (upto <= past && upto + own[k] > past) {
+                sh.digit = tid * span + k;
+                sh.above = upto;
+            }
+            upto += own[k];
+        }
+        __syncthreads();
+        u64 passed = sh.above;
+        token = token_in(a, sh, row, sh.digit, &passed, past, border, top, s);
+    }
+    done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
+}
+
 // WHOLE: the row is its own list.
 template <bool WHOLE>
-__global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
-    __shared__ RowShared<kFinish> sh;
-    constexpr int PER = Listed<kFinish>::PER, W = kFinish / 64;
+__global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
+    __shared__ RowShared sh;
     const int slot = blockIdx.x, r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const float *row = row_of(a, r);
     enum { kBad = 1, kOver = 2, kRest = 4 };
-    int turn = 0;
-    for (int i = tid; i < kLevel; i += kFinish) {
-        sh.number[0][i] = 0;
-        sh.amount[0][i] = 0;
-    }
 
     // ---- what the chunks say, or the row itself
-    Listed<kFinish> l;
-    float z[WHOLE ? PER : 1];
     float top = -INFINITY, ref = 0.0f, tau = INFINITY;
     uint32_t low = ~0u;
     int flags = 0;
     u64 mine = 0;
     double own = 0.0;
-    const int span = WHOLE ? (a.V + kFinish - 1) / kFinish : (a.chunks + kFinish - 1) / kFinish;
-    const int c0 = min(tid * span, a.chunks), c1 = min(c0 + span, a.chunks);
+    const int span = (a.chunks + kThreads - 1) / kThreads, c0 = min(tid * span, a.chunks), c1 = min(c0 + span, a.chunks);
+    const ChunkRec *recs = a.recs + static_cast<int64_t>(slot) * a.chunks;
     if (WHOLE) {
-        l.per = span;
-        l.in = l.over = 0;
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            l.j[i] = tid * span + i;
-            z[i] = i < span && l.j[i] < a.V ? gld(row + l.j[i]) : -INFINITY;
-        }
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            l.key[i] = float_key(z[i]);
-            if (!(z[i] < INFINITY)) flags = kBad;
-            if (z[i] > -INFINITY) {
-                l.in |= 1u << i;
-                low = min(low, l.key[i]);
+        for (int i = tid; i < a.V; i += kThreads) {
+            const float z = gld(row + i);
+            const uint32_t k = float_key(z);
+            if (!(z < INFINITY)) flags = kBad;
+            if (z > -INFINITY) {
+                low = min(low, k);
+                mine++;
             }
-            top = fmaxf(top, z[i]);
+            top = fmaxf(top, z);
+            sh.key[i] = k;
         }
-        mine = __popc(l.in);
     } else {
-        const ChunkRec *recs = a.recs + static_cast<int64_t>(slot) * a.chunks;
         ref = gld(&recs->ref);
         tau = gld(&recs->tau);
         for (int c = c0; c < c1; c++) {
@@ -887,6 +1039,11 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
     }
     const Settings s = settings_of(a, r);
     const double u = number_of(a, r);
+    int turn = 0;
+    for (int i = tid; i < kLevel; i += kThreads) {
+        sh.number[0][i] = 0;
+        sh.amount[0][i] = 0;
+    }
     top = wave_max(top);
     flags = wave_or(flags);
     if (WHOLE) low = wave_least(low);
@@ -902,7 +1059,7 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
         sum_before = upto - own;
     }
     u64 total;
-    const u64 before = scan_once<kFinish>(sh.wave_n, mine, &total);
+    const u64 before = scan_once(sh.wave_n, mine, &total);
 #pragma unroll
     for (int w = 0; w < W; w++) {
         top = fmaxf(top, sh.wave_top[w]);
@@ -919,30 +1076,30 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
         return;
     }
     const bool usable = WHOLE || (!(flags & kOver) && total <= kList);
-    const int n = usable ? static_cast<int>(total) : 0;
     const bool rest = !WHOLE && (!usable || (flags & kRest));
     const bool summed = !WHOLE && sum > 0.0 && (static_cast<double>(top) - static_cast<double>(ref)) * s.per < 900.0;
+    const int finite = usable ? static_cast<int>(total) : 0;  // listed
+    const int n = WHOLE ? a.V : finite;                       // entries; -inf among them are below any border
     if (WHOLE) {
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            l.steps[i] = 0;
-            if (i < span && (l.in >> i & 1)) {
-                const double w = weight_of(z[i], top, s.per);
-                l.steps[i] = steps_of(w, a.shift);
-                l.over |= static_cast<uint32_t>(w >= s.least) << i;
-            }
+        for (int i = tid; i < n; i += kThreads) {
+            const double w = weight_of(value_of(sh.key[i]), top, s.per);
+            sh.steps[i] = steps_of(w, a.shift);
+            sh.j[i] = static_cast<uint32_t>(i) | (w >= s.least ? 0u : kLow);
         }
     } else {
-        int at = static_cast<int>(before);
-        for (int c = c0; c < c1; c++) {
-            sh.offsets[c] = at;
-            at += a.recs[static_cast<int64_t>(slot) * a.chunks + c].n;
+        if (usable) {
+            int at = static_cast<int>(before);
+            for (int c = c0; c < c1; c++) {
+                sh.offsets[c] = static_cast<uint16_t>(at);
+                at += recs[c].n;
+            }
+            if (tid == 0) sh.offsets[a.chunks] = static_cast<uint16_t>(n);
         }
-        if (tid == 0) sh.offsets[a.chunks] = static_cast<int>(total);
         __syncthreads();
-        take_lists(a, sh, slot, n, top, s, &l);
+        if (usable) take_lists(a, sh, slot, top, s);
         low = float_key(fmaxf(tau, -3.402823466e38f));
     }
+    __syncthreads();
     const uint32_t high = float_key(top);
 
     // ---- the border, where it is in the list
@@ -950,12 +1107,11 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
     bool within = !rest;  // what is kept is in the list
     // min-p alone keeps it in the list (weights are monotonic to a step or two of fp64)
     const bool short_of = usable && rest && weight_of(tau, top, s.per) * (1.0 + 1e-12) < s.least;
-    int kind = kDone;
+    Kind kind = kWithin;
     u64 want = 0;
-    if (s.k < n || (s.k == n && rest)) {
-        if (s.k < n) {
-            border = border_of<kFinish, false>(sh, &turn, l, static_cast<u64>(s.k), low, high);
-            cut_to(l, border);
+    if (s.k < finite || (s.k == finite && rest)) {
+        if (s.k < finite) {
+            border = border_of<false>(sh, &turn, n, border, static_cast<u64>(s.k), low, high);
             low = max(low, border.key);
         }
         within = true;
@@ -969,9 +1125,11 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
             within = true;
         }
     }
-    if (kind == kDone && s.p < 1.0) {
-        u64 pool;
-        scan_once<kFinish>(sh.wave, steps_in(l, l.in), &pool);
+    const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+    if (kind == kWithin && s.p < 1.0) {
+        u64 pool = 0;
+        for (int i = i0; i < i1; i++) pool += border.keeps(sh.key[i], static_cast<int>(sh.j[i] & ~kLow)) ? sh.steps[i] : 0;
+        scan_once(sh.wave, pool, &pool);
         if (!within && !summed) {
             kind = kSlow;
         } else {
@@ -980,9 +1138,7 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
             want = goal < 1.0 ? 1 : static_cast<u64>(goal);
             if (within) want = min(want, pool);
             if (want <= pool) {
-                const Border b = border_of<kFinish, true>(sh, &turn, l, want, low, high);
-                border = both(border, b);
-                cut_to(l, border);
+                border = both(border, border_of<true>(sh, &turn, n, border, want, low, high));
                 within = true;
             } else if (short_of) {
                 within = true;
@@ -991,7 +1147,7 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
             }
         }
     }
-    if (kind == kDone && !within) {
+    if (kind == kWithin && !within) {
         if (short_of) {
             within = true;
         } else if (s.least == 0.0 && summed) {
@@ -1002,206 +1158,31 @@ __global__ __launch_bounds__(kFinish) void sample_finish_kernel(SampleArgs a) {
             kind = kNoBorder;
         }
     }
-    if (kind != kDone) {
-        if (tid == 0) {
-            RowState st{};
-            st.kind = kind;
-            st.top = top;
-            st.want = want;
-            a.state[r] = st;
-            a.flat[1 + add_dev(a.flat, 1)] = slot;
-        }
-        for (int i = tid; i < kBins; i += kFinish) a.bins[static_cast<int64_t>(slot) * kBins + i] = 0;
+    if (kind == kSlow) {
+        slow_row(a, sh, r, top, s);
+        return;
+    }
+    if (kind != kWithin) {
+        flat_row(a, sh, r, top, s, kind, want, &turn);
         return;
     }
 
     // ---- the sum and the token
-    const uint32_t keep = l.in & l.over;
-    u64 all, upto = scan_once<kFinish>(sh.wave_kept, steps_in(l, keep), &all);
-    if (u >= 0.0) {
-        const u64 past = threshold(u, all);
-        int token = -1;
-#pragma unroll
-        for (int i = 0; i < PER; i++) {
-            const u64 n = keep >> i & 1 ? l.steps[i] : 0;
-            if (upto <= past && upto + n > past) token = l.j[i];
-            upto += n;
-        }
-        if (token >= 0 && a.tokens) gst(a.tokens + r, token);
-    } else if (tid == 0 && a.tokens) {
-        gst(a.tokens + r, -1);
-    }
-    done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all));
-}
-
-// ------------------------------------------------------------- flat rows
-__global__ __launch_bounds__(kScan) void sample_bins_kernel(SampleArgs a) {
-    __shared__ u64 s_bins[kBins];
-    const int items = gld(a.flat) * a.chunks;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
-        const int kind = gld(&a.state[r].kind);
-        if (kind != kByCount && kind != kByMass) continue;
-        const float top = gld(&a.state[r].top);
-        const Settings s = settings_of(a, r);
-        const Held h(a, row_of(a, r), c);
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += kScan) s_bins[i] = 0;
-        __syncthreads();
-        const float scale = bin_scale(s.per);
-#pragma unroll
-        for (int i = 0; i < kQuads; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float z = h.z[i][e];
-                if (!(z > -INFINITY)) continue;
-                const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
-                atomicAdd(&s_bins[bin_of(z, top, scale)], n);
-            }
-        __syncthreads();
-        u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins;
-        for (int i = threadIdx.x; i < kBins; i += kScan)
-            if (s_bins[i]) add_dev(bins + i, s_bins[i]);
-    }
-}
-
-__global__ __launch_bounds__(kScan) void sample_gather_kernel(SampleArgs a) {
-    __shared__ u64 s_scan[kScan / 64], s_sum[kScan / 64], s_above;
-    __shared__ int s_bin, s_room[64];
-    const int items = gld(a.flat) * a.chunks, tid = threadIdx.x;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
-        const int kind = gld(&a.state[r].kind);
-        if (kind == kSlow) continue;
-        const float top = gld(&a.state[r].top);
-        const u64 want = gld(&a.state[r].want);
-        const Settings s = settings_of(a, r);
-        const Held h(a, row_of(a, r), c);
-        // the border's bin; past all of them if what is wanted is more than there is
-        __syncthreads();
-        if (tid == 0) {
-            s_bin = kBins;
-            s_above = 0;
-        }
-        __syncthreads();
-        if (kind != kNoBorder) {
-            const u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins;
-            const u64 b0 = gld(bins + 2 * tid), b1 = gld(bins + 2 * tid + 1);
-            u64 all;
-            const u64 before = block_scan<kScan>(s_scan, b0 + b1, &all);
-            if (before < want && before + b0 >= want) {
-                s_bin = 2 * tid;
-                s_above = before;
-            } else if (before + b0 < want && before + b0 + b1 >= want) {
-                s_bin = 2 * tid + 1;
-                s_above = before + b0;
-            }
-            __syncthreads();
-        }
-        const int bin = s_bin;
-        const float scale = bin_scale(s.per);
-        Masks masks;
-        u64 sum = 0;
-#pragma unroll
-        for (int i = 0; i < kQuads; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float z = h.z[i][e];
-                const int b = z > -INFINITY ? bin_of(z, top, scale) : kBins + 1;
-                masks[i][e] = __ballot(b == bin);
-                if (b >= bin) continue;
-                const double w = weight_of(z, top, s.per);
-                if (w >= s.least) sum += steps_of(w, a.shift);
-            }
-        sum = wave_sum(sum);
-        if ((tid & 63) == 0) s_sum[tid >> 6] = sum;
-        const int n = list_out(a, slot, c, h, masks, s_room);
-        if (tid == 0) {
-            ChunkRec rec{};
-            rec.n = n;
-            rec.steps = 0;
-            for (int w = 0; w < kScan / 64; w++) rec.steps += s_sum[w];
-            a.recs[static_cast<int64_t>(slot) * a.chunks + c] = rec;
-            if (c == 0) {
-                a.state[r].bin = bin;
-                a.state[r].above = s_above;
-            }
-        }
-    }
-}
-
-__global__ __launch_bounds__(kRow) void sample_settle_kernel(SampleArgs a) {
-    __shared__ RowShared<kRow> sh;
-    const int tid = threadIdx.x;
-    if (static_cast<int>(blockIdx.x) >= gld(a.flat)) return;
-    const int slot = gld(a.flat + 1 + blockIdx.x), r = a.row0 + slot;
-    const RowState st = a.state[r];
-    const Settings s = settings_of(a, r);
-    ChunkRec rec{};
-    if (st.kind != kSlow && tid < a.chunks) rec = a.recs[static_cast<int64_t>(slot) * a.chunks + tid];
-    for (int i = tid; i < kLevel; i += kRow) {
-        sh.number[0][i] = 0;
-        sh.amount[0][i] = 0;
-    }
-    u64 total;
-    // a list that does not hold its chunk's elements counts as too many
-    const u64 before = scan_once<kRow>(sh.wave_n, static_cast<u64>(rec.n > a.cap ? kList + 1 : rec.n), &total);
-    if (st.kind == kSlow || total > kList) {
-        slow_row(a, sh, r, st.top, s);
-        return;
-    }
-    if (tid < a.chunks) sh.offsets[tid] = static_cast<int>(before);
-    if (tid == 0) sh.offsets[a.chunks] = static_cast<int>(total);
-    sh.sums[tid] = 0;
-    __syncthreads();
-    Listed<kRow> l;
-    take_lists(a, sh, slot, static_cast<int>(total), st.top, s, &l);
-    Border border = no_border();
-    if (st.bin < kBins) {
-        uint32_t low = ~0u, high = 0;
-#pragma unroll
-        for (int i = 0; i < Listed<kRow>::PER; i++)
-            if (l.in >> i & 1) {
-                low = min(low, l.key[i]);
-                high = max(high, l.key[i]);
-            }
-        low = wave_least(low);
-        high = ~wave_least(~high);
-        if ((tid & 63) == 0) {
-            sh.wave_low[tid >> 6] = low;
-            sh.wave_flags[tid >> 6] = static_cast<int32_t>(high);
-        }
-        __syncthreads();
-        for (int w = 0; w < kRow / 64; w++) {
-            low = min(low, sh.wave_low[w]);
-            high = max(high, static_cast<uint32_t>(sh.wave_flags[w]));
-        }
-        int turn = 0;
-        border = st.kind == kByCount ? border_of<kRow, false>(sh, &turn, l, st.want - st.above, low, high)
-                                     : border_of<kRow, true>(sh, &turn, l, st.want - st.above, low, high);
-        cut_to(l, border);
-    }
-    // the chunks' kept sums
-#pragma unroll
-    for (int i = 0; i < Listed<kRow>::PER; i++)
-        if (l.in & l.over & 1u << i) atomicAdd(&sh.sums[l.j[i] / kChunk], l.steps[i]);
-    __syncthreads();
-    const u64 own = rec.steps + sh.sums[tid];
-    u64 all;
-    const u64 upto = block_scan<kRow>(sh.wave, own, &all);
-    const double u = number_of(a, r);
+    u64 all, upto = 0;
+    for (int i = i0; i < i1; i++) upto += kept_of(sh, i, border);
+    upto = scan_once(sh.wave_kept, upto, &all);
     int token = -1;
     if (u >= 0.0) {
         const u64 past = threshold(u, all);
-        if (upto <= past && upto + own > past) {
-            sh.digit = tid;
-            sh.above = upto;
+        for (int i = i0; i < i1; i++) {
+            const u64 mass = kept_of(sh, i, border);
+            if (upto <= past && upto + mass > past) sh.at = static_cast<int>(sh.j[i]);
+            upto += mass;
         }
         __syncthreads();
-        const int c = sh.digit;
-        token = token_in(a, sh, row_of(a, r), c * kChunk, min(a.V, (c + 1) * kChunk), sh.above, past, border, st.top, s);
+        token = sh.at;
     }
-    done(a, r, border, st.top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
+    done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
 }
 
 // --------------------------------------------------------------- outputs
@@ -1226,7 +1207,7 @@ __global__ __launch_bounds__(kOut) void sample_out_kernel(SampleArgs a) {
     const RowState st = a.state[r];
     const Settings s = settings_of(a, r);
     const Border border{st.key, st.cut};
-    const float none = st.kind == kFailed ? NAN : 0.0f, dropped = st.kind == kFailed ? NAN : -INFINITY;
+    const float none = st.failed ? NAN : 0.0f, dropped = st.failed ? NAN : -INFINITY;
     const int64_t base = static_cast<int64_t>(r) * a.V;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -1234,7 +1215,7 @@ __global__ __launch_bounds__(kOut) void sample_out_kernel(SampleArgs a) {
         f4u p, k;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            bool keep = st.kind == kDone && z[i][e] > -INFINITY && border.keeps(float_key(z[i][e]), j + e);
+            bool keep = !st.failed && z[i][e] > -INFINITY && border.keeps(float_key(z[i][e]), j + e);
             double w = 0.0;
             if (keep) {
                 w = weight_of(z[i][e], st.top, s.per);
@@ -1267,7 +1248,7 @@ static int check_rows(int64_t rows, int64_t V) {
 struct SamplePlan {
     int chunks, cap, slots;
     bool whole;
-    size_t recs, lists, bins, flat, bytes;
+    size_t recs, lists, bytes;
 };
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 static SamplePlan sample_plan(int64_t rows, int64_t V) {
@@ -1281,9 +1262,7 @@ static SamplePlan sample_plan(int64_t rows, int64_t V) {
     const size_t slots = static_cast<size_t>(p.slots), chunks = static_cast<size_t>(p.chunks);
     p.recs = p.bytes;
     p.lists = p.recs + up256(slots * chunks * sizeof(ChunkRec));
-    p.bins = p.lists + up256(slots * chunks * static_cast<size_t>(p.cap) * sizeof(uint2));
-    p.flat = p.bins + slots * kBins * sizeof(u64);
-    p.bytes = p.flat + up256((slots + 1) * sizeof(int32_t));
+    p.bytes = p.lists + up256(slots * chunks * static_cast<size_t>(p.cap) * sizeof(uint2));
     return p;
 }
 
@@ -1333,24 +1312,18 @@ extern "C" int sv_sample(const float *logits, int64_t rows, int64_t V, int64_t l
     a.state = reinterpret_cast<RowState *>(ws);
     a.recs = reinterpret_cast<ChunkRec *>(ws + p.recs);
     a.lists = reinterpret_cast<uint2 *>(ws + p.lists);
-    a.bins = reinterpret_cast<u64 *>(ws + p.bins);
-    a.flat = reinterpret_cast<int32_t *>(ws + p.flat);
     hipStream_t st = as_stream(stream);
     for (int64_t row0 = 0; row0 < rows; row0 += p.slots) {
         a.row0 = static_cast<int32_t>(row0);
         a.rows = static_cast<int32_t>(std::min<int64_t>(p.slots, rows - row0));
         const dim3 each(a.rows);
         if (p.whole) {
-            hipLaunchKernelGGL(sample_finish_kernel<true>, each, dim3(kFinish), 0, st, a);
+            hipLaunchKernelGGL(sample_finish_kernel<true>, each, dim3(kThreads), 0, st, a);
         } else {
-            // two workgroups a compute unit, if the rows give that many
-            a.group = std::max(1, a.rows * p.chunks / 512);
-            hipLaunchKernelGGL(sample_scan_kernel, dim3((p.chunks + a.group - 1) / a.group, a.rows), dim3(kScan), 0, st, a);
-            hipLaunchKernelGGL(sample_finish_kernel<false>, each, dim3(kFinish), 0, st, a);
-            const dim3 flat(std::min(kFlatGrid, a.rows * p.chunks));
-            hipLaunchKernelGGL(sample_bins_kernel, flat, dim3(kScan), 0, st, a);
-            hipLaunchKernelGGL(sample_gather_kernel, flat, dim3(kScan), 0, st, a);
-            hipLaunchKernelGGL(sample_settle_kernel, each, dim3(kRow), 0, st, a);
+            // four workgroups a compute unit, if the rows give that many
+            a.group = std::max(1, (a.rows * p.chunks + 1023) / 1024);
+            hipLaunchKernelGGL(sample_scan_kernel, dim3((p.chunks + a.group - 1) / a.group, a.rows), dim3(kThreads), 0, st, a);
+            hipLaunchKernelGGL(sample_finish_kernel<false>, each, dim3(kThreads), 0, st, a);
         }
         if (probs || kept)
             hipLaunchKernelGGL(sample_out_kernel, dim3(static_cast<unsigned>((V + kOutPiece - 1) / kOutPiece), a.rows), dim3(kOut), 0,

@@ -164,6 +164,26 @@ __device__ __forceinline__ int32_t dot4_first(uint32_t a, uint32_t b) {
     return r;
 }
 
+// A value that the compiler takes as new, so that what follows from it is
+// formed where it is used and not kept in registers across a loop.
+__device__ __forceinline__ int fresh(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
+// Division of 0 <= x < 2^31 by a number that the host knows.
+struct Div {
+    uint32_t m, sh;
+    __device__ __forceinline__ int operator()(int x) const {
+        return static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * m >> sh);
+    }
+};
+inline Div div_by(uint32_t d) {
+    uint32_t l = 0;
+    while ((1ull << l) < d) l++;
+    return Div{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
 // Order-preserving map of an fp32 value to uint32 (larger float -> larger
 // key); -0 is first turned into +0 so the two compare equal.
 __device__ __forceinline__ uint32_t float_key(float f) {
