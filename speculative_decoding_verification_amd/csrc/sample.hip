@@ -17,7 +17,7 @@
 // V^2 2^-64 of the row (1e-9 for 151936).  Sums over a whole row that nothing
 // filters are fp64, in the order of its chunks.
 //
-// Two launches, and one pass over the logits for nearly every row:
+// One pass over the logits decides nearly every row:
 //   scan    a workgroup per chunk of a row: a sample of the row gives a
 //           threshold that about a thousand of its values pass; these are
 //           listed in the order of their indices, with the chunk's largest
@@ -28,11 +28,14 @@
 //           without filters takes its token from the chunks' sums and one
 //           chunk.
 // A row whose kept set goes past the list (a flat distribution) is read twice
-// more by its workgroup: amounts (elements, or steps of weight) by the distance
-// from the largest value, which gives the border's bin; then that bin's
-// elements make a list, and the kept weights above it are summed per chunk.
+// more, by the workgroups of two launches that find nothing to do otherwise:
+//   bins    amounts (elements, or steps of weight) by the distance from the
+//           largest value, which gives the border's bin;
+//   gather  that bin's elements are listed and the kept weights above it
+//           summed per chunk; the row's last workgroup settles it.
 // What is left (a top-k past the list with a top-p as well, a bin of more
-// elements than a list holds) is selected on the bits of z, in nine passes.
+// elements than a list holds) is selected on the bits of z by that workgroup,
+// in nine passes.
 #include <algorithm>
 
 #include "sv_internal.h"
@@ -53,6 +56,7 @@ constexpr int kBins = 2048;
 constexpr int kLevel = 512;              // parts that a range of keys is cut into
 constexpr int kDigits = 2048;
 constexpr int kSlots = 256;              // rows that are under way at once
+constexpr int kFlatGrid = 512;           // workgroups of the passes over flat rows
 constexpr int64_t kMaxVocab = 1 << 24;
 constexpr int64_t kMaxRows = 65535;
 
@@ -63,16 +67,24 @@ struct ChunkRec {
     int32_t rest;   // finite elements that are not listed: some, or none
     float tau, ref; // of the row: threshold of the list, the sample's largest value
     int32_t pad;
-    double sum;     // of all weights, relative to ref; < 0: not formed
+    union {
+        double sum;  // of all weights, relative to ref; < 0: not formed
+        u64 steps;   // gather: of the kept weights above the border's bin
+    };
 };
 
-// What the outputs of a row are made of.
+enum Kind { kWithin, kFailed, kByCount, kByMass, kNoBorder, kSlow };
+
+// What the outputs of a row are made of, and what is known of a flat one.
 struct RowState {
-    int32_t failed;
+    int32_t kind;
     float top;
     uint32_t key;    // kept: keys above this one,
     int32_t cut;     // and those equal to it with a smaller index
     double scale;    // weight times this: probability
+    u64 want;        // elements or steps to be kept
+    float per_bin;   // bins to a unit of z, below top
+    int32_t gathered;  // chunks
 };
 
 struct SampleArgs {
@@ -90,7 +102,9 @@ struct SampleArgs {
     float *probs, *kept;
     RowState *state;  // [all rows]
     ChunkRec *recs;   // [slots][chunks]
-    uint2 *lists;     // [slots][chunks][cap]: bits of z, index
+    u64 *lists;       // [slots][chunks][cap]: bits of z, index in the high half
+    u64 *bins;        // [slots][kBins]
+    int32_t *flat;    // number of flat rows, then their slots
 };
 
 __device__ __forceinline__ const float *row_of(const SampleArgs &a, int r) { return a.logits + static_cast<int64_t>(r) * a.ld; }
@@ -157,6 +171,8 @@ __device__ __forceinline__ float value_of(uint32_t key) {
 __device__ __forceinline__ int bin_of(float z, float top, float per_bin) {
     return static_cast<int>(fminf((top - z) * per_bin, static_cast<float>(kBins - 1)));
 }
+
+__device__ __forceinline__ u64 entry_of(float z, int j) { return static_cast<u64>(j) << 32 | __float_as_uint(z); }
 
 struct Border {
     uint32_t key;
@@ -494,7 +510,7 @@ __device__ __forceinline__ u64 kept_steps(const SampleArgs &a, const float *row,
                                           u64 (&steps)[kEach]) {
     const int j0 = c * kChunk + threadIdx.x * kEach;
     u64 sum = 0;
-#pragma unroll 4
+#pragma unroll
     for (int i = 0; i < kEach; i++) {
         const float z = gld(row + min(j0 + i, a.V - 1));
         const double w = weight_of(z, top, s.per);
@@ -523,12 +539,12 @@ __device__ int token_in(const SampleArgs &a, RowShared &sh, const float *row, in
 
 __device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale, int token) {
     if (threadIdx.x) return;
-    a.state[r] = RowState{0, top, border.key, border.cut, scale};
+    a.state[r] = RowState{kWithin, top, border.key, border.cut, scale, 0, 0.0f, 0};
     if (a.tokens) gst(a.tokens + r, token);
 }
 __device__ __forceinline__ void failed(const SampleArgs &a, int r) {
     if (threadIdx.x) return;
-    a.state[r].failed = 1;
+    a.state[r].kind = kFailed;
     if (a.tokens) gst(a.tokens + r, -1);
 }
 __device__ __forceinline__ double number_of(const SampleArgs &a, int r) {
@@ -602,6 +618,7 @@ __global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) 
     Held h;
     h.load(a, row, c0);
     const Settings s = settings_of(a, r);
+    if (blockIdx.x == 0 && slot == 0 && tid == 0) a.flat[0] = 0;
     float most = v[0];
 #pragma unroll
     for (int i = 1; i < 8; i++) most = fmaxf(most, v[i]);
@@ -674,7 +691,7 @@ __global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) 
         }
         int at[kQuads];
         const int n = places_of(masks, s_room[now], at);
-        uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
+        u64 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
 #pragma unroll
         for (int i = 0; i < kQuads; i++) {
             if (!(masks[i][0] | masks[i][1] | masks[i][2] | masks[i][3])) continue;
@@ -682,7 +699,7 @@ __global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) 
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 if (h.z[i][e] >= from) {
-                    if (at[i] < a.cap) list[at[i]] = make_uint2(__float_as_uint(h.z[i][e]), j + e);
+                    if (at[i] < a.cap) list[at[i]] = entry_of(h.z[i][e], j + e);
                     at[i]++;
                 }
         }
@@ -721,15 +738,16 @@ __device__ __forceinline__ void take_lists(const SampleArgs &a, RowShared &sh, i
     const int of = 1 << by, first = threadIdx.x >> by, lane = threadIdx.x & (of - 1);
     for (int c = first; c < a.chunks; c += kThreads >> by) {
         const int begin = sh.offsets[c], n = sh.offsets[c + 1] - begin;
-        const uint2 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
+        const u64 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
         for (int i0 = lane; i0 < n; i0 += 4 * of) {
-            uint2 v[4];
+            u64 v[4];
 #pragma unroll
-            for (int k = 0; k < 4; k++) v[k] = gld8(list + min(i0 + k * of, n - 1));
+            for (int k = 0; k < 4; k++) v[k] = ld_dev(list + min(i0 + k * of, n - 1));
 #pragma unroll
             for (int k = 0; k < 4; k++)
                 if (i0 + k * of < n)
-                    enlist(a, sh, begin + i0 + k * of, __uint_as_float(v[k].x), static_cast<int>(v[k].y), top, s);
+                    enlist(a, sh, begin + i0 + k * of, __uint_as_float(static_cast<uint32_t>(v[k])), static_cast<int>(v[k] >> 32),
+                           top, s);
         }
     }
 }
@@ -829,173 +847,6 @@ __device__ float bottom_of(const SampleArgs &a, RowShared &sh, const float *row,
         rank += o < low || (o == low && i < lane);
     }
     return lane_of(low, __ffsll(__ballot(rank == 32)) - 1);
-}
-
-enum Kind { kWithin, kByCount, kByMass, kNoBorder, kSlow };
-
-// A row whose kept set is not in the list: the first `want` elements or steps,
-// or what min-p leaves.  *turn as for border_of.
-__device__ void flat_row(const SampleArgs &a, RowShared &sh, int r, float top, const Settings &s, Kind kind, u64 want, int *turn) {
-    const float *row = row_of(a, r);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    // ---- the border's bin; past all of them if what is wanted is more than there is
-    int bin = kBins;
-    u64 above = 0;
-    float per_bin = 0.0f;
-    if (kind != kNoBorder) {
-        per_bin = static_cast<float>(kBins - 1) / fmaxf(top - bottom_of(a, sh, row, top, s.per), 1e-30f);
-        __syncthreads();
-        for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
-        if (tid == 0) {
-            sh.digit = kBins;
-            sh.above = 0;
-        }
-        __syncthreads();
-        for (int c = 0; c < a.chunks; c++) {
-            Held h;
-            h.load(a, row, c);
-            h.settle(a, c);
-#pragma unroll
-            for (int i = 0; i < kQuads; i++)
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float z = h.z[i][e];
-                    if (!(z > -INFINITY)) continue;
-                    const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
-                    atomicAdd(&sh.hist[bin_of(z, top, per_bin)], n);
-                }
-        }
-        __syncthreads();
-        constexpr int each = kBins / kThreads;
-        u64 b[each], sum = 0, all;
-#pragma unroll
-        for (int i = 0; i < each; i++) {
-            b[i] = sh.hist[tid * each + i];
-            sum += b[i];
-        }
-        u64 before = block_scan(sh.wave, sum, &all);
-#pragma unroll
-        for (int i = 0; i < each; i++) {
-            if (before < want && before + b[i] >= want) {
-                sh.digit = tid * each + i;
-                sh.above = before;
-            }
-            before += b[i];
-        }
-        __syncthreads();
-        bin = sh.digit;
-        above = sh.above;
-        __syncthreads();
-    }
-    // ---- its elements listed, what is kept above it summed (the chunks' sums
-    // in the scratch of the row's lists, which are not needed any more)
-    u64 *sums = reinterpret_cast<u64 *>(a.lists + static_cast<int64_t>(r - a.row0) * a.chunks * a.cap);
-    uint32_t low = ~0u, high = 0;
-    int n = 0;
-    for (int c = 0; c < a.chunks; c++) {
-        Held h;
-        h.load(a, row, c);
-        h.settle(a, c);
-        Masks masks;
-        u64 sum = 0;
-#pragma unroll
-        for (int i = 0; i < kQuads; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float z = h.z[i][e];
-                const int b = z > -INFINITY ? bin_of(z, top, per_bin) : kBins + 1;
-                masks[i][e] = __ballot(b == bin);
-                if (b >= bin) continue;
-                const double w = weight_of(z, top, s.per);
-                if (w >= s.least) sum += steps_of(w, a.shift);
-            }
-        sum = wave_sum(sum);
-        __syncthreads();  // the last chunk's numbers have been read
-        if (lane == 0) sh.wave_kept[wave] = sum;
-        if (tid == 0) sh.offsets[c] = static_cast<uint16_t>(n);
-        const int base = n;
-        int at[kQuads];
-        n += places_of(masks, sh.room, at);
-#pragma unroll
-        for (int i = 0; i < kQuads; i++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float z = h.z[i][e];
-                if (!(z > -INFINITY) || bin_of(z, top, per_bin) != bin) continue;
-                if (base + at[i] < kList) {
-                    enlist(a, sh, base + at[i], z, c * kChunk + (i * kThreads + tid) * 4 + e, top, s);
-                    low = min(low, float_key(z));
-                    high = max(high, float_key(z));
-                }
-                at[i]++;
-            }
-        if (n > kList) break;
-        if (tid == 0) {
-            sum = 0;
-            for (int w = 0; w < W; w++) sum += sh.wave_kept[w];
-            sums[c] = sum;
-        }
-    }
-    __syncthreads();
-    if (n > kList) {
-        slow_row(a, sh, r, top, s);
-        return;
-    }
-    if (tid == 0) sh.offsets[a.chunks] = static_cast<uint16_t>(n);
-    low = wave_least(low);
-    high = ~wave_least(~high);
-    if (lane == 0) {
-        sh.wave_low[wave] = low;
-        sh.wave_high[wave] = high;
-    }
-    __syncthreads();
-    for (int w = 0; w < W; w++) {
-        low = min(low, sh.wave_low[w]);
-        high = max(high, sh.wave_high[w]);
-    }
-    Border border = no_border();
-    if (bin < kBins)
-        border = kind == kByCount ? border_of<false>(sh, turn, n, border, want - above, low, high)
-                                  : border_of<true>(sh, turn, n, border, want - above, low, high);
-    // ---- the kept steps of the list before each of its elements, in the place of its own
-    const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
-    u64 kept = 0, all;
-    for (int i = i0; i < i1; i++) kept += kept_of(sh, i, border);
-    u64 run = block_scan(sh.wave, kept, &all);
-    for (int i = i0; i < i1; i++) {
-        const u64 mass = kept_of(sh, i, border);
-        sh.steps[i] = run;
-        run += mass;
-    }
-    if (tid == 0) sh.steps[n] = all;
-    __syncthreads();
-    // ---- the chunk, and in it the token
-    constexpr int span = kMaxChunks / kThreads;
-    u64 own[span], sum = 0;
-#pragma unroll
-    for (int k = 0; k < span; k++) {
-        const int c = tid * span + k;
-        own[k] = c < a.chunks ? sums[c] + sh.steps[sh.offsets[c + 1]] - sh.steps[sh.offsets[c]] : 0;
-        sum += own[k];
-    }
-    u64 upto = block_scan(sh.wave, sum, &all);
-    const double u = number_of(a, r);
-    int token = -1;
-    if (u >= 0.0) {
-        const u64 past = threshold(u, all);
-#pragma unroll
-        for (int k = 0; k < span; k++) {
-            if (upto <= past && upto + own[k] > past) {
-                sh.digit = tid * span + k;
-                sh.above = upto;
-            }
-            upto += own[k];
-        }
-        __syncthreads();
-        u64 passed = sh.above;
-        token = token_in(a, sh, row, sh.digit, &passed, past, border, top, s);
-    }
-    done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
 }
 
 // WHOLE: the row is its own list.
@@ -1158,12 +1009,14 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
             kind = kNoBorder;
         }
     }
-    if (kind == kSlow) {
-        slow_row(a, sh, r, top, s);
-        return;
-    }
     if (kind != kWithin) {
-        flat_row(a, sh, r, top, s, kind, want, &turn);
+        const float bottom = kind == kByCount || kind == kByMass ? bottom_of(a, sh, row, top, s.per) : 0.0f;
+        if (tid == 0) {
+            const float per_bin = static_cast<float>(kBins - 1) / fmaxf(top - bottom, 1e-30f);
+            a.state[r] = RowState{kind, top, 0, 0, 0.0, want, per_bin, 0};
+            a.flat[1 + add_dev(a.flat, 1)] = slot;
+        }
+        for (int i = tid; i < kBins; i += kThreads) a.bins[static_cast<int64_t>(slot) * kBins + i] = 0;
         return;
     }
 
@@ -1183,6 +1036,228 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
         token = sh.at;
     }
     done(a, r, border, top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
+}
+
+// ------------------------------------------------------------- flat rows
+__global__ __launch_bounds__(kThreads) void sample_bins_kernel(SampleArgs a) {
+    __shared__ u64 s_bins[kBins];
+    const int items = gld(a.flat) * a.chunks;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
+        const int kind = gld(&a.state[r].kind);
+        if (kind != kByCount && kind != kByMass) continue;
+        Held h;
+        h.load(a, row_of(a, r), c);
+        const float top = gld(&a.state[r].top), per_bin = gld(&a.state[r].per_bin);
+        const Settings s = settings_of(a, r);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBins; i += kThreads) s_bins[i] = 0;
+        __syncthreads();
+        h.settle(a, c);
+#pragma unroll
+        for (int i = 0; i < kQuads; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float z = h.z[i][e];
+                const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
+                if (z > -INFINITY) atomicAdd(&s_bins[bin_of(z, top, per_bin)], n);
+            }
+        __syncthreads();
+        u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins;
+        for (int i = threadIdx.x; i < kBins; i += kThreads)
+            if (s_bins[i]) add_dev(bins + i, s_bins[i]);
+    }
+}
+
+// A flat row whose chunks have all been gathered: `above` amounts lie above
+// the border's bin (kBins: all elements do).
+__device__ void settle_row(const SampleArgs &a, RowShared &sh, int slot, const RowState &st, const Settings &s, int bin, u64 above) {
+    const int r = a.row0 + slot, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const float *row = row_of(a, r);
+    if (st.kind == kSlow) {
+        slow_row(a, sh, r, st.top, s);
+        return;
+    }
+    constexpr int span = kMaxChunks / kThreads;
+    const ChunkRec *recs = a.recs + static_cast<int64_t>(slot) * a.chunks;
+    int of[span];
+    u64 own[span];  // kept steps of the thread's chunks
+    u64 mine = 0, total;
+#pragma unroll
+    for (int k = 0; k < span; k++) {
+        const int c = tid * span + k;
+        of[k] = c < a.chunks ? ld_dev(&recs[c].n) : 0;
+        own[k] = c < a.chunks ? ld_dev(&recs[c].steps) : 0;
+        // a list that does not hold its chunk's elements counts as too many
+        mine += static_cast<u64>(of[k] > a.cap ? kList + 1 : of[k]);
+    }
+    for (int i = tid; i < kLevel; i += kThreads) {
+        sh.number[0][i] = 0;
+        sh.amount[0][i] = 0;
+    }
+    const u64 before = block_scan(sh.wave_n, mine, &total);
+    if (total > kList) {
+        slow_row(a, sh, r, st.top, s);
+        return;
+    }
+    const int n = static_cast<int>(total);
+    int at = static_cast<int>(before);
+#pragma unroll
+    for (int k = 0; k < span; k++) {
+        if (tid * span + k < a.chunks) sh.offsets[tid * span + k] = static_cast<uint16_t>(at);
+        at += of[k];
+    }
+    if (tid == 0) sh.offsets[a.chunks] = static_cast<uint16_t>(n);
+    __syncthreads();
+    take_lists(a, sh, slot, st.top, s);
+    __syncthreads();
+    Border border = no_border();
+    if (bin < kBins) {
+        uint32_t low = ~0u, high = 0;
+        for (int i = tid; i < n; i += kThreads) {
+            low = min(low, sh.key[i]);
+            high = max(high, sh.key[i]);
+        }
+        low = wave_least(low);
+        high = ~wave_least(~high);
+        if (lane == 0) {
+            sh.wave_low[wave] = low;
+            sh.wave_high[wave] = high;
+        }
+        __syncthreads();
+        for (int w = 0; w < W; w++) {
+            low = min(low, sh.wave_low[w]);
+            high = max(high, sh.wave_high[w]);
+        }
+        int turn = 0;
+        border = st.kind == kByCount ? border_of<false>(sh, &turn, n, border, st.want - above, low, high)
+                                     : border_of<true>(sh, &turn, n, border, st.want - above, low, high);
+    }
+    // the kept steps of the list before each of its elements, in the place of its own
+    const int per = (n + kThreads - 1) / kThreads, i0 = min(tid * per, n), i1 = min(i0 + per, n);
+    u64 kept = 0, all;
+    for (int i = i0; i < i1; i++) kept += kept_of(sh, i, border);
+    u64 run = block_scan(sh.wave, kept, &all);
+    for (int i = i0; i < i1; i++) {
+        const u64 mass = kept_of(sh, i, border);
+        sh.steps[i] = run;
+        run += mass;
+    }
+    if (tid == 0) sh.steps[n] = all;
+    __syncthreads();
+    // the chunk, and in it the token
+    u64 sum = 0;
+#pragma unroll
+    for (int k = 0; k < span; k++) {
+        const int c = tid * span + k;
+        if (c < a.chunks) own[k] += sh.steps[sh.offsets[c + 1]] - sh.steps[sh.offsets[c]];
+        sum += own[k];
+    }
+    u64 upto = block_scan(sh.wave, sum, &all);
+    const double u = number_of(a, r);
+    int token = -1;
+    if (u >= 0.0) {
+        const u64 past = threshold(u, all);
+#pragma unroll
+        for (int k = 0; k < span; k++) {
+            if (upto <= past && upto + own[k] > past) {
+                sh.digit = tid * span + k;
+                sh.above = upto;
+            }
+            upto += own[k];
+        }
+        __syncthreads();
+        u64 passed = sh.above;
+        token = token_in(a, sh, row, sh.digit, &passed, past, border, st.top, s);
+    }
+    done(a, r, border, st.top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
+}
+
+__global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a) {
+    __shared__ RowShared sh;
+    __shared__ int s_last;
+    const int items = gld(a.flat) * a.chunks, tid = threadIdx.x;
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
+        const RowState st = a.state[r];
+        const Settings s = settings_of(a, r);
+        Held h;
+        h.load(a, row_of(a, r), c);
+        // the border's bin; past all of them if what is wanted is more than there is
+        __syncthreads();
+        if (tid == 0) {
+            sh.digit = kBins;
+            sh.above = 0;
+        }
+        __syncthreads();
+        if (st.kind == kByCount || st.kind == kByMass) {
+            constexpr int each = kBins / kThreads;
+            const u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins + tid * each;
+            u64 b[each], sum = 0, all;
+#pragma unroll
+            for (int i = 0; i < each; i++) {
+                b[i] = gld(bins + i);
+                sum += b[i];
+            }
+            u64 before = block_scan(sh.wave, sum, &all);
+#pragma unroll
+            for (int i = 0; i < each; i++) {
+                if (before < st.want && before + b[i] >= st.want) {
+                    sh.digit = tid * each + i;
+                    sh.above = before;
+                }
+                before += b[i];
+            }
+            __syncthreads();
+        }
+        const int bin = sh.digit;
+        const u64 above = sh.above;
+        if (st.kind != kSlow) {
+            h.settle(a, c);
+            Masks masks;
+            u64 sum = 0;
+#pragma unroll
+            for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float z = h.z[i][e];
+                    const int b = z > -INFINITY ? bin_of(z, st.top, st.per_bin) : kBins + 1;
+                    masks[i][e] = __ballot(b == bin);
+                    const double w = weight_of(z, st.top, s.per);
+                    if (b < bin && w >= s.least) sum += steps_of(w, a.shift);
+                }
+            sum = wave_sum(sum);
+            if ((tid & 63) == 0) sh.wave_kept[tid >> 6] = sum;
+            int at[kQuads];
+            const int n = places_of(masks, sh.room, at);
+            u64 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
+#pragma unroll
+            for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    if (masks[i][e] >> (tid & 63) & 1) {
+                        if (at[i] < a.cap)
+                            st_dev(list + at[i], entry_of(h.z[i][e], c * kChunk + (i * kThreads + tid) * 4 + e));
+                        at[i]++;
+                    }
+            if (tid == 0) {
+                u64 steps = 0;
+                for (int w = 0; w < W; w++) steps += sh.wave_kept[w];
+                ChunkRec *rec = a.recs + static_cast<int64_t>(slot) * a.chunks + c;
+                st_dev(&rec->n, n);
+                st_dev(&rec->steps, steps);
+            }
+        }
+        // lists and sums have been written through before the count that says
+        // so; who sees the row's last one reads them where all see the same
+        drain();
+        __syncthreads();
+        if (tid == 0) s_last = add_dev(&a.state[r].gathered, 1) == a.chunks - 1;
+        __syncthreads();
+        if (!s_last) continue;
+        settle_row(a, sh, slot, st, s, bin, above);
+        __syncthreads();
+    }
 }
 
 // --------------------------------------------------------------- outputs
@@ -1207,7 +1282,7 @@ __global__ __launch_bounds__(kOut) void sample_out_kernel(SampleArgs a) {
     const RowState st = a.state[r];
     const Settings s = settings_of(a, r);
     const Border border{st.key, st.cut};
-    const float none = st.failed ? NAN : 0.0f, dropped = st.failed ? NAN : -INFINITY;
+    const float none = st.kind == kFailed ? NAN : 0.0f, dropped = st.kind == kFailed ? NAN : -INFINITY;
     const int64_t base = static_cast<int64_t>(r) * a.V;
 #pragma unroll
     for (int i = 0; i < 2; i++) {
@@ -1215,7 +1290,7 @@ __global__ __launch_bounds__(kOut) void sample_out_kernel(SampleArgs a) {
         f4u p, k;
 #pragma unroll
         for (int e = 0; e < 4; e++) {
-            bool keep = !st.failed && z[i][e] > -INFINITY && border.keeps(float_key(z[i][e]), j + e);
+            bool keep = st.kind != kFailed && z[i][e] > -INFINITY && border.keeps(float_key(z[i][e]), j + e);
             double w = 0.0;
             if (keep) {
                 w = weight_of(z[i][e], st.top, s.per);
@@ -1248,7 +1323,7 @@ static int check_rows(int64_t rows, int64_t V) {
 struct SamplePlan {
     int chunks, cap, slots;
     bool whole;
-    size_t recs, lists, bytes;
+    size_t recs, lists, bins, flat, bytes;
 };
 static size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 static SamplePlan sample_plan(int64_t rows, int64_t V) {
@@ -1262,7 +1337,9 @@ static SamplePlan sample_plan(int64_t rows, int64_t V) {
     const size_t slots = static_cast<size_t>(p.slots), chunks = static_cast<size_t>(p.chunks);
     p.recs = p.bytes;
     p.lists = p.recs + up256(slots * chunks * sizeof(ChunkRec));
-    p.bytes = p.lists + up256(slots * chunks * static_cast<size_t>(p.cap) * sizeof(uint2));
+    p.bins = p.lists + up256(slots * chunks * static_cast<size_t>(p.cap) * sizeof(u64));
+    p.flat = p.bins + slots * kBins * sizeof(u64);
+    p.bytes = p.flat + up256((slots + 1) * sizeof(int32_t));
     return p;
 }
 
@@ -1311,7 +1388,9 @@ extern "C" int sv_sample(const float *logits, int64_t rows, int64_t V, int64_t l
     a.kept = kept;
     a.state = reinterpret_cast<RowState *>(ws);
     a.recs = reinterpret_cast<ChunkRec *>(ws + p.recs);
-    a.lists = reinterpret_cast<uint2 *>(ws + p.lists);
+    a.lists = reinterpret_cast<u64 *>(ws + p.lists);
+    a.bins = reinterpret_cast<u64 *>(ws + p.bins);
+    a.flat = reinterpret_cast<int32_t *>(ws + p.flat);
     hipStream_t st = as_stream(stream);
     for (int64_t row0 = 0; row0 < rows; row0 += p.slots) {
         a.row0 = static_cast<int32_t>(row0);
@@ -1324,6 +1403,9 @@ extern "C" int sv_sample(const float *logits, int64_t rows, int64_t V, int64_t l
             a.group = std::max(1, (a.rows * p.chunks + 1023) / 1024);
             hipLaunchKernelGGL(sample_scan_kernel, dim3((p.chunks + a.group - 1) / a.group, a.rows), dim3(kThreads), 0, st, a);
             hipLaunchKernelGGL(sample_finish_kernel<false>, each, dim3(kThreads), 0, st, a);
+            const dim3 flat(std::min(kFlatGrid, a.rows * p.chunks));
+            hipLaunchKernelGGL(sample_bins_kernel, flat, dim3(kThreads), 0, st, a);
+            hipLaunchKernelGGL(sample_gather_kernel, flat, dim3(kThreads), 0, st, a);
         }
         if (probs || kept)
             hipLaunchKernelGGL(sample_out_kernel, dim3(static_cast<unsigned>((V + kOutPiece - 1) / kOutPiece), a.rows), dim3(kOut), 0,
