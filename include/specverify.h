@@ -642,12 +642,14 @@ int sv_kv_attention(const sv_kv *kv, int32_t layer, const sv_kv_batch *batch, co
  * the batch: the forks of one prompt, whose full pages sv_kv_fork shares).
  * Of these slots as many whole chunks as there are (shared / chunk) are read
  * once for the rows of all sequences; the rest of each sequence is its own.
- * shared may be less than what the sequences share, and 0; it is at most width
- * * page, and 0 with a window.  A sequence that does not hold a shared chunk's
- * pages as the first does, or has fewer committed slots, is refused: its rows
- * are NaN (SV_KV_NOT_SHARED); so are all where the first is out of range.
- * A row's bits are those of sv_kv_attention with the same chunk length, given
- * by the caller or by a rule (chunk 0) that counts the sharing in.  The
+ * With chunk 0 a rule that counts the sharing in gives the chunk length, or
+ * finds that reading once does not pay (a short prefix, rows that fill their
+ * tiles anyway); then the call is sv_kv_attention.  shared may be less than
+ * what the sequences share, and 0; it is at most width * page, and 0 with a
+ * window.  Where slots are read once, a sequence that does not hold a shared
+ * chunk's pages as the first does, or has fewer committed slots, is refused:
+ * its rows are NaN (SV_KV_NOT_SHARED); so are all where the first is out of
+ * range.  A row's bits are those of sv_kv_attention with the same chunk length.  The
  * queries of rows past n_new may be read here; nothing depends on them.  The
  * workspace is that of sv_kv_attention_shared_workspace_bytes. */
 size_t sv_kv_attention_shared_workspace_bytes(const sv_kv *kv, const sv_kv_batch *batch, const sv_kv_attn *attn,

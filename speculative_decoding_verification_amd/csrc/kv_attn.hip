@@ -248,14 +248,63 @@ static int chunk_rule(int64_t pairs, bool batch, int64_t bound, int64_t window, 
     return c;
 }
 
-// The same where `shared` slots are taken once for all rows, in `tiles` row
-// groups.
-static int chunk_rule_shared(int64_t heads, int64_t B, int64_t tiles, int64_t own_tiles, int64_t bound, int64_t shared) {
-    for (int c = 256; c <= 16384 && c <= shared; c += 128) {
-        const int64_t units = heads * (tiles * (shared / c) + B * own_tiles * ((bound - shared / c * c + c - 1) / c));
-        if (units <= 512) return c;
+// The time of a launch, for the choice of its chunks where slots are shared.
+// Two workgroups a compute unit; a unit of work takes kUnit for its start and
+// end, and a time for each slot of its row group.  Shared chunks come first;
+// the sequences' own ones fill the last round.  A last round of one workgroup
+// a compute unit is faster where two of four waves would share the SIMDs.
+// Fitted to sweeps of the chunk length (us, fp16, 16 sequences of 5 x 5 rows of
+// 128 and 8 heads, 32768 shared slots in chunks of 8192, 4096, 2048, 1280: 137,
+// 147, 147, 159; bf16, 32 sequences of 5 rows, 16384 slots in chunks of 4096,
+// 2048, 1024: 118, 71, 83).
+constexpr double kUnit = 10.0, kJoinBytes = 4e6;  // us; bytes of partial sums a us
+struct Load {
+    double slot;  // us
+    bool two;     // waves of a SIMD come from two workgroups
+    Load(int type, int dim, int rt) {
+        two = type == SV_KV_I8 || (type == SV_KV_F16 && dim <= 128);
+        slot = 0.0149 * (0.3 + 0.7 * dim / 128) * (0.35 + 0.325 * rt) * (type == SV_KV_I8 ? 1.4 : two ? 1.0 : 1.55);
     }
-    return 2048;
+    // n1 units of c1 slots, then n2 of c2
+    double time(int64_t n1, int64_t c1, int64_t n2, int64_t c2) const {
+        const double l1 = kUnit + slot * c1, l2 = kUnit + slot * c2;
+        auto part = [&](int64_t m) { return m == 0 ? 0.0 : two && m <= 256 ? 0.62 : 1.0; };
+        const int64_t left = n1 % 512;
+        double t = l1 * (n1 / 512 + part(left)), over = n2 * l2 - (left ? (512 - left) * l1 : 0.0);
+        if (over > 0.0) t += std::max(over / 512, n1 ? 0.0 : l2 * part(n2 % 512));
+        return t;
+    }
+};
+
+// Slots of a chunk where the first `shared` of up to `bound` are to be read
+// once for the rows of all B sequences, in `tiles` row groups and not in
+// own_tiles for each sequence; 0 where that gains nothing over `plain` slots a
+// chunk without it.  A shared unit takes some 3 us more (positions and tables
+// of several sequences).  us, shared against not: 32 sequences of 5 rows, 16384
+// slots, bf16 71 against 267; 8 trees of 16 x 4 rows of 64, 8000 slots, int8,
+// whose tiles are full either way 46 against 45; 4 x 5 rows, 960 slots 15
+// against 13.
+static int chunk_rule_shared(const KvDev &d, int64_t B, int64_t rows, int rt, int64_t tiles, int own_rt, int64_t own_tiles,
+                             int64_t bound, int64_t shared, int plain) {
+    const double row_bytes = static_cast<double>(d.blk_bytes) / kBlk, parts = static_cast<double>(B) * d.heads * rows * d.dim * 8;
+    const int64_t chunks = (bound + plain - 1) / plain, units = B * d.heads * own_tiles * chunks;
+    double best = Load(d.type, d.dim, own_rt).time(0, 0, units, std::min<int64_t>(plain, bound)) + chunks * parts / kJoinBytes;
+    best = std::max(best, B * d.heads * static_cast<double>(bound) * row_bytes / 6.5e6);
+    const Load load(d.type, d.dim, rt);
+    int64_t chosen = 0;
+    for (int64_t n = 1; n <= 48; n++) {
+        const int64_t c = shared / n / 128 * 128, rest = bound - n * c;
+        if (c < 256) break;
+        if (c > (1 << 23)) continue;
+        const int64_t own = (rest + c - 1) / c;
+        const double t = load.time(d.heads * tiles * n, c, B * d.heads * own_tiles * own, std::min(rest, c)) + 3.0 +
+                         (n + own) * parts / kJoinBytes;
+        if (t < best) {
+            best = t;
+            chosen = c;
+        }
+    }
+    return static_cast<int>(chosen);
 }
 
 struct Plan {
@@ -294,20 +343,27 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     SV_REQUIRE(shared == 0 || at->window == 0, SV_ERR_ARG, "kv_attention: a window and shared slots do not go together");
     shared = std::min(shared, p->bound);
     const int64_t all_rows = static_cast<int64_t>(bt->B) * a->rows;
+    const int own_rt = attn_tiles_per_wave(d.dim, a->rows);
     int rt = attn_tiles_per_wave(d.dim, static_cast<int>(all_rows));
-    auto tiles_of = [&](int64_t rows) { return (rows + 16 * rt - 1) / (16 * rt); };
+    auto tiles_of = [](int64_t rows, int rt) { return (rows + 16 * rt - 1) / (16 * rt); };
     a->chunk = at->chunk;
-    if (!a->chunk && shared >= 256 && bt->B > 1)
-        a->chunk = chunk_rule_shared(d.heads, bt->B, tiles_of(all_rows), tiles_of(a->rows), p->bound, shared);
-    if (!a->chunk) a->chunk = chunk_rule(static_cast<int64_t>(bt->B) * d.heads, bt->B > 1, p->bound, at->window, at->sinks);
+    if (!a->chunk) {
+        a->chunk = chunk_rule(static_cast<int64_t>(bt->B) * d.heads, bt->B > 1, p->bound, at->window, at->sinks);
+        if (shared >= 256 && bt->B > 1) {
+            const int c = chunk_rule_shared(d, bt->B, a->rows, rt, tiles_of(all_rows, rt), own_rt, tiles_of(a->rows, own_rt),
+                                            p->bound, shared, a->chunk);
+            if (c) a->chunk = c;
+            else shared = 0;
+        }
+    }
     const int64_t chunks = chunks_within(p->bound, at->window, at->sinks, a->chunk);
     a->chunks = static_cast<int32_t>(chunks);
     // one sequence, or one chunk, shares nothing
     a->shared = bt->B > 1 && chunks > 1 ? static_cast<int32_t>(shared / a->chunk) : 0;
-    if (!a->shared) rt = attn_tiles_per_wave(d.dim, a->rows);
+    if (!a->shared) rt = own_rt;
     p->rt = rt;
-    a->tiles = static_cast<int32_t>(tiles_of(a->rows));
-    a->shared_tiles = static_cast<int32_t>(tiles_of(all_rows));
+    a->tiles = static_cast<int32_t>(tiles_of(a->rows, rt));
+    a->shared_tiles = static_cast<int32_t>(tiles_of(all_rows, rt));
     const int64_t shared_grid = (static_cast<int64_t>(a->shared) * d.heads + 7) / 8 * 8 * a->shared_tiles;
     SV_REQUIRE(shared_grid < (1ll << 23), SV_ERR_SHAPE, "kv_attention: too many chunks (use a longer chunk)");
     a->shared_grid = static_cast<int32_t>(shared_grid);

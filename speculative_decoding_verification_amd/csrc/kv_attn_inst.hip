@@ -49,6 +49,7 @@
 // before a wave has its first block (lengths, page, queries, angles), 3 for
 // its blocks and 3 for the sums of the waves.
 #include <atomic>
+#include <type_traits>
 
 #include "kv_attn.h"
 
@@ -613,38 +614,39 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
     const int last = min((ac + 1) * per, (sp.total + kBlk - 1) / kBlk);
     const int gap0 = (a.sinks + kBlk - 1) / kBlk, gap1 = sp.lo / kBlk;
     auto settle = [&](int j) {  // j, or the next of the wave's blocks past the gap
+        if (SHARED) return j;   // no window
         return j >= gap0 && j < gap1 ? j + (gap1 - j + W - 1) / W * W : j;
     };
     // The page of a block, by a scalar load (a vector load would be counted
-    // behind the ring's transfers, and waiting for it would drain them).
-    auto page_of = [&](int j) {
-        const int e = j >> a.kv.blk_shift;
-        if (j >= last || e >= a.kv.width) return -1;
-        const int p = *(const __attribute__((address_space(4))) int32_t *)(reinterpret_cast<uintptr_t>(
-            a.kv.table + static_cast<int64_t>(sid) * a.kv.width + e));
-        return p >= 0 && p < a.kv.n_pages ? p : -1;
-    };
+    // behind the ring's transfers, and waiting for it would drain them): what
+    // its entry holds, any entry past the last block.  It is looked at a block
+    // later, so that nothing waits for the load.
+    typedef const __attribute__((address_space(4))) int32_t *Entries;
+    const Entries entries = (Entries)reinterpret_cast<uintptr_t>(a.kv.table + static_cast<int64_t>(sid) * a.kv.width);
+    const int last_entry = max(min(((last - 1) >> a.kv.blk_shift) + 1, a.kv.width), 1) - 1;
+    auto entry_of = [&](int j) { return entries[min(j >> a.kv.blk_shift, last_entry)]; };
+    auto page_in = [&](int p) { return p >= 0 && p < a.kv.n_pages ? p : -1; };
     // a block without a page is read from page 0 and masked
     auto block_at = [&](int j, int page) {
         return kv_block(a.kv, a.layer, max(page, 0), head, j & ((1 << a.kv.blk_shift) - 1));
     };
     int j = settle(ac * per + wave);
     const bool any = j < last;
-    int page = page_of(j);
+    int entry = entry_of(j);
 
     // ---- the ring: `slot` is the half read next and, once it is in
     // registers, the half that is refilled
     const uint32_t ring = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((SV_LDS uint8_t *)s_mem));
     const uint32_t mine = ring + wave * S::HALF, mine_scales = ring + S::SCALES_AT + wave * 256;
     uint32_t slot = 0;  // 0 .. N - 1
-    int ji = j, jin = settle(j + W), pin = page_of(jin);  // block to be requested, the one after it, its page
-    const uint8_t *bi = block_at(ji, page);
+    int ji = j, jin = settle(j + W), pin = entry_of(jin);  // block to be requested, the one after it, its entry
+    const uint8_t *bi = block_at(ji, page_in(entry));
     auto advance = [&]() {
         if (jin < last) {  // past the end the last block is requested again, so that the counts hold
             ji = jin;
-            bi = block_at(ji, pin);
+            bi = block_at(ji, page_in(pin));
             jin = settle(jin + W);
-            pin = page_of(jin);
+            pin = entry_of(jin);
         }
     };
     // fp16, bf16: lane by lane what the lane will read; int8: as it lies
@@ -711,9 +713,14 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         for (int i = 0; i < ND; i++) o[t][i] = f4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     const int whole = sp.len + sp.n - a.window;  // with a window: from here on every row's window has begun
+    // EVERY: all slots are seen by all rows.  A loop of its own where a kernel
+    // has such chunks: what the other blocks' masks need would be kept in
+    // registers across it.
+    auto blocks = [&](auto every) __attribute__((always_inline)) {
+    constexpr bool EVERY = decltype(every)::value;
     while (j < last) {
         const int s0 = j * kBlk;
-        const int jn = settle(j + W), page_n = page_of(jn);
+        const int jn = settle(j + W), entry_n = EVERY ? 0 : entry_of(jn), page = EVERY ? 0 : page_in(entry);
         // ---- scores
         Raw<ESZ> kr[2 * NC], vr[ND];
         float ks[8], vs[8];  // int8: the scales of the lane group's eight slots
@@ -755,7 +762,8 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         }
 
         // ---- what is visible, and the running softmax
-        const bool edge = (page < 0 && !(SHARED && all)) || s0 + kBlk > sp.len || (a.window && s0 < whole && s0 + kBlk > a.sinks);
+        const bool edge = !EVERY && (page < 0 || s0 + kBlk > sp.len ||
+                                     (!SHARED && a.window && s0 < whole && s0 + kBlk > a.sinks));
         // slots of the lane group that any row of the tile sees, and those that all see
         uint32_t any_sees = edge ? 0u : 0xFFu, all_see = 0xFFu;
         uint32_t seen[RT];  // slots of the lane group that the lane's row sees
@@ -776,7 +784,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
                 for (int e = 0; e < 8; e++) {
                     const int slot_e = s0 + 8 * to_g + e, nth = slot_e - sp.len;
                     bool sees = page >= 0 && slot_e < sp.total && (nth < 0 || (nth < sp.n && (mask >> nth & 1u)));
-                    if (a.window && sees) {
+                    if (!SHARED && a.window && sees) {
                         int kpos = slot_e;
                         if (nth > 0 && a.bt.tree) kpos = sp.len + __popc(row_mask(a, b, nth) & ((1u << nth) - 1));
                         sees = pos - kpos < a.window || kpos < a.sinks;
@@ -866,7 +874,8 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         }
 
         // ---- o += V^T P^T
-        const uint8_t *blk = block_at(j, page);
+        const uint8_t *blk = nullptr;
+        if (!EVERY) blk = block_at(j, page);
         if constexpr (ESZ == 2) {
             ring_read<S::LEAVE_V, 1024, ND>(mine + slot * (W * S::HALF) + lane * 16, vr);
         } else {
@@ -910,6 +919,7 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
         }
         if constexpr (TYPE == SV_KV_I8) {
             if (any_far) {
+                if (EVERY) blk = block_at(j, page_in(entry_of(j)));
                 // weights with scales that the maximum does not bound: in
                 // fp32, slot by slot
                 const int at_lane = fresh(lane), to_col = at_lane & 15, to_g = at_lane >> 4;
@@ -986,7 +996,14 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
             }
         }
         j = jn;
-        page = page_n;
+        entry = entry_n;
+    }
+    };
+    if constexpr (SHARED) {
+        if (all) blocks(std::true_type{});
+        else blocks(std::false_type{});
+    } else {
+        blocks(std::false_type{});
     }
     // the last requests land before the ring's memory is used again
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
