@@ -168,6 +168,15 @@ constexpr int kMaxLds = 79 * 1024;  // two workgroups a compute unit
 // 131001 slots, 95 against 148 in one twice, int8 batch 79 against 93).
 inline int attn_tiles_per_wave(int dim, int rows) { return dim > 128 || rows <= 16 ? 1 : rows <= 32 || dim > 64 ? 2 : 4; }
 
+// The same where sequences share chunks: a bf16 wave's registers then leave
+// room for a second one on its SIMD, which gains more than reading a block once
+// (it stays in L2) (us: 32 sequences of 5 rows of 128, 16384 slots, one tile 58,
+// two 71; fp16, 16 of 25 rows, 32768 slots, one tile 165, two 136).
+inline int attn_tiles_shared(int type, int dim, int rows) {
+    const int rt = attn_tiles_per_wave(dim, rows);
+    return type == SV_KV_BF16 ? (dim > 64 ? 1 : rt < 2 ? rt : 2) : rt;
+}
+
 // Units: (sequence, head, chunk), in a call that shares chunks those of the
 // sequences' own chunks.
 int attn_launch_f16(const AttnArgs &a, int rt, int64_t units, hipStream_t st);

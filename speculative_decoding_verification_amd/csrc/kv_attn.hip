@@ -248,30 +248,30 @@ static int chunk_rule(int64_t pairs, bool batch, int64_t bound, int64_t window, 
     return c;
 }
 
-// The time of a launch, for the choice of its chunks where slots are shared.
-// Two workgroups a compute unit; a unit of work takes kUnit for its start and
-// end, and a time for each slot of its row group.  Shared chunks come first;
-// the sequences' own ones fill the last round.  A last round of one workgroup
-// a compute unit is faster where two of four waves would share the SIMDs.
-// Fitted to sweeps of the chunk length (us, fp16, 16 sequences of 5 x 5 rows of
-// 128 and 8 heads, 32768 shared slots in chunks of 8192, 4096, 2048, 1280: 137,
-// 147, 147, 159; bf16, 32 sequences of 5 rows, 16384 slots in chunks of 4096,
-// 2048, 1024: 118, 71, 83).
+// The time of a launch, for the choice of its chunks where slots are shared.  A
+// unit of work takes kUnit for its start and end, and a time for each slot of
+// its row group.  Shared chunks come first; the sequences' own ones fill the
+// last round.  Half a round or less is faster, where it leaves each wave a SIMD
+// of its own.  Fitted to sweeps of the chunk length (us, fp16, 16 sequences of
+// 5 x 5 rows of 128 and 8 heads, 32768 shared slots in chunks of 8192, 4096,
+// 2048, 1280: 136, 145, 147, 162; bf16, 32 sequences of 5 rows, 16384 slots in
+// chunks of 4096, 2048, 1024: 94, 58, 66).
 constexpr double kUnit = 10.0, kJoinBytes = 4e6;  // us; bytes of partial sums a us
 struct Load {
-    double slot;  // us
-    bool two;     // waves of a SIMD come from two workgroups
+    double slot;    // us
+    int64_t round;  // workgroups that the chip holds: of four waves two a compute unit, of two four or (LDS) two
     Load(int type, int dim, int rt) {
-        two = type == SV_KV_I8 || (type == SV_KV_F16 && dim <= 128);
-        slot = 0.0149 * (0.3 + 0.7 * dim / 128) * (0.35 + 0.325 * rt) * (type == SV_KV_I8 ? 1.4 : two ? 1.0 : 1.55);
+        const bool four = type == SV_KV_I8 || (type == SV_KV_F16 && dim <= 128);
+        round = four || dim > 128 ? 512 : 1024;
+        slot = 0.0149 * (0.3 + 0.7 * dim / 128) * (0.35 + 0.325 * rt) * (type == SV_KV_I8 ? 1.4 : four ? 1.0 : 2.1);
     }
     // n1 units of c1 slots, then n2 of c2
     double time(int64_t n1, int64_t c1, int64_t n2, int64_t c2) const {
         const double l1 = kUnit + slot * c1, l2 = kUnit + slot * c2;
-        auto part = [&](int64_t m) { return m == 0 ? 0.0 : two && m <= 256 ? 0.62 : 1.0; };
-        const int64_t left = n1 % 512;
-        double t = l1 * (n1 / 512 + part(left)), over = n2 * l2 - (left ? (512 - left) * l1 : 0.0);
-        if (over > 0.0) t += std::max(over / 512, n1 ? 0.0 : l2 * part(n2 % 512));
+        auto part = [&](int64_t m) { return m == 0 ? 0.0 : m <= round / 2 ? 0.62 : 1.0; };
+        const int64_t left = n1 % round;
+        double t = l1 * (n1 / round + (left ? part(left + n2) : 0.0)), over = n2 * l2 - (left ? (round - left) * l1 : 0.0);
+        if (over > 0.0) t += std::max(over / round, n1 ? 0.0 : l2 * part(n2 % round));
         return t;
     }
 };
@@ -281,7 +281,7 @@ struct Load {
 // own_tiles for each sequence; 0 where that gains nothing over `plain` slots a
 // chunk without it.  A shared unit takes some 3 us more (positions and tables
 // of several sequences).  us, shared against not: 32 sequences of 5 rows, 16384
-// slots, bf16 71 against 267; 8 trees of 16 x 4 rows of 64, 8000 slots, int8,
+// slots, bf16 58 against 228; 8 trees of 16 x 4 rows of 64, 8000 slots, int8,
 // whose tiles are full either way 46 against 45; 4 x 5 rows, 960 slots 15
 // against 13.
 static int chunk_rule_shared(const KvDev &d, int64_t B, int64_t rows, int rt, int64_t tiles, int own_rt, int64_t own_tiles,
@@ -344,7 +344,7 @@ static int plan_of(const KvDev &d, const sv_kv_batch *bt, const sv_kv_attn *at, 
     shared = std::min(shared, p->bound);
     const int64_t all_rows = static_cast<int64_t>(bt->B) * a->rows;
     const int own_rt = attn_tiles_per_wave(d.dim, a->rows);
-    int rt = attn_tiles_per_wave(d.dim, static_cast<int>(all_rows));
+    int rt = attn_tiles_shared(d.type, d.dim, static_cast<int>(all_rows));
     auto tiles_of = [](int64_t rows, int rt) { return (rows + 16 * rt - 1) / (16 * rt); };
     a->chunk = at->chunk;
     if (!a->chunk) {
