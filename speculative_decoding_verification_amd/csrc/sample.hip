@@ -964,6 +964,8 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
         if (s.k < finite) {
             border = border_of<false>(sh, &turn, n, border, static_cast<u64>(s.k), low, high);
             low = max(low, border.key);
+        } else {
+            border = Border{low, INT32_MAX};  // the list: what passes its threshold
         }
         within = true;
     } else if (rest && s.k < a.V) {

@@ -94,7 +94,8 @@ def test_settings():
     f = p.view(np.float32)
     assert (f[:, 0] == 0.5).all() and (f[:, 2] == np.float32(0.9)).all() and (f[:, 3] == 0.25).all()
     assert sv.sampling_params(device="cpu").numpy().view(np.float32)[0, [0, 2, 3]].tolist() == [1.0, 1.0, 0.0]
-    for bad in (dict(temperature=[1.0, 2.0], top_k=[1, 2, 3]), dict(top_p=[[0.5]])):
+    for bad in (dict(temperature=[1.0, 2.0], top_k=[1, 2, 3]), dict(top_p=[[0.5]]), dict(top_p=[]), dict(top_k=40.5),
+                dict(top_k=1 << 31), dict(top_k=[1, -(1 << 31) - 1])):
         with pytest.raises(sv.SpecVerifyError):
             sv.sampling_params(**bad, device="cpu")
 
