@@ -9,10 +9,21 @@ that device's current stream unless one is given.
 
 from __future__ import annotations
 
+_torch = None
+
 
 def _sv():
     import speculative_decoding_verification_amd as sv
     return sv
+
+
+def _lib():
+    """The library; torch, which importing the package leaves out, with it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _sv().lib()
 
 
 def _bad(msg):
@@ -34,8 +45,8 @@ def _tensor(t, name, dtype, index, shape):
     return t.data_ptr()
 
 
-def _call(fn, index, *args, stream=None):
-    import torch
+def _call(fn, index, stream, *args):
+    torch = _torch
     if stream is None:
         # the handle of the current stream, without a Stream object made for it
         current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -58,20 +69,21 @@ def add_norm_q8(x, delta=None, gamma=None, eps=1e-6, fold=False, sum=None, y=Non
     RMS norm with weight gamma [K] to y, and the int8 codes of t * gamma to q
     [rows, K], d and sumsq [rows, K / 32] and s16 [rows, K / 16].  fold: the
     norm's factor is left to the codes' consumer (act(..., sumsq_parts))."""
-    import torch
+    fn = _lib().sv_add_norm_q8
     if x.ndim != 2:
         raise _bad("add_norm_q8: x must be [rows, K]")
     index = _device(x, "add_norm_q8: x")
-    rows, K = x.shape
-    f32 = torch.float32
-    one, b32, b16 = x.shape, (rows, K // 32), (rows, K // 16)
-    _call(_sv().lib().sv_add_norm_q8, index, _tensor(x, "add_norm_q8: x", f32, index, one),
+    one = x.shape
+    rows, K = one
+    f32 = _torch.float32
+    b32 = (rows, K // 32)
+    _call(fn, index, stream, _tensor(x, "add_norm_q8: x", f32, index, one),
           _tensor(delta, "add_norm_q8: delta", f32, index, one), rows, K,
           _tensor(gamma, "add_norm_q8: gamma", f32, index, (K,)), eps, int(fold),
           _tensor(sum, "add_norm_q8: sum", f32, index, one), _tensor(y, "add_norm_q8: y", f32, index, one),
-          _tensor(q, "add_norm_q8: q", torch.int8, index, one), _tensor(d, "add_norm_q8: d", f32, index, b32),
-          _tensor(s16, "add_norm_q8: s16", torch.int32, index, b16),
-          _tensor(sumsq, "add_norm_q8: sumsq", f32, index, b32), stream=stream)
+          _tensor(q, "add_norm_q8: q", _torch.int8, index, one), _tensor(d, "add_norm_q8: d", f32, index, b32),
+          _tensor(s16, "add_norm_q8: s16", _torch.int32, index, (rows, K // 16)),
+          _tensor(sumsq, "add_norm_q8: sumsq", f32, index, b32))
 
 
 def sampling_params(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, device="cuda"):
@@ -81,8 +93,10 @@ def sampling_params(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, device="cuda
     import numpy as np
     import torch
     fields = [np.atleast_1d(np.asarray(v)) for v in (temperature, top_k, top_p, min_p)]
-    if any(f.ndim != 1 for f in fields) or len({f.size for f in fields if f.size != 1}) > 1:
+    if any(f.ndim != 1 or f.size == 0 for f in fields) or len({f.size for f in fields if f.size != 1}) > 1:
         raise _bad("sampling_params: settings must be numbers or sequences of one length")
+    if fields[1].dtype.kind not in "iu" or fields[1].min() < -(1 << 31) or fields[1].max() >= 1 << 31:
+        raise _bad("sampling_params: top_k must be integers of 32 bits")
     n = max(f.size for f in fields)
     out = np.zeros((n, 4), np.int32)
     for i, f in enumerate(fields):
@@ -107,7 +121,7 @@ def sample(logits, params, u, tokens, workspace, probs=None, kept=None, stream=N
     apart) with the settings of sampling_params() and uniforms u fp64 [rows];
     probs, kept fp32 [rows, V]: the distribution sampled from, and the logits
     with -inf for what the filters drop.  tokens may be None (then u too)."""
-    import torch
+    fn, torch = _lib().sv_sample, _torch
     index = _device(logits, "sample: logits")
     if logits.ndim != 2 or logits.dtype != torch.float32 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise _bad("sample: logits must be float32 [rows, V] with contiguous rows")
@@ -115,9 +129,9 @@ def sample(logits, params, u, tokens, workspace, probs=None, kept=None, stream=N
     i32 = torch.int32
     if params.ndim != 2 or workspace is None:
         raise _bad("sample: params must be int32 [1 or rows, 4], and a workspace is needed")
-    _call(_sv().lib().sv_sample, index, logits.data_ptr(), rows, V, logits.stride(0) if rows > 1 else V,
+    _call(fn, index, stream, logits.data_ptr(), rows, V, logits.stride(0) if rows > 1 else V,
           _tensor(params, "sample: params", i32, index, (params.shape[0], 4)), params.shape[0],
           _tensor(u, "sample: u", torch.float64, index, (rows,)), _tensor(tokens, "sample: tokens", i32, index, (rows,)),
           _tensor(probs, "sample: probs", torch.float32, index, (rows, V)),
           _tensor(kept, "sample: kept", torch.float32, index, (rows, V)),
-          _tensor(workspace, "sample: workspace", torch.uint8, index, workspace.shape), workspace.numel(), stream=stream)
+          _tensor(workspace, "sample: workspace", torch.uint8, index, workspace.shape), workspace.numel())
