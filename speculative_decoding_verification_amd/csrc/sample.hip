@@ -35,7 +35,7 @@
 //           summed per chunk; the row's last workgroup settles it.
 // What is left (a top-k past the list with a top-p as well, a bin of more
 // elements than a list holds) is selected on the bits of z by that workgroup,
-// in nine passes.
+// in up to nine passes.
 #include <algorithm>
 
 #include "sv_internal.h"
@@ -443,12 +443,20 @@ __device__ void select(const SampleArgs &a, RowShared &sh, const float *row, flo
         __syncthreads();
         for (int i = tid; i < kDigits; i += kThreads) sh.hist[i] = 0;
         __syncthreads();
-        for (int j = tid; j < a.V; j += kThreads) {
-            const float z = gld(row + j);
-            const uint32_t k = float_key(z);
-            if ((k & known) != prefix || !from.keeps(k, j)) continue;
-            const u64 n = MASS ? steps_of(weight_of(z, top, per), a.shift) : 1;
-            atomicAdd(&sh.hist[(k >> low) & ((1u << bits) - 1)], n);
+        for (int c = 0; c < a.chunks; c++) {
+            Held h;
+            h.load(a, row, c);
+            h.settle(a, c);
+#pragma unroll
+            for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float z = h.z[i][e];
+                    const uint32_t k = float_key(z);
+                    if ((k & known) != prefix || !from.keeps(k, c * kChunk + (i * kThreads + tid) * 4 + e)) continue;
+                    const u64 n = MASS ? steps_of(weight_of(z, top, per), a.shift) : 1;
+                    atomicAdd(&sh.hist[(k >> low) & ((1u << bits) - 1)], n);
+                }
         }
         __syncthreads();
         // digits in falling order
@@ -478,16 +486,19 @@ __device__ void select(const SampleArgs &a, RowShared &sh, const float *row, flo
     const u64 need = (want - above + each - 1) / each;
     u64 passed = 0;
     int cut = a.V;
-    for (int j0 = 0; j0 < a.V; j0 += kThreads) {
-        const int j = j0 + tid;
-        bool is = false;
-        if (j < a.V) {
-            const uint32_t k = float_key(gld(row + j));
-            is = k == prefix && from.keeps(k, j);
+    static_assert(kEach <= 32, "a bit for each");
+    for (int j0 = 0; j0 < a.V; j0 += kChunk) {  // a thread has consecutive ones
+        const int own = j0 + tid * kEach;
+        uint32_t is = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const uint32_t k = float_key(gld(row + min(own + i, a.V - 1)));
+            is |= static_cast<uint32_t>(own + i < a.V && k == prefix && from.keeps(k, own + i)) << i;
         }
         u64 all;
-        const u64 before = passed + block_scan(sh.wave, static_cast<u64>(is), &all);
-        if (is && before + 1 == need) sh.at = j + 1;
+        u64 run = passed + block_scan(sh.wave, static_cast<u64>(__popc(is)), &all);
+        for (; is; is &= is - 1)
+            if (++run == need) sh.at = own + __ffs(is);
         passed += all;
         if (passed >= need) {
             __syncthreads();
@@ -557,17 +568,26 @@ __device__ void slow_row(const SampleArgs &a, RowShared &sh, int r, float top, c
     const float *row = row_of(a, r);
     const int tid = threadIdx.x;
     u64 n = 0, finite;
+#pragma unroll 8
     for (int j = tid; j < a.V; j += kThreads) n += gld(row + j) > -INFINITY;
     block_scan(sh.wave, n, &finite);
     Border border = no_border();
     if (static_cast<u64>(s.k) < finite) select<false>(a, sh, row, top, s.per, static_cast<u64>(s.k), &border);
     auto sum_kept = [&](double least) {
         u64 sum = 0, all;
-        for (int j = tid; j < a.V; j += kThreads) {
-            const float z = gld(row + j);
-            if (!border.keeps(float_key(z), j)) continue;
-            const double w = weight_of(z, top, s.per);
-            if (w >= least) sum += steps_of(w, a.shift);
+        for (int c = 0; c < a.chunks; c++) {
+            Held h;
+            h.load(a, row, c);
+            h.settle(a, c);
+#pragma unroll
+            for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float z = h.z[i][e];
+                    if (!border.keeps(float_key(z), c * kChunk + (i * kThreads + tid) * 4 + e)) continue;
+                    const double w = weight_of(z, top, s.per);
+                    if (w >= least) sum += steps_of(w, a.shift);
+                }
         }
         block_scan(sh.wave, sum, &all);
         return all;
