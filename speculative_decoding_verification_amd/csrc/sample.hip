@@ -490,7 +490,7 @@ __device__ void select(const SampleArgs &a, RowShared &sh, const float *row, flo
     for (int j0 = 0; j0 < a.V; j0 += kChunk) {  // a thread has consecutive ones
         const int own = j0 + tid * kEach;
         uint32_t is = 0;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < kEach; i++) {
             const uint32_t k = float_key(gld(row + min(own + i, a.V - 1)));
             is |= static_cast<uint32_t>(own + i < a.V && k == prefix && from.keeps(k, own + i)) << i;
@@ -516,36 +516,35 @@ __device__ __forceinline__ u64 threshold(double u, u64 total) {
     const u64 t = static_cast<u64>(u * static_cast<double>(total));
     return t < total ? t : total - 1;
 }
-// Steps of a thread's consecutive elements of a chunk, kept ones alone.
-__device__ __forceinline__ u64 kept_steps(const SampleArgs &a, const float *row, int c, Border border, float top, const Settings &s,
-                                          u64 (&steps)[kEach]) {
-    const int j0 = c * kChunk + threadIdx.x * kEach;
-    u64 sum = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; i++) {
-        const float z = gld(row + min(j0 + i, a.V - 1));
-        const double w = weight_of(z, top, s.per);
-        steps[i] = j0 + i < a.V && border.keeps(float_key(z), j0 + i) && w >= s.least ? steps_of(w, a.shift) : 0;
-        sum += steps[i];
-    }
-    return sum;
+// Steps of element j, if it is kept.
+__device__ __forceinline__ u64 kept_steps(const SampleArgs &a, float z, int j, Border border, float top, const Settings &s) {
+    const double w = weight_of(z, top, s.per);
+    return border.keeps(float_key(z), j) && w >= s.least ? steps_of(w, a.shift) : 0;
 }
 // The first element of chunk c at which the running sum of kept weights,
 // `passed` before the chunk, exceeds `past`; -1 if none does, *passed moved.
 __device__ int token_in(const SampleArgs &a, RowShared &sh, const float *row, int c, u64 *passed, u64 past, Border border,
                         float top, const Settings &s) {
-    u64 steps[kEach], all;
-    const u64 sum = kept_steps(a, row, c, border, top, s, steps);
-    u64 run = *passed + block_scan(sh.wave, sum, &all);
-#pragma unroll
+    const int first = c * kChunk, j0 = first + static_cast<int>(threadIdx.x) * kEach;
+    u64 sum = 0, all;
+#pragma unroll 4
     for (int i = 0; i < kEach; i++) {
-        if (run <= past && run + steps[i] > past) sh.at = c * kChunk + static_cast<int>(threadIdx.x) * kEach + i;
-        run += steps[i];
+        const float z = gld(row + min(j0 + i, a.V - 1));
+        sum += j0 + i < a.V ? kept_steps(a, z, j0 + i, border, top, s) : 0;
     }
+    const u64 run = *passed + block_scan(sh.wave, sum, &all);
     *passed += all;
     if (*passed <= past) return -1;
+    if (run <= past && run + sum > past) {
+        sh.at = threadIdx.x;
+        sh.above = run;
+    }
     __syncthreads();
-    return sh.at;
+    // that thread's elements, one a lane
+    static_assert(kEach <= 64, "a lane for each element");
+    const int at = first + sh.at * kEach, lane = threadIdx.x & 63, j = at + lane;
+    const u64 own = lane < kEach && j < a.V ? kept_steps(a, gld(row + j), j, border, top, s) : 0;
+    return at + __ffsll(__ballot(sh.above + wave_scan(own) > past)) - 1;
 }
 
 __device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale, int token) {
@@ -1061,32 +1060,59 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
 }
 
 // ------------------------------------------------------------- flat rows
+// A workgroup's share of the flat rows' chunks: a run of them, so that what it
+// needs of a row or leaves for it is fetched or written once.
+struct Share {
+    int at, end, slot, chunk, to;  // chunks [chunk, to) of the row
+    __device__ Share(const SampleArgs &a, int items) {
+        const int each = items / gridDim.x, more = items % gridDim.x, b = blockIdx.x;
+        at = each * b + min(b, more);
+        end = at + each + (b < more);
+    }
+    __device__ bool next(const SampleArgs &a) {
+        if (at >= end) return false;
+        const int row = at / a.chunks;
+        slot = gld(a.flat + 1 + row);
+        chunk = at - row * a.chunks;
+        to = min(a.chunks, chunk + end - at);
+        at += to - chunk;
+        return true;
+    }
+};
+
 __global__ __launch_bounds__(kThreads) void sample_bins_kernel(SampleArgs a) {
     __shared__ u64 s_bins[kBins];
+    const int tid = threadIdx.x;
     const int items = gld(a.flat) * a.chunks;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
+    if (items == 0) return;
+    Share share(a, items);
+    while (share.next(a)) {
+        const int r = a.row0 + share.slot;
         const int kind = gld(&a.state[r].kind);
         if (kind != kByCount && kind != kByMass) continue;
+        const float *row = row_of(a, r);
         Held h;
-        h.load(a, row_of(a, r), c);
+        h.load(a, row, share.chunk);
         const float top = gld(&a.state[r].top), per_bin = gld(&a.state[r].per_bin);
         const Settings s = settings_of(a, r);
         __syncthreads();
-        for (int i = threadIdx.x; i < kBins; i += kThreads) s_bins[i] = 0;
+        for (int i = tid; i < kBins; i += kThreads) s_bins[i] = 0;
         __syncthreads();
-        h.settle(a, c);
+        for (int c = share.chunk; c < share.to; c++) {
+            if (c > share.chunk) h.load(a, row, c);
+            h.settle(a, c);
 #pragma unroll
-        for (int i = 0; i < kQuads; i++)
+            for (int i = 0; i < kQuads; i++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float z = h.z[i][e];
-                const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
-                if (z > -INFINITY) atomicAdd(&s_bins[bin_of(z, top, per_bin)], n);
-            }
+                for (int e = 0; e < 4; e++) {
+                    const float z = h.z[i][e];
+                    const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
+                    if (z > -INFINITY) atomicAdd(&s_bins[bin_of(z, top, per_bin)], n);
+                }
+        }
         __syncthreads();
-        u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins;
-        for (int i = threadIdx.x; i < kBins; i += kThreads)
+        u64 *bins = a.bins + static_cast<int64_t>(share.slot) * kBins;
+        for (int i = tid; i < kBins; i += kThreads)
             if (s_bins[i]) add_dev(bins + i, s_bins[i]);
     }
 }
@@ -1195,89 +1221,117 @@ __device__ void settle_row(const SampleArgs &a, RowShared &sh, int slot, const R
     done(a, r, border, st.top, ldexp(1.0, a.shift) / static_cast<double>(all), token);
 }
 
-__global__ __launch_bounds__(kThreads) void sample_gather_kernel(SampleArgs a) {
+// The border's bin of a flat row, and what lies above it; past all bins if what
+// is wanted is more than there is.
+__device__ __forceinline__ int border_bin(const SampleArgs &a, RowShared &sh, int slot, const RowState &st, u64 *above) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid == 0) {
+        sh.digit = kBins;
+        sh.above = 0;
+    }
+    __syncthreads();
+    if (st.kind == kByCount || st.kind == kByMass) {
+        constexpr int each = kBins / kThreads;
+        const u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins + tid * each;
+        u64 b[each], sum = 0, all;
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            b[i] = gld(bins + i);
+            sum += b[i];
+        }
+        u64 before = block_scan(sh.wave, sum, &all);
+#pragma unroll
+        for (int i = 0; i < each; i++) {
+            if (before < st.want && before + b[i] >= st.want) {
+                sh.digit = tid * each + i;
+                sh.above = before;
+            }
+            before += b[i];
+        }
+        __syncthreads();
+    }
+    *above = sh.above;
+    return sh.digit;
+}
+
+// A workgroup's chunks come first, then the rows whose last chunks it had: a row
+// settled in between would hold up the next one.  Two workgroups share a
+// compute unit, at the price of a few registers that wait in memory while a row
+// is settled (us, 64 and 256 flat rows of 151936: 43 and 103; one a unit 55 and
+// 124; chunks dealt one by one and not in runs 72 and 291).
+static_assert(kSlots <= kFlatGrid, "a workgroup's chunks are of two rows at most");
+__global__ __launch_bounds__(kThreads, 4) void sample_gather_kernel(SampleArgs a) {
     __shared__ RowShared sh;
-    __shared__ int s_last;
-    const int items = gld(a.flat) * a.chunks, tid = threadIdx.x;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int slot = gld(a.flat + 1 + it / a.chunks), c = it % a.chunks, r = a.row0 + slot;
+    __shared__ int s_last[2], s_n;
+    const int tid = threadIdx.x;
+    const int items = gld(a.flat) * a.chunks;
+    if (items == 0) return;
+    Share share(a, items);
+    if (tid == 0) s_n = 0;
+    while (share.next(a)) {
+        const int slot = share.slot, r = a.row0 + slot;
         const RowState st = a.state[r];
-        const Settings s = settings_of(a, r);
-        Held h;
-        h.load(a, row_of(a, r), c);
-        // the border's bin; past all of them if what is wanted is more than there is
-        __syncthreads();
-        if (tid == 0) {
-            sh.digit = kBins;
-            sh.above = 0;
-        }
-        __syncthreads();
-        if (st.kind == kByCount || st.kind == kByMass) {
-            constexpr int each = kBins / kThreads;
-            const u64 *bins = a.bins + static_cast<int64_t>(slot) * kBins + tid * each;
-            u64 b[each], sum = 0, all;
-#pragma unroll
-            for (int i = 0; i < each; i++) {
-                b[i] = gld(bins + i);
-                sum += b[i];
-            }
-            u64 before = block_scan(sh.wave, sum, &all);
-#pragma unroll
-            for (int i = 0; i < each; i++) {
-                if (before < st.want && before + b[i] >= st.want) {
-                    sh.digit = tid * each + i;
-                    sh.above = before;
-                }
-                before += b[i];
-            }
-            __syncthreads();
-        }
-        const int bin = sh.digit;
-        const u64 above = sh.above;
         if (st.kind != kSlow) {
-            h.settle(a, c);
-            Masks masks;
-            u64 sum = 0;
+            const float *row = row_of(a, r);
+            Held h;
+            h.load(a, row, share.chunk);
+            const Settings s = settings_of(a, r);
+            u64 above;
+            const int bin = border_bin(a, sh, slot, st, &above);
+            for (int c = share.chunk; c < share.to; c++) {
+                if (c > share.chunk) h.load(a, row, c);
+                h.settle(a, c);
+                Masks masks;
+                u64 sum = 0;
 #pragma unroll
-            for (int i = 0; i < kQuads; i++)
+                for (int i = 0; i < kQuads; i++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float z = h.z[i][e];
-                    const int b = z > -INFINITY ? bin_of(z, st.top, st.per_bin) : kBins + 1;
-                    masks[i][e] = __ballot(b == bin);
-                    const double w = weight_of(z, st.top, s.per);
-                    if (b < bin && w >= s.least) sum += steps_of(w, a.shift);
-                }
-            sum = wave_sum(sum);
-            if ((tid & 63) == 0) sh.wave_kept[tid >> 6] = sum;
-            int at[kQuads];
-            const int n = places_of(masks, sh.room, at);
-            u64 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
-#pragma unroll
-            for (int i = 0; i < kQuads; i++)
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    if (masks[i][e] >> (tid & 63) & 1) {
-                        if (at[i] < a.cap)
-                            st_dev(list + at[i], entry_of(h.z[i][e], c * kChunk + (i * kThreads + tid) * 4 + e));
-                        at[i]++;
+                    for (int e = 0; e < 4; e++) {
+                        const float z = h.z[i][e];
+                        const int b = z > -INFINITY ? bin_of(z, st.top, st.per_bin) : kBins + 1;
+                        masks[i][e] = __ballot(b == bin);
+                        const double w = weight_of(z, st.top, s.per);
+                        if (b < bin && w >= s.least) sum += steps_of(w, a.shift);
                     }
-            if (tid == 0) {
-                u64 steps = 0;
-                for (int w = 0; w < W; w++) steps += sh.wave_kept[w];
-                ChunkRec *rec = a.recs + static_cast<int64_t>(slot) * a.chunks + c;
-                st_dev(&rec->n, n);
-                st_dev(&rec->steps, steps);
+                sum = wave_sum(sum);
+                __syncthreads();  // the last chunk's sums and numbers have been read
+                if ((tid & 63) == 0) sh.wave_kept[tid >> 6] = sum;
+                int at[kQuads];
+                const int n = places_of(masks, sh.room, at);
+                u64 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
+#pragma unroll
+                for (int i = 0; i < kQuads; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (masks[i][e] >> (tid & 63) & 1) {
+                            if (at[i] < a.cap)
+                                st_dev(list + at[i], entry_of(h.z[i][e], c * kChunk + (i * kThreads + tid) * 4 + e));
+                            at[i]++;
+                        }
+                if (tid == 0) {
+                    u64 steps = 0;
+                    for (int w = 0; w < W; w++) steps += sh.wave_kept[w];
+                    ChunkRec *rec = a.recs + static_cast<int64_t>(slot) * a.chunks + c;
+                    st_dev(&rec->n, n);
+                    st_dev(&rec->steps, steps);
+                }
             }
         }
         // lists and sums have been written through before the count that says
         // so; who sees the row's last one reads them where all see the same
         drain();
         __syncthreads();
-        if (tid == 0) s_last = add_dev(&a.state[r].gathered, 1) == a.chunks - 1;
-        __syncthreads();
-        if (!s_last) continue;
-        settle_row(a, sh, slot, st, s, bin, above);
+        const int own = share.to - share.chunk;
+        if (tid == 0 && add_dev(&a.state[r].gathered, own) == a.chunks - own) s_last[s_n++] = slot;
+    }
+    __syncthreads();
+    for (int i = 0; i < s_n; i++) {
+        const int slot = s_last[i], r = a.row0 + slot;
+        const RowState st = a.state[r];
+        u64 above;
+        const int bin = border_bin(a, sh, slot, st, &above);
+        settle_row(a, sh, slot, st, settings_of(a, r), bin, above);
         __syncthreads();
     }
 }
