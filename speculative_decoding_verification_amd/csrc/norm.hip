@@ -12,6 +12,11 @@
 // apart: lanes 4, 2 and 1 apart here, then the elements of a lane.  The row's
 // sum of squares is that of its blocks' sums, taken from LDS in an order that
 // K alone gives, so that a row's bits do not depend on the other rows.
+//
+// Bound by memory where the rows are many (8192 rows of 5120, codes: 119 us, 4.8
+// TB/s of 13.5 bytes an element, what a large copy reaches; 3001 of 2560, y: 20),
+// by the latency of one launch where they are few (5 rows of 5120: 3.0 us with
+// the factor left out, 4.3 with it).
 #include "sv_internal.h"
 
 namespace sv {
@@ -140,19 +145,21 @@ __global__ __launch_bounds__(THREADS) void add_norm_kernel(NormArgs a) {
 }
 
 constexpr int kNormGrid = 1 << 20;  // threads of a launch fit 32 bits
-template <int THREADS>
+// 1024 threads a row where few rows leave the chip empty (up to 512 of more than
+// 1024 elements) and from the lengths on at which 256 threads would hold six
+// quads each: us with 256 and 1024 threads, codes, in a graph: 5 rows of 5120
+// 6.1 and 4.3, 256 7.4 and 5.7, 1024 17.2 and 17.2; 8192 rows of 2560 51 and 69,
+// of 5120 113 and 114, of 8192 181 and 169; 64 rows of 1024 3.0 and 3.3.
+constexpr int kNarrow = 5120;
+inline bool wide_rows(int64_t rows, int64_t K) { return K > kNarrow || (rows <= 512 && K > 1024); }
+
+template <int THREADS, int NV = 1>
 static void launch_norm(const NormArgs &a, hipStream_t st) {
-    const dim3 grid(a.rows < kNormGrid ? a.rows : kNormGrid), block(THREADS);
-    switch ((a.K / 4 + THREADS - 1) / THREADS) {
-        case 1: hipLaunchKernelGGL((add_norm_kernel<THREADS, 1>), grid, block, 0, st, a); break;
-        case 2: hipLaunchKernelGGL((add_norm_kernel<THREADS, 2>), grid, block, 0, st, a); break;
-        case 3: hipLaunchKernelGGL((add_norm_kernel<THREADS, 3>), grid, block, 0, st, a); break;
-        case 4: hipLaunchKernelGGL((add_norm_kernel<THREADS, 4>), grid, block, 0, st, a); break;
-        case 5: hipLaunchKernelGGL((add_norm_kernel<THREADS, 5>), grid, block, 0, st, a); break;
-        case 6: hipLaunchKernelGGL((add_norm_kernel<THREADS, 6>), grid, block, 0, st, a); break;
-        case 7: hipLaunchKernelGGL((add_norm_kernel<THREADS, 7>), grid, block, 0, st, a); break;
-        default: hipLaunchKernelGGL((add_norm_kernel<THREADS, 8>), grid, block, 0, st, a); break;
+    constexpr int longest = THREADS == 256 ? kNarrow : 32 * kNormBlocks;
+    if constexpr (4 * THREADS * NV < longest) {
+        if (a.K > 4 * THREADS * NV) return launch_norm<THREADS, NV + 1>(a, st);
     }
+    hipLaunchKernelGGL((add_norm_kernel<THREADS, NV>), dim3(a.rows < kNormGrid ? a.rows : kNormGrid), dim3(THREADS), 0, st, a);
 }
 
 }  // namespace sv
@@ -195,10 +202,10 @@ extern "C" int sv_add_norm_q8(const float *x, const float *delta, int64_t rows, 
     if (fold) {
         const int64_t quads = rows * (K / 4);
         hipLaunchKernelGGL(add_quant_kernel, dim3(static_cast<unsigned>((quads + kFold - 1) / kFold)), dim3(kFold), 0, st, a);
-    } else if (K <= 4 * 8 * 256) {
-        launch_norm<256>(a, st);
-    } else {
+    } else if (wide_rows(rows, K)) {
         launch_norm<1024>(a, st);
+    } else {
+        launch_norm<256>(a, st);
     }
     return hip_check(hipGetLastError(), "add_norm_q8 launch");
 }
