@@ -28,7 +28,7 @@
 //           without filters takes its token from the chunks' sums and one
 //           chunk.
 // A row whose kept set goes past the list (a flat distribution) is read twice
-// more, by the workgroups of two launches that find nothing to do otherwise:
+// more, by workgroups of one or two launches that find nothing to do otherwise:
 //   bins    amounts (elements, or steps of weight) by the distance from the
 //           largest value, which gives the border's bin;
 //   gather  that bin's elements are listed and the kept weights above it
@@ -57,6 +57,7 @@ constexpr int kLevel = 512;              // parts that a range of keys is cut in
 constexpr int kDigits = 2048;
 constexpr int kSlots = 256;              // rows that are under way at once
 constexpr int kFlatGrid = 512;           // workgroups of the passes over flat rows
+constexpr int kOneLaunch = 256;
 constexpr int64_t kMaxVocab = 1 << 24;
 constexpr int64_t kMaxRows = 65535;
 
@@ -84,7 +85,7 @@ struct RowState {
     double scale;    // weight times this: probability
     u64 want;        // elements or steps to be kept
     float per_bin;   // bins to a unit of z, below top
-    int32_t gathered;  // chunks
+    int32_t counted, gathered;  // chunks
 };
 
 struct SampleArgs {
@@ -104,7 +105,7 @@ struct SampleArgs {
     ChunkRec *recs;   // [slots][chunks]
     u64 *lists;       // [slots][chunks][cap]: bits of z, index in the high half
     u64 *bins;        // [slots][kBins]
-    int32_t *flat;    // number of flat rows, then their slots
+    int32_t *flat;    // number of flat rows, of parts of their work taken, then their slots
 };
 
 __device__ __forceinline__ const float *row_of(const SampleArgs &a, int r) { return a.logits + static_cast<int64_t>(r) * a.ld; }
@@ -549,7 +550,7 @@ __device__ int token_in(const SampleArgs &a, RowShared &sh, const float *row, in
 
 __device__ __forceinline__ void done(const SampleArgs &a, int r, Border border, float top, double scale, int token) {
     if (threadIdx.x) return;
-    a.state[r] = RowState{kWithin, top, border.key, border.cut, scale, 0, 0.0f, 0};
+    a.state[r] = RowState{kWithin, top, border.key, border.cut, scale, 0, 0.0f, 0, 0};
     if (a.tokens) gst(a.tokens + r, token);
 }
 __device__ __forceinline__ void failed(const SampleArgs &a, int r) {
@@ -637,7 +638,7 @@ __global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) 
     Held h;
     h.load(a, row, c0);
     const Settings s = settings_of(a, r);
-    if (blockIdx.x == 0 && slot == 0 && tid == 0) a.flat[0] = 0;
+    if (blockIdx.x == 0 && slot == 0 && tid < 2) a.flat[tid] = 0;
     float most = v[0];
 #pragma unroll
     for (int i = 1; i < 8; i++) most = fmaxf(most, v[i]);
@@ -1034,8 +1035,8 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
         const float bottom = kind == kByCount || kind == kByMass ? bottom_of(a, sh, row, top, s.per) : 0.0f;
         if (tid == 0) {
             const float per_bin = static_cast<float>(kBins - 1) / fmaxf(top - bottom, 1e-30f);
-            a.state[r] = RowState{kind, top, 0, 0, 0.0, want, per_bin, 0};
-            a.flat[1 + add_dev(a.flat, 1)] = slot;
+            a.state[r] = RowState{kind, top, 0, 0, 0.0, want, per_bin, 0, 0};
+            a.flat[2 + add_dev(a.flat, 1)] = slot;
         }
         for (int i = tid; i < kBins; i += kThreads) a.bins[static_cast<int64_t>(slot) * kBins + i] = 0;
         return;
@@ -1060,19 +1061,19 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
 }
 
 // ------------------------------------------------------------- flat rows
-// A workgroup's share of the flat rows' chunks: a run of them, so that what it
+// Part `at` of `parts` of the flat rows' chunks: a run of them, so that what it
 // needs of a row or leaves for it is fetched or written once.
 struct Share {
     int at, end, slot, chunk, to;  // chunks [chunk, to) of the row
-    __device__ Share(const SampleArgs &a, int items) {
-        const int each = items / gridDim.x, more = items % gridDim.x, b = blockIdx.x;
-        at = each * b + min(b, more);
-        end = at + each + (b < more);
+    __device__ Share(int items, int part, int parts) {
+        const int each = items / parts, more = items % parts;
+        at = each * part + min(part, more);
+        end = at + each + (part < more);
     }
     __device__ bool next(const SampleArgs &a) {
         if (at >= end) return false;
         const int row = at / a.chunks;
-        slot = gld(a.flat + 1 + row);
+        slot = gld(a.flat + 2 + row);
         chunk = at - row * a.chunks;
         to = min(a.chunks, chunk + end - at);
         at += to - chunk;
@@ -1080,41 +1081,31 @@ struct Share {
     }
 };
 
-__global__ __launch_bounds__(kThreads) void sample_bins_kernel(SampleArgs a) {
-    __shared__ u64 s_bins[kBins];
+// Amounts of a row's chunks by the distance from its largest value.
+__device__ void count_bins(const SampleArgs &a, RowShared &sh, const Share &share, const RowState &st, const Settings &s) {
     const int tid = threadIdx.x;
-    const int items = gld(a.flat) * a.chunks;
-    if (items == 0) return;
-    Share share(a, items);
-    while (share.next(a)) {
-        const int r = a.row0 + share.slot;
-        const int kind = gld(&a.state[r].kind);
-        if (kind != kByCount && kind != kByMass) continue;
-        const float *row = row_of(a, r);
-        Held h;
-        h.load(a, row, share.chunk);
-        const float top = gld(&a.state[r].top), per_bin = gld(&a.state[r].per_bin);
-        const Settings s = settings_of(a, r);
-        __syncthreads();
-        for (int i = tid; i < kBins; i += kThreads) s_bins[i] = 0;
-        __syncthreads();
-        for (int c = share.chunk; c < share.to; c++) {
-            if (c > share.chunk) h.load(a, row, c);
-            h.settle(a, c);
+    const float *row = row_of(a, a.row0 + share.slot);
+    Held h;
+    h.load(a, row, share.chunk);
+    __syncthreads();
+    for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+    __syncthreads();
+    for (int c = share.chunk; c < share.to; c++) {
+        if (c > share.chunk) h.load(a, row, c);
+        h.settle(a, c);
 #pragma unroll
-            for (int i = 0; i < kQuads; i++)
+        for (int i = 0; i < kQuads; i++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float z = h.z[i][e];
-                    const u64 n = kind == kByCount ? 1 : steps_of(weight_of(z, top, s.per), a.shift);
-                    if (z > -INFINITY) atomicAdd(&s_bins[bin_of(z, top, per_bin)], n);
-                }
-        }
-        __syncthreads();
-        u64 *bins = a.bins + static_cast<int64_t>(share.slot) * kBins;
-        for (int i = tid; i < kBins; i += kThreads)
-            if (s_bins[i]) add_dev(bins + i, s_bins[i]);
+            for (int e = 0; e < 4; e++) {
+                const float z = h.z[i][e];
+                const u64 n = st.kind == kByCount ? 1 : steps_of(weight_of(z, st.top, s.per), a.shift);
+                if (z > -INFINITY) atomicAdd(&sh.hist[bin_of(z, st.top, st.per_bin)], n);
+            }
     }
+    __syncthreads();
+    u64 *bins = a.bins + static_cast<int64_t>(share.slot) * kBins;
+    for (int i = tid; i < kBins; i += kThreads)
+        if (sh.hist[i]) add_dev(bins + i, sh.hist[i]);
 }
 
 // A flat row whose chunks have all been gathered: `above` amounts lie above
@@ -1237,7 +1228,7 @@ __device__ __forceinline__ int border_bin(const SampleArgs &a, RowShared &sh, in
         u64 b[each], sum = 0, all;
 #pragma unroll
         for (int i = 0; i < each; i++) {
-            b[i] = gld(bins + i);
+            b[i] = ld_dev(bins + i);
             sum += b[i];
         }
         u64 before = block_scan(sh.wave, sum, &all);
@@ -1255,84 +1246,114 @@ __device__ __forceinline__ int border_bin(const SampleArgs &a, RowShared &sh, in
     return sh.digit;
 }
 
-// A workgroup's chunks come first, then the rows whose last chunks it had: a row
-// settled in between would hold up the next one.  Two workgroups share a
-// compute unit, at the price of a few registers that wait in memory while a row
-// is settled (us, 64 and 256 flat rows of 151936: 43 and 103; one a unit 55 and
-// 124; chunks dealt one by one and not in runs 72 and 291).
-static_assert(kSlots <= kFlatGrid, "a workgroup's chunks are of two rows at most");
-__global__ __launch_bounds__(kThreads, 4) void sample_gather_kernel(SampleArgs a) {
-    __shared__ RowShared sh;
-    __shared__ int s_last[2], s_n;
+// Lists the border's bin of a row's chunks and sums the kept weights above it.
+__device__ void gather(const SampleArgs &a, RowShared &sh, const Share &share, const RowState &st, const Settings &s, int bin) {
     const int tid = threadIdx.x;
-    const int items = gld(a.flat) * a.chunks;
-    if (items == 0) return;
-    Share share(a, items);
-    if (tid == 0) s_n = 0;
-    while (share.next(a)) {
-        const int slot = share.slot, r = a.row0 + slot;
-        const RowState st = a.state[r];
-        if (st.kind != kSlow) {
-            const float *row = row_of(a, r);
-            Held h;
-            h.load(a, row, share.chunk);
+    const float *row = row_of(a, a.row0 + share.slot);
+    for (int c = share.chunk; c < share.to; c++) {
+        Held h;
+        h.load(a, row, c);
+        h.settle(a, c);
+        Masks masks;
+        u64 sum = 0;
+#pragma unroll
+        for (int i = 0; i < kQuads; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float z = h.z[i][e];
+                const int b = z > -INFINITY ? bin_of(z, st.top, st.per_bin) : kBins + 1;
+                masks[i][e] = __ballot(b == bin);
+                const double w = weight_of(z, st.top, s.per);
+                if (b < bin && w >= s.least) sum += steps_of(w, a.shift);
+            }
+        sum = wave_sum(sum);
+        __syncthreads();  // the last chunk's sums and numbers have been read
+        if ((tid & 63) == 0) sh.wave_kept[tid >> 6] = sum;
+        int at[kQuads];
+        const int n = places_of(masks, sh.room, at);
+        u64 *list = a.lists + (static_cast<int64_t>(share.slot) * a.chunks + c) * a.cap;
+#pragma unroll
+        for (int i = 0; i < kQuads; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (masks[i][e] >> (tid & 63) & 1) {
+                    if (at[i] < a.cap) st_dev(list + at[i], entry_of(h.z[i][e], c * kChunk + (i * kThreads + tid) * 4 + e));
+                    at[i]++;
+                }
+        if (tid == 0) {
+            u64 steps = 0;
+            for (int w = 0; w < W; w++) steps += sh.wave_kept[w];
+            ChunkRec *rec = a.recs + static_cast<int64_t>(share.slot) * a.chunks + c;
+            st_dev(&rec->n, n);
+            st_dev(&rec->steps, steps);
+        }
+    }
+}
+
+// The passes over the flat rows: a launch each, or one (kBoth), where the call
+// has at most kOneLaunch chunks.  That spares a call without flat rows 2 us and
+// costs one whose rows are all flat the numbers' traffic (us, one launch against
+// two, no flat row and all: 1 row of 151936 14.8 against 16.8 and 43.8 against
+// 42.8; 48 rows of 33024 18.8 against 20.9 and 51.9 against 47.5; 32 rows of
+// 151936, 608 chunks, all flat 83 against 67).  In one launch workgroups take
+// parts of the work by a running number, first all parts of the counting, then
+// all of the gathering.  Who gathers waits for the row's counting; its parts
+// have lower numbers, so running workgroups have them, and these do not wait:
+// the wait ends, however few workgroups run at once.  What one workgroup leaves
+// for another is written through before the count that says so, and read where
+// all see the same.  Two workgroups share a compute unit, at the price of a few
+// registers that wait in memory while a row is settled (us, 64 and 256 flat rows
+// of 151936: 43 and 103 for the gathering; one a unit 55 and 124).  Chunks go to
+// workgroups in runs (dealt one by one 72 and 291, one a unit).
+enum Pass { kCount, kGather, kBoth };
+template <Pass PASS>
+__global__ __launch_bounds__(kThreads, 4) void sample_flat_kernel(SampleArgs a) {
+    __shared__ RowShared sh;
+    __shared__ int s_part, s_last;
+    const int items = gld(a.flat) * a.chunks, tid = threadIdx.x, parts = min(static_cast<int>(gridDim.x), items);
+    if (static_cast<int>(blockIdx.x) >= parts) return;
+    for (bool first = true;; first = false) {
+        int part = blockIdx.x;
+        if (PASS == kBoth) {
+            __syncthreads();
+            if (tid == 0) s_part = add_dev(a.flat + 1, 1);
+            __syncthreads();
+            part = s_part;
+            if (part >= 2 * parts) break;
+        } else if (!first) {
+            break;
+        }
+        const bool counting = PASS == kCount || (PASS == kBoth && part < parts);
+        Share share(items, PASS == kBoth && !counting ? part - parts : part, parts);
+        while (share.next(a)) {
+            const int slot = share.slot, r = a.row0 + slot, own = share.to - share.chunk;
+            const RowState st = a.state[r];
             const Settings s = settings_of(a, r);
+            const bool counted = st.kind == kByCount || st.kind == kByMass;
+            if (counting) {
+                if (!counted) continue;
+                count_bins(a, sh, share, st, s);
+                if (PASS == kBoth) {
+                    drain();
+                    __syncthreads();
+                    if (tid == 0) add_dev(&a.state[r].counted, own);
+                }
+                continue;
+            }
+            if (PASS == kBoth && counted) {
+                if (tid == 0)
+                    while (ld_dev(&a.state[r].counted) != a.chunks) __builtin_amdgcn_s_sleep(4);
+                __syncthreads();
+            }
             u64 above;
             const int bin = border_bin(a, sh, slot, st, &above);
-            for (int c = share.chunk; c < share.to; c++) {
-                if (c > share.chunk) h.load(a, row, c);
-                h.settle(a, c);
-                Masks masks;
-                u64 sum = 0;
-#pragma unroll
-                for (int i = 0; i < kQuads; i++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const float z = h.z[i][e];
-                        const int b = z > -INFINITY ? bin_of(z, st.top, st.per_bin) : kBins + 1;
-                        masks[i][e] = __ballot(b == bin);
-                        const double w = weight_of(z, st.top, s.per);
-                        if (b < bin && w >= s.least) sum += steps_of(w, a.shift);
-                    }
-                sum = wave_sum(sum);
-                __syncthreads();  // the last chunk's sums and numbers have been read
-                if ((tid & 63) == 0) sh.wave_kept[tid >> 6] = sum;
-                int at[kQuads];
-                const int n = places_of(masks, sh.room, at);
-                u64 *list = a.lists + (static_cast<int64_t>(slot) * a.chunks + c) * a.cap;
-#pragma unroll
-                for (int i = 0; i < kQuads; i++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        if (masks[i][e] >> (tid & 63) & 1) {
-                            if (at[i] < a.cap)
-                                st_dev(list + at[i], entry_of(h.z[i][e], c * kChunk + (i * kThreads + tid) * 4 + e));
-                            at[i]++;
-                        }
-                if (tid == 0) {
-                    u64 steps = 0;
-                    for (int w = 0; w < W; w++) steps += sh.wave_kept[w];
-                    ChunkRec *rec = a.recs + static_cast<int64_t>(slot) * a.chunks + c;
-                    st_dev(&rec->n, n);
-                    st_dev(&rec->steps, steps);
-                }
-            }
+            if (st.kind != kSlow) gather(a, sh, share, st, s, bin);
+            drain();
+            __syncthreads();
+            if (tid == 0) s_last = add_dev(&a.state[r].gathered, own) == a.chunks - own;
+            __syncthreads();
+            if (s_last) settle_row(a, sh, slot, st, s, bin, above);
         }
-        // lists and sums have been written through before the count that says
-        // so; who sees the row's last one reads them where all see the same
-        drain();
-        __syncthreads();
-        const int own = share.to - share.chunk;
-        if (tid == 0 && add_dev(&a.state[r].gathered, own) == a.chunks - own) s_last[s_n++] = slot;
-    }
-    __syncthreads();
-    for (int i = 0; i < s_n; i++) {
-        const int slot = s_last[i], r = a.row0 + slot;
-        const RowState st = a.state[r];
-        u64 above;
-        const int bin = border_bin(a, sh, slot, st, &above);
-        settle_row(a, sh, slot, st, settings_of(a, r), bin, above);
-        __syncthreads();
     }
 }
 
@@ -1415,7 +1436,7 @@ static SamplePlan sample_plan(int64_t rows, int64_t V) {
     p.lists = p.recs + up256(slots * chunks * sizeof(ChunkRec));
     p.bins = p.lists + up256(slots * chunks * static_cast<size_t>(p.cap) * sizeof(u64));
     p.flat = p.bins + slots * kBins * sizeof(u64);
-    p.bytes = p.flat + up256((slots + 1) * sizeof(int32_t));
+    p.bytes = p.flat + up256((slots + 2) * sizeof(int32_t));
     return p;
 }
 
@@ -1480,8 +1501,12 @@ extern "C" int sv_sample(const float *logits, int64_t rows, int64_t V, int64_t l
             hipLaunchKernelGGL(sample_scan_kernel, dim3((p.chunks + a.group - 1) / a.group, a.rows), dim3(kThreads), 0, st, a);
             hipLaunchKernelGGL(sample_finish_kernel<false>, each, dim3(kThreads), 0, st, a);
             const dim3 flat(std::min(kFlatGrid, a.rows * p.chunks));
-            hipLaunchKernelGGL(sample_bins_kernel, flat, dim3(kThreads), 0, st, a);
-            hipLaunchKernelGGL(sample_gather_kernel, flat, dim3(kThreads), 0, st, a);
+            if (a.rows * p.chunks <= kOneLaunch) {
+                hipLaunchKernelGGL(sample_flat_kernel<kBoth>, flat, dim3(kThreads), 0, st, a);
+            } else {
+                hipLaunchKernelGGL(sample_flat_kernel<kCount>, flat, dim3(kThreads), 0, st, a);
+                hipLaunchKernelGGL(sample_flat_kernel<kGather>, flat, dim3(kThreads), 0, st, a);
+            }
         }
         if (probs || kept)
             hipLaunchKernelGGL(sample_out_kernel, dim3(static_cast<unsigned>((V + kOutPiece - 1) / kOutPiece), a.rows), dim3(kOut), 0,

@@ -256,3 +256,17 @@ def test_shared_slots_past_the_sequences_and_one_sequence():
         f = Forks(km.F16, 2, 3, 64, 64, prompt, own, 2)
         for shared in (0, 1, f.shared // 2, f.shared):
             assert np.array_equal(f.run(f.plan(shared, 128)), f.run(f.plan(0, 128))), (own, shared)
+
+
+@pytest.mark.parametrize("rows,V", [(1, 2561), (5, 50021), (13, 151936), (14, 151936), (64, 30000), (65, 30000)])
+def test_flat_rows_in_one_launch_and_in_two(rows, V):
+    """About the number of chunks up to which both passes over flat rows are
+    one launch; a row's bits are the same either way."""
+    rng = np.random.default_rng(rows)
+    z, u = logits_of(rng, rows, V, "flat"), rng.random(rows)
+    s = [SETTINGS[i % 10] for i in range(rows)]
+    got = run_sample(z, s, u)
+    check_sample(z, s, u, got)
+    many = run_sample(np.concatenate([z] * 20), s * 20, np.concatenate([u] * 20))
+    for n in got:
+        assert got[n].tobytes() * 20 == many[n].tobytes(), n
