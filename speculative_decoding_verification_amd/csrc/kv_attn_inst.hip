@@ -283,9 +283,24 @@ __device__ __forceinline__ void lds_read8(uint32_t at, uint32_t at4, float (&s)[
 // Transfers global memory to LDS, 16 bytes a lane (lane i to `to` + 16 i).
 // ONCE: no other workgroup of the launch reads it, so it need not stay in
 // the caches (non-temporal).
-template <bool ONCE>
+// OFFSET is added to both addresses by the instruction.
+template <bool ONCE, int OFFSET = 0>
 __device__ __forceinline__ void to_lds(const uint8_t *from, uint32_t to) {
-    __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, 0, ONCE ? 2 : 0);
+    __builtin_amdgcn_global_load_lds(from, (SV_LDS void *)static_cast<uintptr_t>(to), 16, OFFSET, ONCE ? 2 : 0);
+}
+// Transfers I .. N - 1 of a half, 1024 bytes apart in LDS and in memory
+// PAIR * (i / 2) + ODD * (i % 2) bytes from the lane's first, `own` bytes past a
+// uniform address.  Four KB of memory share an address: the rest is the
+// instruction's offset, which the LDS address takes back.  (An address in vector
+// registers for each transfer takes an addition and two scalar registers for its
+// constant, of which the loop has too few: us, 16 rounds over 32768 shared
+// slots 140.5 against 138.5, trees 25.5 against 25.2.)
+template <bool ONCE, int PAIR, int ODD, int N, int I = 0>
+__device__ __forceinline__ void half_to_lds(const uint8_t *from, uint32_t own, uint32_t to) {
+    constexpr int AT = PAIR * (I / 2) + ODD * (I % 2), OFFSET = AT % 4096;
+    static_assert(I * 1024 >= OFFSET, "an LDS address below the half");
+    to_lds<ONCE, OFFSET>(from + (AT - OFFSET) + own, to + I * 1024 - OFFSET);
+    if constexpr (I + 1 < N) half_to_lds<ONCE, PAIR, ODD, N, I + 1>(from, own, to);
 }
 
 // Waves and their rings, for two workgroups a compute unit: four where the
@@ -653,17 +668,14 @@ __global__ __launch_bounds__((64 * Shape<TYPE, D, RT>::W), (Shape<TYPE, D, RT>::
     const uint32_t k_from = ESZ == 2 ? (g * 32 + 8 * (col >> 2) + (col & 3)) * 16 : lane * 16;
     const uint32_t v_from = ESZ == 2 ? (g * D + col) * 16 : lane * 16;
     auto request_k = [&]() {
-#pragma unroll
-        for (int i = 0; i < S::LOADS; i++)
-            to_lds<ONCE>(bi + k_from + (ESZ == 2 ? (i >> 1) * 2048 + (i & 1) * 64 : i * 1024), mine + slot * (W * S::HALF) + i * 1024);
+        half_to_lds<ONCE, 2048, (ESZ == 2 ? 64 : 1024), S::LOADS>(bi, fresh(k_from), mine + slot * (W * S::HALF));
         if constexpr (S::SCALES) {
             if (lane < 16) to_lds<ONCE>(bi + 64 * D + lane * 16, mine_scales + (slot >> 1) * (W * 256));
         }
     };
     auto request_v = [&]() {
-#pragma unroll
-        for (int i = 0; i < S::LOADS; i++)
-            to_lds<ONCE>(bi + S::HALF + v_from + (ESZ == 2 ? i * 256 : i * 1024), mine + slot * (W * S::HALF) + i * 1024);
+        half_to_lds<ONCE, (ESZ == 2 ? 512 : 2048), (ESZ == 2 ? 256 : 1024), S::LOADS>(bi + S::HALF, fresh(v_from),
+                                                                                     mine + slot * (W * S::HALF));
         advance();
     };
     auto turn = [&]() { slot = slot + 1 == S::N ? 0 : slot + 1; };
