@@ -414,7 +414,8 @@ typedef struct {
  * Weights are fp64 and summed as whole numbers of steps of 2^-s, s = min(51,
  * 63 - ceil(log2 V)): exact in any order, so a row's results depend on
  * nothing but the row.  Weights below half a step, 1e-9 of the row at most
- * for V = 151936, are never drawn.
+ * for V = 151936, are then never drawn.  A row that no filter touches may be
+ * summed in fp64 instead, in an order that V alone gives.
  * A row that holds NaN or +inf or no finite logit, or whose settings are out
  * of range, fails: token -1, probs and kept NaN throughout.  A u outside
  * [0, 1) gives token -1 alone.
