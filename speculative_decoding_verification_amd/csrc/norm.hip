@@ -13,10 +13,10 @@
 // sum of squares is that of its blocks' sums, taken from LDS in an order that
 // K alone gives, so that a row's bits do not depend on the other rows.
 //
-// Bound by memory where the rows are many (8192 rows of 5120, codes: 119 us, 4.8
-// TB/s of 13.5 bytes an element, what a large copy reaches; 3001 of 2560, y: 20),
-// by the latency of one launch where they are few (5 rows of 5120: 3.0 us with
-// the factor left out, 4.3 with it).
+// Bound by memory where the rows are many (8192 rows of 5120, codes: 104 us, 5.4
+// TB/s of 13.5 bytes an element, past what a large copy reaches; 3001 of 2560, y:
+// 19.5), by the latency of one launch where they are few (in a graph, 5 rows of
+// 5120: 2.4 us with the factor left out, 4.3 with it).
 #include "sv_internal.h"
 
 namespace sv {
@@ -36,7 +36,10 @@ struct NormArgs {
 };
 
 __device__ __forceinline__ f4 ld4(const float *p) { return *(const SV_GLOBAL f4 *)p; }
-__device__ __forceinline__ void st4(float *p, f4 v) { *(SV_GLOBAL f4 *)p = v; }
+// Vectors are stored past the L2, which holds nothing for the next launch's
+// other XCDs anyway (us in a graph: 512 rows of 5120, codes 9.4 -> 7.5; 8192 of
+// 2560 49 -> 44, y 65 -> 49; 80 rows the same).
+__device__ __forceinline__ void st4(float *p, f4 v) { __builtin_nontemporal_store(v, (SV_GLOBAL f4 *)p); }
 
 // Largest value, and sum, over the eight lanes of a block.
 __device__ __forceinline__ float max8(float v) {
@@ -52,10 +55,13 @@ __device__ __forceinline__ f4 sum8(f4 v) {
     return v;
 }
 
-// t = x + delta of a quad, stored; the block's sum of squares.
+// t = x + delta of a quad.  ONCE: what is read fits no cache, and is loaded past
+// them (kCached below).
+template <bool ONCE>
 __device__ __forceinline__ f4 add_quad(const NormArgs &a, int64_t at) {
-    f4 t = ld4(a.x + at);
-    if (a.delta) t += ld4(a.delta + at);
+    auto ld = [](const float *p) { return ONCE ? __builtin_nontemporal_load((const SV_GLOBAL f4 *)p) : ld4(p); };
+    f4 t = ld(a.x + at);
+    if (a.delta) t += ld(a.delta + at);
     return t;
 }
 __device__ __forceinline__ float block_squares(f4 t) {
@@ -77,7 +83,7 @@ __device__ __forceinline__ void store_codes(const NormArgs &a, int64_t at, f4 v,
     }
     s += __shfl_xor(s, 2, 64);
     s += __shfl_xor(s, 1, 64);
-    gst(reinterpret_cast<uint32_t *>(a.q + at), w);
+    __builtin_nontemporal_store(w, (SV_GLOBAL uint32_t *)(a.q + at));
     const int lane = threadIdx.x & 7;
     if ((lane & 3) == 0) gst(a.s16 + at / 16, s);
     if (lane == 0) {
@@ -88,12 +94,13 @@ __device__ __forceinline__ void store_codes(const NormArgs &a, int64_t at, f4 v,
 
 // Factor left to the consumer: no row is needed as a whole.
 constexpr int kFold = 256;
+template <bool ONCE>
 __global__ __launch_bounds__(kFold) void add_quant_kernel(NormArgs a) {
     const int i = blockIdx.x * kFold + threadIdx.x, quads = a.K / 4;
     const int row = a.by_quads(i);
     if (row >= a.rows) return;  // eight lanes of a block leave together
     const int64_t at = static_cast<int64_t>(i) * 4;
-    const f4 t = add_quad(a, at);
+    const f4 t = add_quad<ONCE>(a, at);
     f4 v = t;
     if (a.gamma) v *= ld4(a.gamma + 4 * (i - row * quads));
     if (a.sum) st4(a.sum + at, t);
@@ -102,7 +109,7 @@ __global__ __launch_bounds__(kFold) void add_quant_kernel(NormArgs a) {
 
 // Factor applied: a workgroup a row, NV quads a thread in registers.
 constexpr int kNormBlocks = 1024;  // of a row
-template <int THREADS, int NV>
+template <int THREADS, int NV, bool ONCE>
 __global__ __launch_bounds__(THREADS) void add_norm_kernel(NormArgs a) {
     __shared__ float s_sq[kNormBlocks];
     const int tid = threadIdx.x, quads = a.K / 4, nb = a.K / 32;
@@ -113,7 +120,7 @@ __global__ __launch_bounds__(THREADS) void add_norm_kernel(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < NV; k++) {
             const int i = tid + k * THREADS;
-            t[k] = i < quads ? add_quad(a, base + 4 * i) : f4{0.0f, 0.0f, 0.0f, 0.0f};
+            t[k] = i < quads ? add_quad<ONCE>(a, base + 4 * i) : f4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         __syncthreads();  // the last row's sums have been read
 #pragma unroll
@@ -153,13 +160,30 @@ constexpr int kNormGrid = 1 << 20;  // threads of a launch fit 32 bits
 constexpr int kNarrow = 5120;
 inline bool wide_rows(int64_t rows, int64_t K) { return K > kNarrow || (rows <= 512 && K > 1024); }
 
-template <int THREADS, int NV = 1>
+// Bytes of x and delta past which nothing of them is found in the memory-side
+// cache of 256 MB, and loads that do not ask it are faster (us in a graph, codes,
+// such loads against others: 8192 rows of 5120, 336 MB, 105 and 111; 20000 222
+// and 241; 8192 of 2560, 168 MB, 50 and 44).
+constexpr int64_t kCached = 1ll << 28;
+
+template <int THREADS, bool ONCE, int NV = 1>
 static void launch_norm(const NormArgs &a, hipStream_t st) {
     constexpr int longest = THREADS == 256 ? kNarrow : 32 * kNormBlocks;
     if constexpr (4 * THREADS * NV < longest) {
-        if (a.K > 4 * THREADS * NV) return launch_norm<THREADS, NV + 1>(a, st);
+        if (a.K > 4 * THREADS * NV) return launch_norm<THREADS, ONCE, NV + 1>(a, st);
     }
-    hipLaunchKernelGGL((add_norm_kernel<THREADS, NV>), dim3(a.rows < kNormGrid ? a.rows : kNormGrid), dim3(THREADS), 0, st, a);
+    hipLaunchKernelGGL((add_norm_kernel<THREADS, NV, ONCE>), dim3(a.rows < kNormGrid ? a.rows : kNormGrid), dim3(THREADS), 0, st, a);
+}
+template <bool ONCE>
+static void launch(const NormArgs &a, bool fold, hipStream_t st) {
+    if (fold) {
+        const int64_t quads = static_cast<int64_t>(a.rows) * (a.K / 4);
+        hipLaunchKernelGGL(add_quant_kernel<ONCE>, dim3(static_cast<unsigned>((quads + kFold - 1) / kFold)), dim3(kFold), 0, st, a);
+    } else if (wide_rows(a.rows, a.K)) {
+        launch_norm<1024, ONCE>(a, st);
+    } else {
+        launch_norm<256, ONCE>(a, st);
+    }
 }
 
 }  // namespace sv
@@ -199,13 +223,7 @@ extern "C" int sv_add_norm_q8(const float *x, const float *delta, int64_t rows, 
     NormArgs a{x, delta, gamma, sum, y, q, d, s16, sumsq, static_cast<int32_t>(rows), static_cast<int32_t>(K), eps,
                div_by(static_cast<uint32_t>(K / 4))};
     hipStream_t st = as_stream(stream);
-    if (fold) {
-        const int64_t quads = rows * (K / 4);
-        hipLaunchKernelGGL(add_quant_kernel, dim3(static_cast<unsigned>((quads + kFold - 1) / kFold)), dim3(kFold), 0, st, a);
-    } else if (wide_rows(rows, K)) {
-        launch_norm<1024>(a, st);
-    } else {
-        launch_norm<256>(a, st);
-    }
+    if (rows * K * (delta ? 8 : 4) > kCached) launch<true>(a, fold, st);
+    else launch<false>(a, fold, st);
     return hip_check(hipGetLastError(), "add_norm_q8 launch");
 }
