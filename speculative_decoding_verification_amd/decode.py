@@ -9,7 +9,7 @@ that device's current stream unless one is given.
 
 from __future__ import annotations
 
-_torch = None
+_torch = _library = _raw_stream = None
 
 
 def _sv():
@@ -18,12 +18,15 @@ def _sv():
 
 
 def _lib():
-    """The library; torch, which importing the package leaves out, with it."""
-    global _torch
-    if _torch is None:
+    """The library; torch, which importing the package leaves out, with it,
+    and its call for the handle of a device's current stream, where it has one
+    that makes no Stream object."""
+    global _torch, _library, _raw_stream
+    if _library is None:
         import torch
-        _torch = torch
-    return _sv().lib()
+        _torch, _library = torch, _sv().lib()
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return _library
 
 
 def _bad(msg):
@@ -46,21 +49,18 @@ def _tensor(t, name, dtype, index, shape):
 
 
 def _call(fn, index, stream, *args):
-    torch = _torch
+    cuda = _torch.cuda
     if stream is None:
-        # the handle of the current stream, without a Stream object made for it
-        current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = current(index) if current else torch.cuda.current_stream(index).cuda_stream
+        stream = _raw_stream(index) if _raw_stream else cuda.current_stream(index).cuda_stream
     elif hasattr(stream, "cuda_stream"):
         stream = stream.cuda_stream
-    if torch.cuda.current_device() == index:
+    if cuda.current_device() == index:
         rc = fn(*args, stream)
     else:
-        with torch.cuda.device(index):
+        with cuda.device(index):
             rc = fn(*args, stream)
     if rc:
-        sv = _sv()
-        raise sv.SpecVerifyError(rc, sv.lib().sv_last_error().decode())
+        raise _sv().SpecVerifyError(rc, _library.sv_last_error().decode())
 
 
 def add_norm_q8(x, delta=None, gamma=None, eps=1e-6, fold=False, sum=None, y=None, q=None, d=None, s16=None,
