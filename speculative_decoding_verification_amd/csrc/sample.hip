@@ -152,10 +152,18 @@ __device__ __forceinline__ double exp2_of(double y) {
 __device__ __forceinline__ double weight_of(float z, float one, double per) {
     return exp2_of((static_cast<double>(z) - static_cast<double>(one)) * per);
 }
-// The same relative to the sample's largest value, in one rounding less: a
-// factor that all weights of a row share does not matter.  shift_of = -ref *
-// per; not for (z - ref) * per past 1000.
+// The same relative to the sample's largest value ref, in one rounding less:
+// 2^(z per - hi) with hi = ref per as fp64 rounds it (shift_of = -hi), for (z -
+// ref) per up to 1000.  What that rounding leaves, lo = ref per - hi, is in all
+// weights of a row as a factor 2^lo, and with it in their sums: rest_of tells
+// lo, exactly, to who compares such a sum with weights of the other form.
+// Where abs(ref) per reaches kLoose, lo may be any number: such sums are not
+// used (below it abs(lo) is at most a quarter).
+constexpr double kLoose = 4503599627370496.0;  // 2^52
 __device__ __forceinline__ double shift_of(float ref, double per) { return -(static_cast<double>(ref) * per); }
+__device__ __forceinline__ double rest_of(float ref, double per) {
+    return fma(static_cast<double>(ref), per, shift_of(ref, per));
+}
 __device__ __forceinline__ double loose_weight(float z, double per, double shift) {
     return exp2_of(fma(static_cast<double>(z), per, shift));
 }
@@ -948,7 +956,10 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
     }
     const bool usable = WHOLE || (!(flags & kOver) && total <= kList);
     const bool rest = !WHOLE && (!usable || (flags & kRest));
-    const bool summed = !WHOLE && sum > 0.0 && (static_cast<double>(top) - static_cast<double>(ref)) * s.per < 900.0;
+    const bool summed = !WHOLE && sum > 0.0 && fabs(static_cast<double>(ref)) * s.per < kLoose &&
+                        (static_cast<double>(top) - static_cast<double>(ref)) * s.per < 900.0;
+    // the sum of all weights relative to the row's largest value
+    const double whole = summed ? sum * exp2_of((static_cast<double>(ref) - static_cast<double>(top)) * s.per - rest_of(ref, s.per)) : 0.0;
     const int finite = usable ? static_cast<int>(total) : 0;  // listed
     const int n = WHOLE ? a.V : finite;                       // entries; -inf among them are below any border
     if (WHOLE) {
@@ -1006,8 +1017,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
         if (!within && !summed) {
             kind = kSlow;
         } else {
-            const double goal = ceil(s.p * (within ? static_cast<double>(pool)
-                                                   : sum * weight_of(ref, top, s.per) * ldexp(1.0, a.shift)));
+            const double goal = ceil(s.p * (within ? static_cast<double>(pool) : ldexp(whole, a.shift)));
             want = goal < 1.0 ? 1 : static_cast<u64>(goal);
             if (within) want = min(want, pool);
             if (want <= pool) {
@@ -1025,7 +1035,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
             within = true;
         } else if (s.least == 0.0 && summed) {
             const int token = u >= 0.0 ? token_unfiltered(a, sh, slot, row, c0, c1, own, sum_before, u * sum, ref, s.per) : -1;
-            done(a, r, no_border(), top, 1.0 / (sum * weight_of(ref, top, s.per)), token);
+            done(a, r, no_border(), top, 1.0 / whole, token);
             return;
         } else {
             kind = kNoBorder;
