@@ -798,16 +798,22 @@ __device__ int token_unfiltered(const SampleArgs &a, RowShared &sh, int slot, co
         sh.last = 0;
     }
     __syncthreads();
-    if (c0 < c1 && before + own > past) atomicMin(&sh.at, tid);
+    // of those with a weight the first that passes it, or the last: the sums
+    // before a thread's chunks and those before its elements are rounded in
+    // different orders, so that none may, or one without any weight
+    if (own > 0.0 && before + own > past) atomicMin(&sh.at, tid);
     if (own > 0.0) atomicMax(&sh.last, tid);
     __syncthreads();
-    if (tid == (sh.at < INT32_MAX ? sh.at : sh.last)) {  // walks its chunks
+    if (tid == (sh.at < INT32_MAX ? sh.at : sh.last)) {  // walks its chunks, in the same way
         int c = c0;
-        double base = before;
-        for (; c + 1 < c1; c++) {
-            const double next = base + a.recs[static_cast<int64_t>(slot) * a.chunks + c].sum;
-            if (next > past) break;
+        double base = before, next = before;
+        for (int i = c0; i < c1; i++) {
+            const double sum = a.recs[static_cast<int64_t>(slot) * a.chunks + i].sum;
+            if (sum == 0.0) continue;
+            c = i;
             base = next;
+            next += sum;
+            if (next > past) break;
         }
         sh.digit = c;
         sh.base = base;

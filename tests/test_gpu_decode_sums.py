@@ -72,3 +72,23 @@ def test_rows_of_one_value_are_uniform(V):
         got = run_sample(z, [(t, 0, 0.25, 0.0)], u)
         n = -(-V // 4)
         assert ((got["kept"] != -np.inf).sum(1) == n).all() and (got["kept"][:, :n] == z[:, :n]).all()
+
+
+@pytest.mark.parametrize("V,at", [(67 * 8192, (64, 65)), (1 << 24, (256, 260)), (1 << 24, (2040, 2044)), (1 << 24, (2044, 2045))])
+def test_the_last_tokens_of_a_masked_row(V, at):
+    """A certain token and, in two later pieces of 8192, one each of weight
+    0.4 * 2^-52, which sums lose or not by their order; all behind is masked.
+    u next to 1 gives one of the three, never a masked token."""
+    t = torch()
+    z = t.full((1, V), -np.inf, device="cuda")
+    z[0, :8192] = -5000.0                       # finite, and of no weight
+    able = [5] + [8192 * c + 100 for c in at]
+    z[0, able[0]] = 0.0
+    z[0, able[1:]] = -36.96
+    tok = t.zeros(1, dtype=t.int32, device="cuda")
+    u = t.full((1,), 1 - 2.0 ** -53, dtype=t.float64, device="cuda")
+    sv.sample(z, sv.sampling_params(1.0), u, tok, sv.sample_workspace(1, V))
+    assert tok.item() in able
+    u.fill_(0.5)
+    sv.sample(z, sv.sampling_params(1.0), u, tok, sv.sample_workspace(1, V))
+    assert tok.item() == 5
