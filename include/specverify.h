@@ -413,9 +413,12 @@ typedef struct {
  *   distribution.
  * Weights are fp64 and summed as whole numbers of steps of 2^-s, s = min(51,
  * 63 - ceil(log2 V)): exact in any order, so a row's results depend on
- * nothing but the row.  Weights below half a step, 1e-9 of the row at most
- * for V = 151936, are then never drawn.  A row that no filter touches may be
- * summed in fp64 instead, in an order that V alone gives.
+ * nothing but the row.  Weights below half a step, together V 2^-(s + 1) of
+ * the largest at most (2.2e-9 for V = 151936, 1.5e-5 for 2^24), are then never
+ * drawn.  Two sums may be fp64 instead, of the weights as they are, in an order
+ * that V alone gives: that of a row that no filter touches, and, without a
+ * top_k, the one that top_p is a share of.  This share counts the weights below
+ * half a step; where it passes all that the steps make up, all are kept.
  * A row that holds NaN or +inf or no finite logit, or whose settings are out
  * of range, fails: token -1, probs and kept NaN throughout.  A u outside
  * [0, 1) gives token -1 alone.

@@ -13,9 +13,12 @@
 // as the nearest multiple of 2^-s with s = 63 - ceil(log2 V), at most 51
 // (2^-45 for 151936 tokens), so a sum of V of them fits 64 bits and is the
 // same in any order: atomics and any split of a row give the same bits.  A
-// weight below half a step is never drawn: all of them together are less than
-// V^2 2^-64 of the row (1e-9 for 151936).  Sums over a whole row that nothing
-// filters are fp64, in the order of its chunks.
+// weight below half a step is never drawn: all of them together are at most V
+// 2^-(s + 1) of the largest (2.2e-9 for 151936, 1.5e-5 for 2^24).  Sums over a
+// whole row whose list does not hold it are fp64, of the weights as they are, in
+// the order of its chunks: that of a row that nothing filters, and without a
+// top-k the one that top-p is a share of.  That share is compared with sums of
+// steps, so its border is off by what they leave out at most.
 //
 // One pass over the logits decides nearly every row:
 //   scan    a workgroup per chunk of a row: a sample of the row gives a

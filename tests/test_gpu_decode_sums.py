@@ -92,3 +92,20 @@ def test_the_last_tokens_of_a_masked_row(V, at):
     u.fill_(0.5)
     sv.sample(z, sv.sampling_params(1.0), u, tok, sv.sample_workspace(1, V))
     assert tok.item() == 5
+
+
+def test_a_share_of_weights_below_half_a_step():
+    """One token of weight 1 and 2^22 - 1 just below half a step, whose sum
+    passes what top-p leaves: by the sum of the weights as they are nearly all
+    are kept, and as the steps do not reach it, all."""
+    V = 1 << 22
+    z = np.full((1, V), -29.2, np.float32)
+    assert np.exp(-29.2) < 2.0 ** -(dm.steps(V) + 1)
+    z[0, 77] = 0.0
+    s, u = [(1.0, 0, 1 - 2.0 ** -24, 0.0)], [0.9]
+    got = run_sample(z, s, u)
+    check_sample(z, s, u, got)
+    assert got["tokens"].tolist() == [77] and (got["kept"] == z).all()
+    s = [(1.0, 0, 0.999, 0.0)]
+    got = run_sample(z, s, u)
+    assert (got["kept"] != -np.inf).sum() == 1 and got["kept"][0, 77] == 0.0
