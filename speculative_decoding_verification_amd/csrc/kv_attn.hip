@@ -283,7 +283,11 @@ struct Load {
 // of several sequences).  us, shared against not: 32 sequences of 5 rows, 16384
 // slots, bf16 58 against 228; 8 trees of 16 x 4 rows of 64, 8000 slots, int8,
 // whose tiles are full either way 46 against 45; 4 x 5 rows, 960 slots 15
-// against 13.
+// against 13.  The sequences' own chunks are counted in own_tiles row groups too,
+// though bf16 is launched with groups half as tall (from 17 rows on, 33 up to 64
+// of dim): counted as launched, the choice differs in 31 of 4000 drawn shapes,
+// which then take 1195 us together and not 1122 (15 x 24 rows of 96, 2048 slots
+// 38 against 30; but 4 x 64 rows of 96, 18368 slots 37 against 43).
 static int chunk_rule_shared(const KvDev &d, int64_t B, int64_t rows, int rt, int64_t tiles, int own_rt, int64_t own_tiles,
                              int64_t bound, int64_t shared, int plain) {
     const double row_bytes = static_cast<double>(d.blk_bytes) / kBlk, parts = static_cast<double>(B) * d.heads * rows * d.dim * 8;
