@@ -160,9 +160,13 @@ __device__ __forceinline__ double weight_of(float z, float one, double per) {
 // ref) per up to 1000.  What that rounding leaves, lo = ref per - hi, is in all
 // weights of a row as a factor 2^lo, and with it in their sums: rest_of tells
 // lo, exactly, to who compares such a sum with weights of the other form.
-// Where abs(ref) per reaches kLoose, lo may be any number: such sums are not
-// used (below it abs(lo) is at most a quarter).
-constexpr double kLoose = 4503599627370496.0;  // 2^52
+// per is taken by powers of two below what brings abs(ref) per to 2^51, so
+// abs(lo) is at most an eighth: past that, values next to each other are 2^26
+// apart in the exponent, and with less than their per the same weights stay 1
+// and 0.
+__device__ __forceinline__ double loose_per(float ref, double per) {
+    return ldexp(per, min(51 - __builtin_amdgcn_frexp_exp(static_cast<double>(ref) * per), 0));
+}
 __device__ __forceinline__ double shift_of(float ref, double per) { return -(static_cast<double>(ref) * per); }
 __device__ __forceinline__ double rest_of(float ref, double per) {
     return fma(static_cast<double>(ref), per, shift_of(ref, per));
@@ -674,7 +678,7 @@ __global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) 
     __syncthreads();
     const float tau = s_tau, ref = s_ref, from = fmaxf(tau, -3.402823466e38f);  // finite ones alone
     const bool summed = s.k == a.V && (s.p < 1.0 || s.least == 0.0);
-    const double less = shift_of(ref, s.per);
+    const double per = loose_per(ref, s.per), less = shift_of(ref, per);
 
     // ---- the chunks
     for (int c = c0; c < c1; c++) {
@@ -712,7 +716,7 @@ __global__ __launch_bounds__(kThreads, 8) void sample_scan_kernel(SampleArgs a) 
 #pragma unroll
             for (int i = 0; i < kQuads; i++)
 #pragma unroll
-                for (int e = 0; e < 4; e++) sum += loose_weight(h.z[i][e], s.per, less);
+                for (int e = 0; e < 4; e++) sum += loose_weight(h.z[i][e], per, less);
             sum = wave_sum(sum);
         }
         if (lane == 0) {
@@ -965,10 +969,11 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
     }
     const bool usable = WHOLE || (!(flags & kOver) && total <= kList);
     const bool rest = !WHOLE && (!usable || (flags & kRest));
-    const bool summed = !WHOLE && sum > 0.0 && fabs(static_cast<double>(ref)) * s.per < kLoose &&
-                        (static_cast<double>(top) - static_cast<double>(ref)) * s.per < 900.0;
+    const bool summed = !WHOLE && sum > 0.0 && (static_cast<double>(top) - static_cast<double>(ref)) * s.per < 900.0;
     // the sum of all weights relative to the row's largest value
-    const double whole = summed ? sum * exp2_of((static_cast<double>(ref) - static_cast<double>(top)) * s.per - rest_of(ref, s.per)) : 0.0;
+    const double sum_per = loose_per(ref, s.per);
+    const double whole =
+        summed ? sum * exp2_of((static_cast<double>(ref) - static_cast<double>(top)) * s.per - rest_of(ref, sum_per)) : 0.0;
     const int finite = usable ? static_cast<int>(total) : 0;  // listed
     const int n = WHOLE ? a.V : finite;                       // entries; -inf among them are below any border
     if (WHOLE) {
@@ -1043,7 +1048,7 @@ __global__ __launch_bounds__(kThreads) void sample_finish_kernel(SampleArgs a) {
         if (short_of) {
             within = true;
         } else if (s.least == 0.0 && summed) {
-            const int token = u >= 0.0 ? token_unfiltered(a, sh, slot, row, c0, c1, own, sum_before, u * sum, ref, s.per) : -1;
+            const int token = u >= 0.0 ? token_unfiltered(a, sh, slot, row, c0, c1, own, sum_before, u * sum, ref, sum_per) : -1;
             done(a, r, no_border(), top, 1.0 / whole, token);
             return;
         } else {
